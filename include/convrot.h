@@ -405,6 +405,107 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
                                  void* stream);
 
 /*
+ * Low-rank adapters beside a projection: the bf16 branch that the model cards
+ * keep next to a quantised layer ("Qwen-Image-Edit-2511 -- W4A8 ConvRot", notes
+ * on LoRA).  A pool of num_adapters adapters of one rank; every row of a batch
+ * names its own, so the tokens of many requests run in one call.
+ *
+ *   adapter  int32 [M] (device): the row's adapter; an index outside
+ *            [0, num_adapters), such as -1, means none.  NULL: every row uses
+ *            adapter 0.  Rows in any order; equal neighbours are cheapest.
+ *   down     bf16 [num_adapters, rank, K], dense (A, row j = rank j)
+ *   up       bf16 [num_adapters, rank, N], dense (U, the transpose of the
+ *            [N, rank] factor: both factors lie along the layer's rows)
+ *   scale    float32 [num_adapters]
+ * An adapter of lower rank is padded with zero rows in both factors.
+ *
+ * cr_lora_forward -- with a = adapter[m]:
+ *   V[m, :] = X[m, :] A[a]^T            (float32 sums; zero for a row without adapter)
+ *   Y[m, :] = bf16_rn( base[m, :] + scale[a] * V[m, :] U[a] )
+ *   X        bf16 [M, K], row stride ldx >= K
+ *   base     bf16 [M, N], row stride ldb >= N (the projection's output), or
+ *            NULL for zero.  base may be Y itself (same pointer and stride);
+ *            any other overlap is an error of the caller.
+ *   Y        out: bf16 [M, N], row stride ldy >= N.  Rows without adapter: base.
+ *   V        out: bf16 [M, rank], dense: V rounded once, for the backward pass;
+ *            NULL if not wanted.  (Y is computed from the float32 V.)
+ * A row's values never enter another row's results: infinities and NaN stay in
+ * their row, and those of an adapter in the rows that name it.
+ *
+ * cr_lora_backward -- gradients of the same map:
+ *   dV[m, :]    = scale[a] * dY[m, :] U[a]^T           (float32 sums)
+ *   dX[m, :]    = bf16_rn( dX_base[m, :] + dV[m, :] A[a] )
+ *   d_down[a]   = bf16_rn( sum over the rows m of a:  dV[m, :]^T X[m, :] )
+ *   d_up[a]     = bf16_rn( scale[a] * sum over the rows m of a:  V[m, :]^T dY[m, :] )
+ *   dY       bf16 [M, N], row stride lddy
+ *   X        bf16 [M, K], row stride ldx, or NULL and
+ *   codes, code_scales  X's 8-bit checkpoint from cr_ckpt_save (K % 256 == 0);
+ *            the product reads the codes themselves, nothing is restored first
+ *   V        bf16 [M, rank] from cr_lora_forward
+ *   dX_base  bf16 [M, K], row stride ldb (the projection's own input gradient,
+ *            e.g. from cr_w4a4_grad_input), NULL for zero; may be dX itself
+ *   dX, d_down, d_up  outputs, each NULL if not wanted; d_down [num_adapters,
+ *            rank, K] and d_up [num_adapters, rank, N], dense, written whole
+ *            (zeros for an adapter without rows).
+ * X / codes are read for d_down only, V for d_up only.  Sums over rows are
+ * taken in an order fixed by the sizes: the same call gives the same bits.
+ *
+ * Both: M >= 0 (forward: nothing happens; backward: the gradients are zero),
+ * N and K in [8, CR_MAX_K] and multiples of 8, rank a multiple of 4 in
+ * [4, CR_MAX_RANK], num_adapters in [1, CR_MAX_ADAPTERS].  Alignment: data
+ * pointers 16 bytes, V 8 bytes, leading dimensions % 8 == 0.
+ * Workspace: of at least the size returned by the matching size call, 256-byte
+ * aligned; none of it needs to be zero before: the call writes its status word
+ * (the first 16 bytes, read with cr_read_device_status) itself.
+ */
+#define CR_MAX_RANK 128
+#define CR_MAX_ADAPTERS 4096
+size_t cr_lora_forward_workspace_size(int M, int N, int K, int rank, int num_adapters);
+size_t cr_lora_backward_workspace_size(int M, int N, int K, int rank, int num_adapters);
+cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, const void* down, const void* up,
+                          const float* scale, const void* base, int64_t ldb, void* Y, int64_t ldy, void* V,
+                          int M, int N, int K, int rank, int num_adapters,
+                          void* workspace, size_t workspace_bytes, void* stream);
+cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* codes,
+                           const float* code_scales, const void* V, const int32_t* adapter, const void* down,
+                           const void* up, const float* scale, const void* dX_base, int64_t ldb,
+                           void* dX, int64_t lddx, void* d_down, void* d_up,
+                           int M, int N, int K, int rank, int num_adapters,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * cr_ckpt_save, cr_ckpt_load -- activations kept in 8 bits for the backward
+ * pass.  For every row and slice of 256 columns:
+ *   y = x H256 (float32),  s = max(amax|y| / 127, 2^-100),  c = round_half_even(y / s)
+ * and back: x^ = bf16_rn( (c s) H256 ).
+ *   X       bf16 [M, K], row stride ldx >= K
+ *   codes   int8 [M, K], dense;  scales  float32 [M, K/256], dense
+ * A slice whose rotation holds an infinity or NaN gets the scale NaN: all its
+ * values come back as NaN.  Half a step of the code is s / 2 in the rotated
+ * values.  cr_lora_backward takes codes and scales in place of X.
+ * Shape rules: M >= 0, K >= 256, K % 256 == 0, K <= CR_MAX_K.  Alignment: X,
+ * codes 16-byte aligned, ldx % 8 == 0.  No workspace.
+ */
+cr_status cr_ckpt_save(const void* X, int M, int K, int64_t ldx, void* codes, float* scales, void* stream);
+cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, void* X, int64_t ldx, void* stream);
+
+/*
+ * cr_w4a4_grad_input -- input gradient of the W4A4 layer with its weights
+ * frozen (the quantisation of X taken as the identity):
+ *   dX = dY W^,   W^[n, :] = bf16_rn( w_scale[n] * (q[n, :] H_group) )
+ * with float32 sums, rounded once to bf16.  The same Wq and w_scale as the
+ * forward calls (either scale mode).
+ *   dY  bf16 [M, N], row stride lddy >= N;  dX  out: bf16 [M, K], row stride lddx >= K
+ * Shape and alignment rules as cr_w4a4_linear, lddy and lddx % 8 == 0,
+ * N <= CR_MAX_K; N == 0 writes zeros.  The workspace holds the bf16 weights
+ * (2 N K bytes) during the call; none of it needs to be zero before.
+ */
+size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group);
+cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const float* w_scale,
+                             void* dX, int64_t lddx, int M, int N, int K, int group,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * cr_selftest_wait_timeout -- diagnostic: enqueue one small kernel that runs the
  * library's bounded device-side wait on a barrier that is never completed.
  * The wait gives up after its limit (about 2 s) and the kernel writes

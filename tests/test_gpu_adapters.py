@@ -1,0 +1,461 @@
+"""Adapters beside a projection, their gradients, 8-bit checkpoints and the input gradient on the GPU,
+against the float64 oracle with its derived bounds."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import adapter_oracle as ao
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def cr():
+    import w4a8_rotated_quantized_b200 as m
+
+    return m
+
+
+def f64(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, std=1.0):
+    return (torch.randn(*shape, device="cuda", generator=g) * std).to(BF)
+
+
+def strided(t, pad):
+    """The same matrix with rows `pad` elements further apart, the gap filled with NaN."""
+    if not pad:
+        return t
+    big = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=t.device)
+    big[:, :t.shape[1]] = t
+    return big[:, :t.shape[1]]
+
+
+def rows_of(mix, M, L, g):
+    if mix == "all":
+        return None
+    if mix == "none":
+        return torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    if mix == "rows":  # any order, some outside the pool on either side
+        return torch.randint(-2, L + 2, (M,), device="cuda", generator=g, dtype=torch.int32)
+    if mix == "last":  # one row only, the last
+        a = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+        a[-1] = L - 1
+        return a
+    # runs: one after the other, padding behind the last
+    cuts = torch.sort(torch.randint(0, M + 1, (L,), device="cuda", generator=g)).values
+    a = torch.searchsorted(cuts, torch.arange(M, device="cuda"), right=True).to(torch.int32)
+    return torch.where(a >= L, torch.full_like(a, -1), a)
+
+
+def make(M, K, N, r, L, mix, seed=0):
+    g = gen(seed)
+    return dict(X=randn(g, M, K), down=randn(g, L, r, K, std=K ** -0.5), up=randn(g, L, r, N, std=0.05),
+                scale=0.25 + torch.rand(L, device="cuda", generator=g), adapter=rows_of(mix, M, L, g),
+                base=randn(g, M, N), dY=randn(g, M, N, std=1e-2), dbase=randn(g, M, K, std=1e-2))
+
+
+def within(got, want, bound, what):
+    got = f64(got).reshape(want.shape)
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    off = np.abs(got - want) - bound
+    assert off.max(initial=-1) <= 0, f"{what}: over its bound by {off.max():.3g} at {np.unravel_index(off.argmax(), off.shape)}"
+
+
+def ids(a):
+    return None if a is None else a.cpu().numpy()
+
+
+SHAPES = [  # M, K, N, rank, adapters, rows
+    (1, 2560, 9728, 16, 1, "all"),
+    (1, 8, 8, 4, 1, "all"),
+    (3, 264, 72, 12, 2, "rows"),
+    (16, 2560, 1000, 8, 5, "rows"),
+    (17, 512, 256, 100, 3, "rows"),
+    (64, 1032, 520, 16, 48, "rows"),
+    (65, 768, 2056, 128, 2, "runs"),
+    (128, 256, 264, 20, 7, "rows"),
+    (129, 512, 256, 64, 2, "last"),
+    (130, 9728, 2560, 32, 3, "runs"),
+    (300, 640, 384, 4, 300, "rows"),
+    (513, 512, 512, 36, 9, "runs"),
+    (777, 512, 256, 8, 5, "runs"),
+    (1100, 3072, 1544, 64, 1, "all"),
+    (2049, 1280, 776, 128, 4, "runs"),
+    (200, 256, 256, 16, 3, "none"),
+    (40, 256, 256, 32, 20, "none"),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape):
+    d = make(*shape, seed=1)
+    want, v, ey, ev = ao.lora_forward(f64(d["X"]), f64(d["down"]), f64(d["up"]), f64(d["scale"]), ids(d["adapter"]),
+                                      f64(d["base"]))
+    Y, V = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=d["base"],
+                                save_v=True)
+    within(Y, want, ey, "Y")
+    within(V, v, ev, "V")
+    Y2 = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=d["base"])
+    assert torch.equal(Y.view(torch.int16), Y2.view(torch.int16))
+
+
+@pytest.mark.parametrize("shape", [(5, 264, 136, 8, 2, "rows"), (150, 520, 264, 24, 3, "runs"), (1, 256, 64, 4, 1, "all")],
+                         ids=str)
+def test_forward_strides_no_base_and_in_place(shape):
+    d = make(*shape, seed=2)
+    X = strided(d["X"], 24)
+    args = (d["down"], d["up"], d["scale"])
+    plain = cr().cr_lora_forward(d["X"], *args, adapter=d["adapter"], base=d["base"])
+    big = strided(d["base"].clone(), 40)
+    whole = big._base if big._base is not None else big
+    gap = whole[:, d["base"].shape[1]:].clone()
+    got = cr().cr_lora_forward(X, *args, adapter=d["adapter"], base=big, out=big)
+    assert got is big and torch.equal(got, plain)
+    assert torch.equal(whole[:, d["base"].shape[1]:].view(torch.int16), gap.view(torch.int16))  # between the rows: untouched
+    want, _, ey, _ = ao.lora_forward(f64(d["X"]), *(f64(t) for t in args), ids(d["adapter"]))
+    within(cr().cr_lora_forward(X, *args, adapter=d["adapter"]), want, ey, "Y without base")
+
+
+@pytest.mark.parametrize("M", [24, 200, 600])
+def test_values_stay_in_their_rows(M):
+    """NaN and infinities in one row, in one adapter or in rows without adapter change nothing else."""
+    d = make(M, 512, 264, 16, 4, "rows", seed=3)
+    a = d["adapter"]
+    a[:5] = torch.tensor([0, 1, 2, 3, -1], device="cuda")
+    args = dict(adapter=a, base=d["base"])
+    Y0, V0 = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], save_v=True, **args)
+    X, down, up = d["X"].clone(), d["down"].clone(), d["up"].clone()
+    X[1, 7], X[4, :] = float("inf"), float("nan")
+    down[2, 3, 5], up[2, 1, :] = float("nan"), float("inf")
+    Y, V = cr().cr_lora_forward(X, down, up, d["scale"], save_v=True, **args)
+    ok = (a != 2)
+    ok[1] = False
+    assert torch.equal(Y[ok].view(torch.int16), Y0[ok].view(torch.int16))
+    assert torch.equal(V[ok].view(torch.int16), V0[ok].view(torch.int16))
+    assert not torch.isfinite(Y[1]).any() and not torch.isfinite(Y[a == 2]).any()
+    # gradients: rows without adapter, and adapter 2's rows, hold NaN; the others' gradients are as before
+    none = ~((a >= 0) & (a < 4))
+    dY = d["dY"]
+    g0 = cr().cr_lora_backward(dY, d["X"], V0, d["down"], d["up"], d["scale"], adapter=a, base=d["dbase"])
+    c0 = cr().cr_ckpt_save(d["X"])
+    h0 = cr().cr_lora_backward(dY, c0, V0, d["down"], d["up"], d["scale"], adapter=a, base=d["dbase"])
+    bad = none | (a == 2)
+    Xb, dYb, Vb = d["X"].clone(), dY.clone(), V0.clone()
+    Xb[bad], dYb[bad], Vb[bad] = float("nan"), float("inf"), float("nan")
+    cb = cr().cr_ckpt_save(Xb)
+    assert torch.isnan(cb[1][bad]).all() and torch.isfinite(cb[1][~bad]).all()
+    for kept, ref in ((Xb, g0), (cb, h0)):
+        dX, dd, du = cr().cr_lora_backward(dYb, kept, Vb, d["down"], d["up"], d["scale"], adapter=a, base=d["dbase"])
+        assert torch.equal(dX[~bad].view(torch.int16), ref[0][~bad].view(torch.int16))
+        assert torch.equal(dX[none].view(torch.int16), d["dbase"][none].view(torch.int16))
+        for x, y in ((dd, ref[1]), (du, ref[2])):
+            assert torch.equal(x[[0, 1, 3]].view(torch.int16), y[[0, 1, 3]].view(torch.int16))
+        assert not torch.isfinite(dd[2]).all() and not torch.isfinite(du[2]).all()
+
+
+@pytest.mark.parametrize("kept", ["bf16", "int8"])
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] != 1] + [(1, 512, 256, 16, 1, "all"), (5000, 256, 264, 8, 3, "runs")],
+                         ids=str)
+def test_backward(shape, kept):
+    M, K, N, r, L, mix = shape
+    if kept == "int8":
+        K = max(256, K // 256 * 256)
+    d = make(M, K, N, r, L, mix, seed=4)
+    _, V = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], save_v=True)
+    if kept == "int8":
+        keep = cr().cr_ckpt_save(d["X"])
+        x, mags = ao.ckpt_values(keep[0].cpu().numpy(), keep[1].cpu().numpy())
+    else:
+        keep, x, mags = d["X"], f64(d["X"]), None
+    want, bound = ao.lora_backward(f64(d["dY"]), x, f64(V), f64(d["down"]), f64(d["up"]), f64(d["scale"]),
+                                   ids(d["adapter"]), f64(d["dbase"]), mags)
+    args = (d["dY"], keep, V, d["down"], d["up"], d["scale"])
+    got = cr().cr_lora_backward(*args, adapter=d["adapter"], base=d["dbase"])
+    for g, w, b, name in zip(got, want, bound, ("dX", "d_down", "d_up")):
+        within(g, w, b, name)
+    again = cr().cr_lora_backward(*args, adapter=d["adapter"], base=d["dbase"])
+    for x1, x2 in zip(got, again):
+        assert torch.equal(x1.view(torch.int16), x2.view(torch.int16))
+
+
+def test_backward_parts_strides_and_in_place():
+    d = make(333, 512, 264, 24, 3, "runs", seed=5)
+    _, V = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], save_v=True)
+    tail = (d["down"], d["up"], d["scale"])
+    want = cr().cr_lora_backward(d["dY"], d["X"], V, *tail, adapter=d["adapter"], base=d["dbase"])
+    base = strided(d["dbase"].clone(), 8)
+    got = cr().cr_lora_backward(strided(d["dY"], 16), strided(d["X"], 24), V, *tail, adapter=d["adapter"], base=base,
+                                out=base)
+    assert got[0] is base
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    dx, dd, du = cr().cr_lora_backward(d["dY"], None, None, *tail, adapter=d["adapter"], base=d["dbase"],
+                                       need_down=False, need_up=False)
+    assert dd is None and du is None and torch.equal(dx, want[0])
+    dx, dd, du = cr().cr_lora_backward(d["dY"], d["X"], None, *tail, adapter=d["adapter"], need_dx=False, need_up=False)
+    assert dx is None and du is None and torch.equal(dd, want[1])
+    dx, dd, du = cr().cr_lora_backward(d["dY"], None, V, *tail, adapter=d["adapter"], need_dx=False, need_down=False)
+    assert dx is None and dd is None and torch.equal(du, want[2])
+
+
+def test_no_rows():
+    d = make(0, 512, 264, 8, 2, "all", seed=6)
+    Y, V = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], base=d["base"], save_v=True)
+    assert Y.shape == (0, 264) and V.shape == (0, 8)
+    dX, dd, du = cr().cr_lora_backward(d["dY"], d["X"], V, d["down"], d["up"], d["scale"])
+    assert dX.shape == (0, 512) and not dd.any() and not du.any()
+    c, s = cr().cr_ckpt_save(d["X"])
+    assert cr().cr_ckpt_load(c, s).shape == (0, 512)
+
+
+@pytest.mark.parametrize("which", ["X", "down", "up"])
+def test_gradients_against_differences(which):
+    """The output is linear in each of X, down and up, so a difference over a whole step is exact up to the
+    outputs' rounding: <dY, Y(t + d) - Y(t)> = <grad, d>, off by at most 2^-8 sum |dY| (|Y(t + d)| + |Y(t)|)
+    and the gradient's own rounding, 2^-8 sum |grad d|."""
+    d = make(96, 256, 128, 8, 2, "rows", seed=7)
+    d["up"] *= 4
+    kw = dict(adapter=d["adapter"])
+    Y, V = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], save_v=True, **kw)
+    dY = (Y.float() * 0.01).to(BF)  # a loss that pulls the output to zero
+    grads = dict(zip(("X", "down", "up"), cr().cr_lora_backward(dY, d["X"], V, d["down"], d["up"], d["scale"], **kw)))
+    step = grads[which].float()
+    step = (step * (f64(d[which]).std() / f64(grads[which]).std())).to(BF)
+    moved = dict(d)
+    moved[which] = (d[which].float() + step.float()).to(BF)
+    step = f64(moved[which]) - f64(d[which])
+    Y2 = cr().cr_lora_forward(moved["X"], moved["down"], moved["up"], moved["scale"], **kw)
+    diff = (f64(dY) * (f64(Y2) - f64(Y))).sum()
+    along = (f64(grads[which]) * step).sum()
+    # float32 sums add less than one more rounding of the outputs: twice the bound covers both
+    tol = 2 * (ao.BF16 * (np.abs(f64(dY)) * (np.abs(f64(Y2)) + np.abs(f64(Y)))).sum()
+               + ao.BF16 * np.abs(f64(grads[which]) * step).sum())
+    assert along > 4 * tol  # the comparison says something
+    assert abs(diff - along) <= tol
+
+
+# ---------------------------------------------------------------------------------------------- checkpoints
+
+def loud(g, M, K):
+    x = torch.randn(M, K, device="cuda", generator=g)
+    x[:, torch.rand(K, device="cuda", generator=g) < 0.02] *= 50
+    return x.to(BF)
+
+
+@pytest.mark.parametrize("M,K,pad", [(1, 256, 0), (7, 256, 8), (21, 2560, 0), (33, 768, 264), (130, 9728, 0), (1000, 1024, 0)])
+def test_checkpoint(M, K, pad):
+    x = loud(gen(M), M, K)
+    codes, scales = cr().cr_ckpt_save(strided(x, pad))
+    want, s, t = ao.ckpt_save(f64(x))
+    got_s = scales.cpu().numpy()
+    # 12 float32 roundings on the way through the transform, each at most 2^-24 of the slice's sum of magnitudes / 16
+    err = 12 * 2.0 ** -24 * np.abs(f64(x)).reshape(M, -1, 256).sum(-1) / 16
+    assert (np.abs(got_s.astype(np.float64) - s) <= err / 127 + 2.0 ** -24 * s).all()
+    c = codes.cpu().numpy().astype(np.int32)
+    # a code may differ where y / s lies as near to a border as those roundings (and the scale's own) reach
+    reach = np.repeat((2 * err / s + 127 * 2.0 ** -23), 256, axis=1).reshape(M, K)
+    flips = c != want
+    assert (np.abs(c - want) <= 1).all() and (np.abs(np.abs(t - np.floor(t)) - 0.5) <= reach)[flips].all()
+    assert np.abs(c).max() <= 127
+    # what the codes stand for: one float32 product and one rounding
+    back, mags = ao.ckpt_values(codes.cpu().numpy(), got_s)
+    out = torch.full((M, K + pad), float("nan"), dtype=BF, device="cuda")
+    r = cr().cr_ckpt_load(codes, scales, out=out[:, :K])
+    within(r, back, ao.BF16 * np.abs(back) + 2.0 ** -23 * np.abs(back) + 1e-300 * mags, "restored")
+    assert torch.isnan(out[:, K:]).all()
+    # half a step in every rotated value: at most sqrt(256) s / 2 = 8 s over a slice's norm
+    d = (f64(r) - f64(x)).reshape(M, -1, 256)
+    room = 8 * got_s + ao.BF16 * np.linalg.norm(back.reshape(M, -1, 256), axis=-1) + 16 * err
+    assert (np.linalg.norm(d, axis=-1) <= room * (1 + 1e-6)).all()
+
+
+def test_checkpoint_extremes():
+    x = torch.zeros(6, 512, dtype=BF, device="cuda")
+    x[1, 3] = 1e-38  # scale at its floor: comes back as zero
+    x[2, 300] = float("inf")
+    x[3, 7] = float("nan")
+    x[4] = 3e38  # the rotation leaves float32
+    x[5, :256] = 2.0 ** 100
+    c, s = cr().cr_ckpt_save(x)
+    r = cr().cr_ckpt_load(c, s)
+    assert not r[:2].any() and not c[:2].any()
+    assert torch.isnan(r[2, 256:]).all() and not r[2, :256].any() and not c[2].any()
+    assert torch.isnan(r[3, :256]).all() and not r[3, 256:].any()
+    assert torch.isnan(r[4]).all()
+    assert torch.isfinite(r[5]).all() and float((r[5, :256].double() / 2.0 ** 100 - 1).abs().max()) <= 2.0 ** -7 + 8 / 127
+
+
+def test_checkpoint_past_32_bit_offsets():
+    M, K = 40000, 65536  # 2.6e9 values
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    x[-1] = loud(gen(1), 1, K)[0]
+    c, s = cr().cr_ckpt_save(x)
+    assert not c[:-1].any()
+    c1, s1 = cr().cr_ckpt_save(x[-1:].contiguous())
+    assert torch.equal(c[-1:], c1) and torch.equal(s[-1:], s1)
+    x.fill_(1)
+    r = cr().cr_ckpt_load(c, s, out=x)
+    assert not r[:-1].any() and torch.equal(r[-1:], cr().cr_ckpt_load(c1, s1))
+
+
+# ---------------------------------------------------------------------------------------------- input gradient
+
+@pytest.mark.parametrize("M,K,N,group,mode", [
+    (1, 256, 8, 256, "tensor"), (1, 2560, 9728, 256, "row"), (21, 1024, 136, 1024, "row"), (130, 512, 256, 16, "tensor"),
+    (129, 768, 264, 64, "row"), (257, 1280, 1000, 256, "tensor"), (300, 9728, 2560, 256, "row"), (1030, 3072, 1544, 256, "tensor"),
+    (5, 4096, 72, 1024, "tensor")])
+def test_grad_input(M, K, N, group, mode):
+    g = gen(M + N)
+    W = randn(g, N, K, std=0.02)
+    Wq, s = cr().cr_pack_weight(W, group=group, scale_mode=mode)
+    dY = randn(g, M, N, std=1e-3)
+    want, bound = ao.grad_input(f64(dY), Wq.cpu().numpy(), s.cpu().numpy(), group)
+    within(cr().cr_w4a4_grad_input(dY, Wq, s, group=group), want, bound, "dX")
+    out = torch.full((M, K + 8), float("nan"), dtype=BF, device="cuda")
+    within(cr().cr_w4a4_grad_input(strided(dY, 32), Wq, s, group=group, out=out[:, :K]), want, bound, "dX, strided")
+    assert torch.isnan(out[:, K:]).all()
+
+
+def test_grad_input_empty():
+    dY = torch.zeros(4, 0, dtype=BF, device="cuda")
+    Wq, s = torch.zeros(0, 128, dtype=torch.uint8, device="cuda"), torch.zeros(0, device="cuda")
+    assert not cr().cr_w4a4_grad_input(dY, Wq, s).any()
+    dY = torch.zeros(0, 8, dtype=BF, device="cuda")
+    Wq, s = torch.zeros(8, 128, dtype=torch.uint8, device="cuda"), torch.zeros(8, device="cuda")
+    assert cr().cr_w4a4_grad_input(dY, Wq, s).shape == (0, 256)
+
+
+def test_grad_input_keeps_non_finite_rows_apart():
+    g = gen(9)
+    Wq, s = cr().cr_pack_weight(randn(g, 264, 512))
+    dY = randn(g, 200, 264)
+    want = cr().cr_w4a4_grad_input(dY, Wq, s)
+    dY[77, 5] = float("nan")
+    got = cr().cr_w4a4_grad_input(dY, Wq, s)
+    ok = torch.arange(200, device="cuda") != 77
+    assert torch.equal(got[ok], want[ok]) and torch.isnan(got[77]).all()
+
+
+# ---------------------------------------------------------------------------------------------- together
+
+def step(d, Wq, s_w):
+    """One training step's calls around a frozen packed layer with adapters, as a user makes them."""
+    m = cr()
+    kept = m.cr_ckpt_save(d["X"])
+    y0 = m.cr_w4a4_linear(d["X"], Wq, s_w)
+    Y, V = m.cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=y0, out=y0, save_v=True)
+    dx0 = m.cr_w4a4_grad_input(d["dY"], Wq, s_w)
+    dX, dd, du = m.cr_lora_backward(d["dY"], kept, V, d["down"], d["up"], d["scale"], adapter=d["adapter"], base=dx0,
+                                    out=dx0)
+    return Y, dX, dd, du
+
+
+@pytest.mark.parametrize("M,mix", [(40, "rows"), (700, "runs")])
+def test_training_step(M, mix):
+    d = make(M, 512, 768, 16, 3, mix, seed=11)
+    Wq, s_w = cr().cr_pack_weight(randn(gen(12), 768, 512, std=0.02))
+    Y, dX, dd, du = step(d, Wq, s_w)
+    torch.cuda.synchronize()
+    down, up, sc, a = f64(d["down"]), f64(d["up"]), f64(d["scale"]), ids(d["adapter"])
+    y0 = f64(cr().cr_w4a4_linear(d["X"], Wq, s_w))
+    want, v, ey, _ = ao.lora_forward(f64(d["X"]), down, up, sc, a, y0)
+    within(Y, want, ey, "Y")
+    dx0, e0 = ao.grad_input(f64(d["dY"]), Wq.cpu().numpy(), s_w.cpu().numpy())
+    codes, scales = cr().cr_ckpt_save(d["X"])
+    x, mags = ao.ckpt_values(codes.cpu().numpy(), scales.cpu().numpy())
+    V = torch.from_numpy(v).to(BF).double().numpy()  # may differ by a step from the kernel's
+    (wx, wd, wu), (ex, ed, eu) = ao.lora_backward(f64(d["dY"]), x, V, down, up, sc, a, dx0, mags)
+    within(dX, wx, ex + e0 * (1 + ao.BF16), "dX")
+    within(dd, wd, ed, "d_down")
+    extra = np.stack([sc[k] * 2 * ao.BF16 * (np.abs(v[r]).T @ np.abs(f64(d["dY"])[r])) for k, r in ao.row_masks(a, M, 3)])
+    within(du, wu, eu + extra, "d_up")
+
+
+def test_other_stream_and_captured_graphs():
+    """Two captured steps of different sizes replayed in turn and together with eager calls on another
+    stream: every result as the eager call's."""
+    Wq, s_w = cr().cr_pack_weight(randn(gen(12), 768, 512, std=0.02))
+    sets = [make(700, 512, 768, 16, 3, "runs", seed=21), make(60, 512, 768, 64, 5, "rows", seed=22)]
+    want = [[t.clone() for t in step(d, Wq, s_w)] for d in sets]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for d in sets:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(d, Wq, s_w)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(d, Wq, s_w))
+        graphs.append(g)
+    for o in outs:
+        for t in o:
+            t.fill_(float("nan"))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+        with torch.cuda.stream(other):
+            eager = cr().cr_lora_forward(sets[0]["X"], sets[0]["down"], sets[0]["up"], sets[0]["scale"],
+                                         adapter=sets[0]["adapter"])
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            for x, y in zip(o, w):
+                assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    ref = cr().cr_lora_forward(sets[0]["X"], sets[0]["down"], sets[0]["up"], sets[0]["scale"], adapter=sets[0]["adapter"])
+    assert torch.equal(eager, ref)
+
+
+def test_own_workspace_and_status():
+    d = make(300, 512, 264, 16, 2, "runs", seed=31)
+    from w4a8_rotated_quantized_b200 import binding
+
+    n = binding._lib.cr_lora_forward_workspace_size(300, 264, 512, 16, 2)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # nothing needs to be zero before
+    want = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"])
+    got = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], workspace=ws)
+    assert torch.equal(got, want) and cr().cr_read_device_status(ws=ws) == 0
+    with pytest.raises(cr().ConvRotError):
+        cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], workspace=ws[:256])
+
+
+def test_refusals():
+    m = cr()
+    d = make(8, 512, 264, 8, 2, "rows", seed=41)
+    ok = (d["X"], d["down"], d["up"], d["scale"])
+    with pytest.raises(TypeError):
+        m.cr_lora_forward(d["X"].float(), *ok[1:])
+    with pytest.raises(ValueError):
+        m.cr_lora_forward(d["X"][:, :256], *ok[1:])  # K disagrees with down
+    with pytest.raises(TypeError):
+        m.cr_lora_forward(*ok, adapter=d["adapter"].long())
+    with pytest.raises(ValueError):
+        m.cr_lora_forward(*ok, adapter=d["adapter"][:-1])
+    with pytest.raises(ValueError):
+        m.cr_lora_forward(*ok, base=d["base"][:4])
+    with pytest.raises(m.ConvRotError):
+        m.cr_lora_forward(*ok, base=d["base"][:1].expand(8, 264))  # rows that lie on one another
+    with pytest.raises(m.ConvRotError):
+        m.cr_lora_forward(d["X"], d["down"][:, :6].contiguous(), d["up"][:, :6].contiguous(), d["scale"])  # rank % 4
+    with pytest.raises(ValueError):
+        m.cr_lora_backward(d["dY"], None, None, *ok[1:], need_up=False)
+    with pytest.raises(ValueError):
+        m.cr_lora_backward(d["dY"], (torch.zeros(8, 512, dtype=torch.int8, device="cuda"), torch.zeros(8, 1, device="cuda")),
+                           None, *ok[1:], need_up=False)
+    with pytest.raises(m.ConvRotError):
+        m.cr_ckpt_save(d["X"][:, :264].contiguous())  # K % 256
+    with pytest.raises(m.ConvRotError):
+        m.cr_w4a4_grad_input(d["base"], torch.zeros(264, 256, dtype=torch.uint8, device="cuda"),
+                             torch.ones(264, device="cuda"), group=32)

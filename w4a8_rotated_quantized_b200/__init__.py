@@ -9,7 +9,9 @@ INT8 / any-format calls ``cr_pack_weight_ex``, ``cr_rotate_quant_act_ex``,
 ``cr_pack_weight_w4a8``, ``cr_w4a8_gemm``, ``cr_w4a8_gemm_f32``, ``cr_w4a8_linear``,
 and the INT8-activation branch of the W4A4 weights ``cr_a8w4_gemm``, ``cr_a8w4_gemm_s32``,
 ``cr_a8w4_linear``, and shared activation quantisation for several projections
-``cr_w4a4_gemm_multi``, ``cr_w4a4_gemm_multi_s32``, ``cr_w4a4_linear_multi``.  They are loaded lazily from
+``cr_w4a4_gemm_multi``, ``cr_w4a4_gemm_multi_s32``, ``cr_w4a4_linear_multi``, and low-rank adapters beside a
+projection and what training them takes, ``cr_lora_forward``, ``cr_lora_backward``, ``cr_ckpt_save``,
+``cr_ckpt_load``, ``cr_w4a4_grad_input``.  They are loaded lazily from
 the in-tree CUDA library, so that ``workloads`` and ``build`` can be imported
 on a machine where the library is not built yet; touching any of them without
 the library raises ImportError.  There is no CPU fallback.
@@ -21,6 +23,7 @@ _BINDING_NAMES = {
     "cr_pack_weight_w4a8", "cr_w4a8_gemm", "cr_w4a8_gemm_f32", "cr_w4a8_linear",
     "cr_a8w4_gemm", "cr_a8w4_gemm_s32", "cr_a8w4_linear", "cr_selftest_wait_timeout", "cr_selftest_act_fallback",
     "cr_w4a4_gemm_multi", "cr_w4a4_gemm_multi_s32", "cr_w4a4_linear_multi",
+    "cr_lora_forward", "cr_lora_backward", "cr_ckpt_save", "cr_ckpt_load", "cr_w4a4_grad_input",
     "cr_status_string", "cr_api_version", "ConvRotError", "workspace", "LIB_PATH",
     "LINEAR_AUTO", "LINEAR_ONE_LAUNCH", "LINEAR_TWO_LAUNCHES",
 }

@@ -69,8 +69,20 @@ _SIGS = {
     "cr_w4a4_gemm_multi": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "cr_w4a4_gemm_multi_s32": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "cr_w4a4_linear_multi": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "cr_lora_forward_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "cr_lora_backward_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "cr_lora_forward": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i, _i, _i, _i, _i, _vp, _sz,
+                             _vp]),
+    "cr_lora_backward": (_i, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                              _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "cr_ckpt_save": (_i, [_vp, _i, _i, _i64, _vp, _vp, _vp]),
+    "cr_ckpt_load": (_i, [_vp, _vp, _i, _i, _vp, _i64, _vp]),
+    "cr_w4a4_grad_input_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "cr_w4a4_grad_input": (_i, [_vp, _i64, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _sz, _vp]),
 }
 CR_MAX_PROJ = 4
+CR_MAX_RANK = 128
+CR_MAX_ADAPTERS = 4096
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
     _f.restype = _res
@@ -289,10 +301,14 @@ def cr_w4a4_linear(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, bia
     return out
 
 
-def cr_read_device_status(device: Optional[torch.device] = None) -> int:
-    """Device status word of this device's shared workspace (synchronises the current stream)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    ws = workspace(device, 256)
+def cr_read_device_status(device: Optional[torch.device] = None, ws: Optional[torch.Tensor] = None) -> int:
+    """Device status word of this device's shared workspace, or of the workspace ``ws`` that a call was
+    given (synchronises the current stream)."""
+    if ws is not None:
+        device = ws.device
+    else:
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        ws = workspace(device, 256)
     st = ctypes.c_int(0)
     _check("cr_read_device_status", _lib.cr_read_device_status(_ptr(ws), ctypes.byref(st), _stream(device)))
     return st.value
@@ -647,3 +663,208 @@ def cr_a8w4_linear(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, bia
 def cr_selftest_wait_timeout(ws: torch.Tensor) -> None:
     """Enqueue the bounded-wait self-test on ``ws`` (a zeroed uint8 CUDA workspace of >= 256 bytes)."""
     _check("cr_selftest_wait_timeout", _lib.cr_selftest_wait_timeout(_ptr(ws), ws.numel(), _stream(ws.device)))
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters beside a projection, 8-bit activation checkpoints, and the packed layer's input
+# gradient.  Their scratch is a buffer of its own for each call, taken from torch's allocator on the
+# current stream (inside a graph capture: from the graph's pool), so calls on several streams and
+# captured graphs share nothing.  A caller's ``workspace`` takes its place; its status word can then be
+# read with ``cr_read_device_status(ws=...)``.
+# ---------------------------------------------------------------------------
+
+class _on:
+    """Makes ``device`` current for the library call where it is not already."""
+
+    def __init__(self, device: torch.device):
+        self.to = device.index
+        self.back = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.to:
+            torch.cuda.set_device(self.to)
+            self.back = now
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _scratch(given: Optional[torch.Tensor], nbytes: int, device: torch.device) -> torch.Tensor:
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _dev(given, "workspace", torch.uint8, device)
+    if given.dim() != 1 or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous 1-D uint8 tensor")
+    return given
+
+
+def _matrix(t: torch.Tensor, name: str, device: torch.device, M: int, C: int) -> int:
+    """A bf16 [M, C] matrix with dense columns; returns its row stride."""
+    _dev(t, name, torch.bfloat16, device)
+    if tuple(t.shape) != (M, C):
+        raise ValueError(f"{name} must have shape {(M, C)}, got {tuple(t.shape)}")
+    if M <= 1 or C == 0:  # the stride of a single row or of an empty tensor says nothing
+        if M == 1 and C > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit stride along the last dimension")
+        return C
+    return _rows(t, name)[2]
+
+
+def _out_matrix(out: Optional[torch.Tensor], name: str, device: torch.device, M: int, C: int) -> Tuple[torch.Tensor, int]:
+    if out is None:
+        return torch.empty((M, C), dtype=torch.bfloat16, device=device), C
+    return out, _matrix(out, name, device, M, C)
+
+
+def _adapters(adapter: Optional[torch.Tensor], down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor, M: int,
+              N: Optional[int], K: Optional[int], device: torch.device) -> Tuple[int, int, int, int]:
+    """The pool's factors down [L, r, K] and up [L, r, N], its scales [L] and the rows' adapters [M]."""
+    for t, name in ((down, "down"), (up, "up")):
+        _dev(t, name, torch.bfloat16, device)
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be 3-D [adapters, rank, columns]")
+    L, r = down.shape[0], down.shape[1]
+    K = down.shape[2] if K is None else K
+    N = up.shape[2] if N is None else N
+    _dense(down, "down", torch.bfloat16, device, (L, r, K))
+    _dense(up, "up", torch.bfloat16, device, (L, r, N))
+    _vec(scale, "scale", torch.float32, device, L)
+    if adapter is not None:
+        _vec(adapter, "adapter", torch.int32, device, M)
+    return L, r, N, K
+
+
+def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
+                    adapter: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, save_v: bool = False,
+                    workspace: Optional[torch.Tensor] = None):
+    """Y bf16 [M, N] = base + scale[a] * (X down[a]^T) up[a], a = adapter[m] (int32 [M]; outside the pool: Y = base).
+
+    X bf16 [M, K]; down bf16 [L, r, K]; up bf16 [L, r, N]; scale float32 [L].  Without ``adapter`` every
+    row uses adapter 0; without ``base`` the sum starts at zero.  ``out`` may be ``base`` itself.  With
+    ``save_v`` returns (Y, V), V bf16 [M, r] = X down[a]^T for the backward pass.
+    """
+    _bf16_cuda(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D [M, K]")
+    dev = X.device
+    M, K = X.shape
+    ldx = _matrix(X, "X", dev, M, K)
+    L, r, N, _ = _adapters(adapter, down, up, scale, M, None, K, dev)
+    ldb = 0 if base is None else _matrix(base, "base", dev, M, N)
+    with _on(dev):
+        Y, ldy = _out_matrix(out, "out", dev, M, N)
+        V = torch.empty((M, r), dtype=torch.bfloat16, device=dev) if save_v else None
+        ws = _scratch(workspace, _lib.cr_lora_forward_workspace_size(M, N, K, r, L), dev)
+        _check("cr_lora_forward", _lib.cr_lora_forward(
+            X.data_ptr(), ldx, _addr(adapter), down.data_ptr(), up.data_ptr(), scale.data_ptr(), _addr(base), ldb,
+            Y.data_ptr(), ldy, _addr(V), M, N, K, r, L, ws.data_ptr(), ws.numel(), _stream(dev)))
+    return (Y, V) if save_v else Y
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch.Tensor, up: torch.Tensor,
+                     scale: torch.Tensor, adapter: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, need_dx: bool = True, need_down: bool = True,
+                     need_up: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`cr_lora_forward`: (dX bf16 [M, K], d_down as down, d_up as up), None where not needed.
+
+    ``X`` is the forward's input, or ``(codes, scales)`` of :func:`cr_ckpt_save` (None if d_down is not
+    needed); ``V`` is what the forward kept (None if d_up is not needed).  dX starts at ``base`` (the
+    projection's own input gradient; zero without it); ``out`` takes dX and may be ``base`` itself.
+    """
+    _bf16_cuda(dY, "dY")
+    if dY.dim() != 2:
+        raise ValueError("dY must be 2-D [M, N]")
+    dev = dY.device
+    M, N = dY.shape
+    lddy = _matrix(dY, "dY", dev, M, N)
+    L, r, _, K = _adapters(adapter, down, up, scale, M, N, None, dev)
+    if need_down and X is None:
+        raise ValueError("X (or its checkpoint) is needed for d_down")
+    if need_up and V is None:
+        raise ValueError("V is needed for d_up")
+    x = codes = code_scales = None
+    ldx = 0
+    if isinstance(X, (tuple, list)):
+        if len(X) != 2:
+            raise ValueError("a checkpoint is (codes, scales)")
+        codes, code_scales = X
+        _dense(codes, "codes", torch.int8, dev, (M, K))
+        _dense(code_scales, "scales", torch.float32, dev, (M, K // 256))
+    elif X is not None:
+        x, ldx = X, _matrix(X, "X", dev, M, K)
+    if V is not None:
+        _dense(V, "V", torch.bfloat16, dev, (M, r))
+    ldb = 0 if base is None else _matrix(base, "base", dev, M, K)
+    if out is not None and not need_dx:
+        raise ValueError("out takes dX, which is not needed")
+    with _on(dev):
+        dX, lddx = _out_matrix(out, "out", dev, M, K) if need_dx else (None, 0)
+        dd = torch.empty_like(down) if need_down else None
+        du = torch.empty_like(up) if need_up else None
+        ws = _scratch(workspace, _lib.cr_lora_backward_workspace_size(M, N, K, r, L), dev)
+        _check("cr_lora_backward", _lib.cr_lora_backward(
+            dY.data_ptr(), lddy, _addr(x), ldx, _addr(codes), _addr(code_scales), _addr(V), _addr(adapter),
+            down.data_ptr(), up.data_ptr(), scale.data_ptr(), _addr(base), ldb, _addr(dX), lddx, _addr(dd), _addr(du),
+            M, N, K, r, L, ws.data_ptr(), ws.numel(), _stream(dev)))
+    return dX, dd, du
+
+
+def cr_ckpt_save(X: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """X bf16 [M, K] in 8 bits: (codes int8 [M, K] of the rotated rows, scales float32 [M, K/256])."""
+    _bf16_cuda(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D [M, K]")
+    dev = X.device
+    M, K = X.shape
+    ldx = _matrix(X, "X", dev, M, K)
+    with _on(dev):
+        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
+        scales = torch.empty((M, K // 256), dtype=torch.float32, device=dev)
+        _check("cr_ckpt_save", _lib.cr_ckpt_save(X.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr(),
+                                                 _stream(dev)))
+    return codes, scales
+
+
+def cr_ckpt_load(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bf16 [M, K] values that a checkpoint of :func:`cr_ckpt_save` stands for."""
+    M, K = _codes(codes, "codes", torch.int8)
+    _cuda(codes, "codes")
+    dev = codes.device
+    _dense(scales, "scales", torch.float32, dev, (M, K // 256))
+    with _on(dev):
+        X, ldx = _out_matrix(out, "out", dev, M, K)
+        _check("cr_ckpt_load", _lib.cr_ckpt_load(codes.data_ptr(), scales.data_ptr(), M, K, X.data_ptr(), ldx,
+                                                 _stream(dev)))
+    return X
+
+
+def cr_w4a4_grad_input(dY: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, group: int = GROUP,
+                       out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Input gradient of the W4A4 layer with frozen weights: dX bf16 [M, K] = dY [M, N] . (w_scale * Wq H_group)."""
+    _bf16_cuda(dY, "dY")
+    if dY.dim() != 2:
+        raise ValueError("dY must be 2-D [M, N]")
+    dev = dY.device
+    M, N = dY.shape
+    lddy = _matrix(dY, "dY", dev, M, N)
+    _dev(Wq, "Wq", torch.uint8, dev)
+    if Wq.dim() != 2:
+        raise ValueError("Wq must be 2-D [N, K/2]")
+    K = 2 * Wq.shape[1]
+    _dense(Wq, "Wq", torch.uint8, dev, (N, K // 2))
+    _vec(w_scale, "w_scale", torch.float32, dev, N)
+    with _on(dev):
+        dX, lddx = _out_matrix(out, "out", dev, M, K)
+        ws = _scratch(workspace, _lib.cr_w4a4_grad_input_workspace_size(M, N, K, group), dev)
+        _check("cr_w4a4_grad_input", _lib.cr_w4a4_grad_input(
+            dY.data_ptr(), lddy, Wq.data_ptr(), w_scale.data_ptr(), dX.data_ptr(), lddx, M, N, K, group, ws.data_ptr(),
+            ws.numel(), _stream(dev)))
+    return dX

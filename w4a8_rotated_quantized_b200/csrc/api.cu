@@ -75,6 +75,8 @@ inline int* ws_status(void* workspace) {
 
 }  // namespace
 
+int cr::check_current_device(int* num_sms) { return check_device(num_sms); }
+
 extern "C" {
 
 const char* cr_status_string(int status) {

@@ -1,0 +1,214 @@
+// api_adapters.cu -- the extern "C" entry points for low-rank adapters beside a projection (forward and
+// backward), the 8-bit activation checkpoints and the packed layer's input gradient: argument validation
+// on the host, device check, workspace carving and launches on the caller's stream.
+//
+// The adapters are the bf16 branch that the model cards keep beside a quantised layer ("Qwen-Image-Edit-
+// 2511 -- W4A8 ConvRot", notes on LoRA: merged by requantising the weight, or kept as a branch of its own).
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/convrot.h"
+#include "cr_internal.h"
+
+namespace {
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline cr_status cuda_status(cudaError_t e) { return e == cudaSuccess ? CR_OK : CR_ERR_CUDA; }
+
+inline int* ws_status(void* workspace) {
+  return reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + cr::kWsStatusOff);
+}
+
+// Workspace of the adapter calls: the status word's 256 bytes, then the parts below, each on 256 bytes.
+constexpr size_t kWsHead = 256;
+
+inline size_t bytes_f32(int64_t n) { return cr::round_up(static_cast<size_t>(n) * 4, 256); }
+
+// Sizes are sized for the SM count of a B200 whatever device is current, so that the size calls need none.
+constexpr int kSizingSms = 160;
+
+bool sizes_ok(int M, int N, int K, int rank, int L) {
+  return M >= 0 && N >= 8 && N % 8 == 0 && N <= CR_MAX_K && K >= 8 && K % 8 == 0 && K <= CR_MAX_K && rank >= 4 &&
+         rank <= CR_MAX_RANK && rank % 4 == 0 && L >= 1 && L <= CR_MAX_ADAPTERS;
+}
+
+size_t v_bytes(int M, int K, int rank) {
+  return bytes_f32(static_cast<int64_t>(M) * rank * cr::lora_row_splits(M > 0 ? M : 1, K, rank, kSizingSms));
+}
+
+cr_status check_rows(const void* p, int64_t ld, int cols) {
+  if (ld < cols) return CR_ERR_INVALID_ARG;
+  return (!aligned(p, 16) || ld % 8 != 0) ? CR_ERR_MISALIGNED : CR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t cr_lora_forward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
+  if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
+  return kWsHead + v_bytes(M, K, rank);
+}
+
+cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, const void* down, const void* up,
+                          const float* scale, const void* base, int64_t ldb, void* Y, int64_t ldy, void* V, int M,
+                          int N, int K, int rank, int num_adapters, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  if (M < 0 || N < 0 || K < 0 || rank < 0 || num_adapters < 0 || ldx < 0 || ldb < 0 || ldy < 0)
+    return CR_ERR_INVALID_ARG;
+  if (M > 0 && (!X || !down || !up || !scale || !Y)) return CR_ERR_INVALID_ARG;
+  if (!sizes_ok(M, N, K, rank, num_adapters)) return CR_ERR_UNSUPPORTED_SHAPE;
+  cr_status st = check_rows(X, ldx, K);
+  if (st == CR_OK) st = check_rows(Y, ldy, N);
+  if (st == CR_OK && base) st = check_rows(base, ldb, N);
+  if (st != CR_OK) return st;
+  if (!aligned(down, 16) || !aligned(up, 16) || !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(V, 8))
+    return CR_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < cr_lora_forward_workspace_size(M, N, K, rank, num_adapters) ||
+      !aligned(workspace, 256))
+    return CR_ERR_WORKSPACE;
+  int nsm = 0;
+  if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
+  if (M == 0) return CR_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead);
+  const int splits = cr::lora_row_splits(M, K, rank, nsm < kSizingSms ? nsm : kSizingSms);
+  const uint16_t* dn = static_cast<const uint16_t*>(down);
+  const uint16_t* u = static_cast<const uint16_t*>(up);
+  cudaError_t e = cr::launch_lora_v_rows(static_cast<const uint16_t*>(X), ldx, adapter, dn, v, M, K, rank,
+                                         num_adapters, splits, ws_status(workspace), s);
+  if (e == cudaSuccess)
+    e = cr::launch_lora_y_rows(v, splits, adapter, u, scale, static_cast<const uint16_t*>(base), ldb,
+                               static_cast<uint16_t*>(Y), ldy, static_cast<uint16_t*>(V), M, N, rank, num_adapters, s);
+  return cuda_status(e);
+}
+
+size_t cr_lora_backward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
+  if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
+  return kWsHead + v_bytes(M, N, rank) + bytes_f32(static_cast<int64_t>(num_adapters) * rank * K) +
+         bytes_f32(static_cast<int64_t>(num_adapters) * rank * N);
+}
+
+cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* codes,
+                           const float* code_scales, const void* V, const int32_t* adapter, const void* down,
+                           const void* up, const float* scale, const void* dX_base, int64_t ldb, void* dX, int64_t lddx,
+                           void* d_down, void* d_up, int M, int N, int K, int rank, int num_adapters, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || rank < 0 || num_adapters < 0 || lddy < 0 || ldx < 0 || ldb < 0 || lddx < 0)
+    return CR_ERR_INVALID_ARG;
+  if (M > 0 && (!dY || !down || !up)) return CR_ERR_INVALID_ARG;
+  if (!scale || (X && codes) || ((codes != nullptr) != (code_scales != nullptr))) return CR_ERR_INVALID_ARG;
+  if (M > 0 && ((d_down && !X && !codes) || (d_up && !V))) return CR_ERR_INVALID_ARG;
+  if (!sizes_ok(M, N, K, rank, num_adapters) || (codes && K % 256 != 0)) return CR_ERR_UNSUPPORTED_SHAPE;
+  cr_status st = check_rows(dY, lddy, N);
+  if (st == CR_OK && X) st = check_rows(X, ldx, K);
+  if (st == CR_OK && dX) st = check_rows(dX, lddx, K);
+  if (st == CR_OK && dX && dX_base) st = check_rows(dX_base, ldb, K);
+  if (st != CR_OK) return st;
+  if (!aligned(codes, 16) || !aligned(code_scales, 4) || !aligned(V, 8) || !aligned(adapter, 4) || !aligned(down, 16) ||
+      !aligned(up, 16) || !aligned(scale, 4) || !aligned(d_down, 16) || !aligned(d_up, 16))
+    return CR_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < cr_lora_backward_workspace_size(M, N, K, rank, num_adapters) ||
+      !aligned(workspace, 256))
+    return CR_ERR_WORKSPACE;
+  int nsm = 0;
+  if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int L = num_adapters;
+  const int64_t nd = static_cast<int64_t>(L) * rank * K, nu = static_cast<int64_t>(L) * rank * N;
+  if (M == 0) {  // no rows: the gradients are zero
+    cudaError_t e = cudaSuccess;
+    if (d_down) e = cudaMemsetAsync(d_down, 0, static_cast<size_t>(nd) * 2, s);
+    if (e == cudaSuccess && d_up) e = cudaMemsetAsync(d_up, 0, static_cast<size_t>(nu) * 2, s);
+    return cuda_status(e);
+  }
+  uint8_t* w = static_cast<uint8_t*>(workspace) + kWsHead;
+  float* dv = reinterpret_cast<float*>(w);
+  float* gd = reinterpret_cast<float*>(w + v_bytes(M, N, rank));
+  float* gu = reinterpret_cast<float*>(w + v_bytes(M, N, rank) + bytes_f32(nd));
+  const int splits = cr::lora_row_splits(M, N, rank, nsm < kSizingSms ? nsm : kSizingSms);
+  cudaError_t e = cudaSuccess;
+  if (dX || d_down)
+    e = cr::launch_lora_v_rows(static_cast<const uint16_t*>(dY), lddy, adapter, static_cast<const uint16_t*>(up), dv, M,
+                               N, rank, L, splits, ws_status(workspace), s);
+  if (e == cudaSuccess && dX)
+    e = cr::launch_lora_y_rows(dv, splits, adapter, static_cast<const uint16_t*>(down), scale,
+                               static_cast<const uint16_t*>(dX_base), ldb, static_cast<uint16_t*>(dX), lddx, nullptr, M,
+                               K, rank, L, s);
+  if (e == cudaSuccess && d_down)
+    e = cr::launch_lora_grad_rows(codes ? codes : X, ldx, code_scales, dv, nullptr, splits, adapter, scale, gd, M, K,
+                                  rank, L, s);
+  if (e == cudaSuccess && d_down)
+    e = cr::launch_lora_grad_finish(gd, 1, 0, static_cast<uint16_t*>(d_down), nd, codes != nullptr, s);
+  if (e == cudaSuccess && d_up)
+    e = cr::launch_lora_grad_rows(dY, lddy, nullptr, nullptr, static_cast<const uint16_t*>(V), 1, adapter, scale, gu, M,
+                                  N, rank, L, s);
+  if (e == cudaSuccess && d_up)
+    e = cr::launch_lora_grad_finish(gu, 1, 0, static_cast<uint16_t*>(d_up), nu, false, s);
+  return cuda_status(e);
+}
+
+cr_status cr_ckpt_save(const void* X, int M, int K, int64_t ldx, void* codes, float* scales, void* stream) {
+  if (M < 0 || K < 0 || ldx < 0 || (M > 0 && (!X || !codes || !scales))) return CR_ERR_INVALID_ARG;
+  if (K < 256 || K % 256 != 0 || K > CR_MAX_K) return CR_ERR_UNSUPPORTED_SHAPE;
+  cr_status st = check_rows(X, ldx, K);
+  if (st != CR_OK) return st;
+  if (!aligned(codes, 16) || !aligned(scales, 4)) return CR_ERR_MISALIGNED;
+  int nsm = 0;
+  if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
+  if (M == 0) return CR_OK;
+  return cuda_status(cr::launch_ckpt_save(static_cast<const uint16_t*>(X), M, K, ldx, static_cast<int8_t*>(codes),
+                                          scales, static_cast<cudaStream_t>(stream)));
+}
+
+cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, void* X, int64_t ldx, void* stream) {
+  if (M < 0 || K < 0 || ldx < 0 || (M > 0 && (!X || !codes || !scales))) return CR_ERR_INVALID_ARG;
+  if (K < 256 || K % 256 != 0 || K > CR_MAX_K) return CR_ERR_UNSUPPORTED_SHAPE;
+  cr_status st = check_rows(X, ldx, K);
+  if (st != CR_OK) return st;
+  if (!aligned(codes, 16) || !aligned(scales, 4)) return CR_ERR_MISALIGNED;
+  int nsm = 0;
+  if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
+  if (M == 0) return CR_OK;
+  return cuda_status(cr::launch_ckpt_load(static_cast<const int8_t*>(codes), scales, M, K, static_cast<uint16_t*>(X),
+                                          ldx, static_cast<cudaStream_t>(stream)));
+}
+
+size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group) {
+  (void)M;
+  (void)group;
+  if (N < 0 || K < 0) return kWsHead;
+  return kWsHead + cr::round_up(static_cast<size_t>(N) * static_cast<size_t>(K) * 2, 256);
+}
+
+cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const float* w_scale, void* dX, int64_t lddx,
+                             int M, int N, int K, int group, void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || lddy < 0 || lddx < 0) return CR_ERR_INVALID_ARG;
+  if (M > 0 && (!dX || (N > 0 && (!dY || !Wq || !w_scale)))) return CR_ERR_INVALID_ARG;
+  if ((group != CR_GROUP_16 && group != CR_GROUP_64 && group != CR_GROUP_256 && group != CR_GROUP_1024) || K < 256 ||
+      K % 256 != 0 || K % group != 0 || K > CR_MAX_K || N % 8 != 0 || N > CR_MAX_K)
+    return CR_ERR_UNSUPPORTED_SHAPE;
+  cr_status st = check_rows(dY, lddy, N);
+  if (st == CR_OK) st = check_rows(dX, lddx, K);
+  if (st != CR_OK) return st;
+  if (!aligned(Wq, 16) || !aligned(w_scale, 4)) return CR_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < cr_w4a4_grad_input_workspace_size(M, N, K, group) || !aligned(workspace, 256))
+    return CR_ERR_WORKSPACE;
+  int nsm = 0;
+  if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
+  if (M == 0) return CR_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0)  // no outputs: the gradient is zero
+    return cuda_status(cudaMemset2DAsync(dX, static_cast<size_t>(lddx) * 2, 0, static_cast<size_t>(K) * 2,
+                                         static_cast<size_t>(M), s));
+  uint16_t* w = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWsHead);
+  cudaError_t e = cr::launch_weight_values(static_cast<const uint8_t*>(Wq), w_scale, w, N, K, group,
+                                           ws_status(workspace), s);
+  if (e != cudaSuccess) return CR_ERR_CUDA;
+  return static_cast<cr_status>(cr::launch_gemm_bf16(dY, lddy, w, dX, lddx, M, N, K, ws_status(workspace), nsm, s));
+}
+
+}  // extern "C"

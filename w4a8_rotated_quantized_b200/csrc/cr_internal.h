@@ -152,6 +152,41 @@ int launch_w4a4_gemm_multi_s32(const void* Xq, int num_proj, const void* const* 
                                const int64_t* ldc, const int* N, int M, int K, int* status, int num_sms,
                                cudaStream_t stream);
 
+// ---- adapters beside a projection, their gradients, 8-bit checkpoints (lora_rows.cu, ckpt_kernels.cu) ----
+constexpr int kMaxRank = 128;
+// K splits of the row form's V product; V holds that many partial [M, rank] arrays.
+int lora_row_splits(int M, int K, int rank, int num_sms);
+// V partials of the rows' own adapters (zeros for rows without one).  Clears the status word.
+cudaError_t launch_lora_v_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, float* V,
+                               int M, int K, int rank, int L, int splits, int* status, cudaStream_t stream);
+// Y = base + scale[a] * V . up[a]; the unscaled V, splits added, also to Vout (bf16 [M, rank]) if given.
+cudaError_t launch_lora_y_rows(const float* V, int splits, const int32_t* adapter, const uint16_t* up,
+                               const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy,
+                               uint16_t* Vout, int M, int N, int rank, int L, cudaStream_t stream);
+// G float32 [L, rank, C] = scale[a] * sum over the adapter's rows of V^T Z; Z bf16 rows, or codes with
+// code_scale.  V: float32 partials (V32, splits) or bf16 (V16).
+cudaError_t launch_lora_grad_rows(const void* Z, int64_t ldz, const float* code_scale, const float* V32,
+                                  const uint16_t* V16, int splits, const int32_t* adapter, const float* scale, float* G,
+                                  int M, int C, int rank, int L, cudaStream_t stream);
+// bf16 G = the partial sums added in order, rotated by H256 if `rotate` (then total is a multiple of 256).
+cudaError_t launch_lora_grad_finish(const float* parts_sum, int parts, int64_t part_stride, uint16_t* G, int64_t total,
+                                    bool rotate, cudaStream_t stream);
+cudaError_t launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes, float* scales,
+                             cudaStream_t stream);
+cudaError_t launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uint16_t* X, int64_t ldx,
+                             cudaStream_t stream);
+
+// ---- the W4A4 layer's input gradient (ckpt_kernels.cu, gemm_bf16.cu) ----
+// W bf16 [N, K] = w_scale[n] * (q[n, :] H_group).  Clears the status word.
+cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16_t* W, int N, int K, int group,
+                                 int* status, cudaStream_t stream);
+// Y[M, K] = A[M, N] . W[N, K], bf16 operands (row stride lda; W dense), float32 sums, bf16 out.
+int launch_gemm_bf16(const void* A, int64_t lda, const void* W, void* Y, int64_t ldy, int M, int N, int K, int* status,
+                     int num_sms, cudaStream_t stream);
+
+// Supported device = compute capability 10.0 (api.cu): CR_OK and its SM count, or the status to return.
+int check_current_device(int* num_sms);
+
 // Raw int32 product C[M, N] = sum_k qa*qw (same kernel, integer epilogue).
 int launch_w4a4_gemm_s32(const void* Xq, const void* Wq, int32_t* C, int64_t ldc, int M, int N, int K, int* status,
                          int num_sms, cudaStream_t stream);

@@ -1,0 +1,44 @@
+// lora_device.cuh -- small device helpers of the adapter kernels: bf16 conversions of eight values and
+// the adapter of a row.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace cr {
+
+// bf16 -> float32 is a 16-bit shift of the bit pattern.
+__device__ __forceinline__ float bf16_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+__device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+
+__device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+__device__ __forceinline__ void widen8(uint4 q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    v[2 * h] = __uint_as_float(w[h] << 16);
+    v[2 * h + 1] = __uint_as_float(w[h] & 0xFFFF0000u);
+  }
+}
+
+// Two floats -> packed bf16 (round to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+// Row m's adapter, -1 where it has none (an index outside the pool); without indices every row has the first.
+__device__ __forceinline__ int row_adapter(const int32_t* __restrict__ adapter, int64_t m, int L) {
+  if (!adapter) return 0;
+  const int a = __ldg(adapter + m);
+  return static_cast<unsigned>(a) < static_cast<unsigned>(L) ? a : -1;
+}
+
+}  // namespace cr
