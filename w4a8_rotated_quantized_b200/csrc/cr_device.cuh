@@ -136,6 +136,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
 // Tile load by one CTA of a CTA pair whose completion is counted on `bar`, an
 // mbarrier that may live in either CTA of the pair (a shared::cluster address
 // from mapa_shared): both CTAs' loads of one stage complete on the leader's
@@ -218,6 +227,47 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
          | (1u << 10)                                // B: signed 8-bit
          | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// Shared-memory matrix descriptor for an operand whose rows run along the product's sum ("MN-major": 64
+// consecutive 16-bit values of the M or N side in each 128-byte swizzle row): 8-row atoms of 1024 bytes
+// stacked along the sum (stride byte offset 1024), the next 64 values of the M or N side
+// `group_bytes` further (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t group_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((group_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16 on bf16 operands, float32 accumulator, tile M x N;
+// `a_mn` / `b_mn`: the operand is MN-major instead of K-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4)                                   // D format: f32
+         | (1u << 7)                                 // A: bf16
+         | (1u << 10)                                // B: bf16
+         | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u)
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T on 16-bit operands, one CTA.  Only lane 0 of the converged warp issues.
+__device__ __forceinline__ void umma_f16_ss_lane0(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t accumulate, int lane) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.eq.s32 e, %5, 0; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_lane0(uint32_t bar, int lane) {
+  asm volatile(
+      "{ .reg .pred e; setp.eq.s32 e, %1, 0; "
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lane)
+      : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, one CTA.  `accumulate` = 0 overwrites D.
@@ -358,6 +408,15 @@ __device__ __forceinline__ void umma_i8_pair_ss_lane0(uint32_t d_tmem, uint64_t 
   asm volatile(
       "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.eq.s32 e, %5, 0; "
       "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
+      : "memory");
+}
+// Same on 16-bit operands.
+__device__ __forceinline__ void umma_f16_pair_ss_lane0(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                       uint32_t accumulate, int lane) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.eq.s32 e, %5, 0; "
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
       : "memory");
 }

@@ -82,6 +82,12 @@ bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* ptr, 
                   uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle,
                   CUtensorMapL2promotion promo);
 
+// 3-D tensor map over `planes` dense [rows, cols] matrices one after the other; boxes of one plane: rows
+// past a plane's last read as zeros, never as the next plane's.
+bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* ptr, uint64_t planes, uint64_t rows,
+                  uint64_t cols, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle,
+                  CUtensorMapL2promotion promo);
+
 // ---- INT8 GEMM (gemm_i8.cu) ----
 // Y = bf16(acc * a_scale[0] * w_scale[n] + bias[n]), acc = Xq . Wq^T over one-byte codes.
 int launch_i8_gemm(const void* Xq, const float* a_scale, const void* Wq, const float* w_scale, const void* bias,
