@@ -35,8 +35,13 @@ bool sizes_ok(int M, int N, int K, int rank, int L) {
          rank <= CR_MAX_RANK && rank % 4 == 0 && L >= 1 && L <= CR_MAX_ADAPTERS;
 }
 
-size_t v_bytes(int M, int K, int rank) {
-  return bytes_f32(static_cast<int64_t>(M) * rank * cr::lora_row_splits(M > 0 ? M : 1, K, rank, kSizingSms));
+// Row-form V holds a partial sum for each K split, the tensor-core form one array.
+int v_splits(int M, int K, int rank, int num_sms) {
+  return M <= cr::kLoraRowsMaxM ? cr::lora_row_splits(M > 0 ? M : 1, K, rank, num_sms) : 1;
+}
+
+size_t grad_bytes(int M, int C, int rank, int L) {
+  return bytes_f32(static_cast<int64_t>(cr::lora_grad_splits(M > 0 ? M : 1, C, L, kSizingSms)) * L * rank * C);
 }
 
 cr_status check_rows(const void* p, int64_t ld, int cols) {
@@ -50,7 +55,7 @@ extern "C" {
 
 size_t cr_lora_forward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  return kWsHead + v_bytes(M, K, rank);
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank * v_splits(M, K, rank, kSizingSms));
 }
 
 cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, const void* down, const void* up,
@@ -75,21 +80,30 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if (M == 0) return CR_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead);
-  const int splits = cr::lora_row_splits(M, K, rank, nsm < kSizingSms ? nsm : kSizingSms);
+  if (nsm > kSizingSms) nsm = kSizingSms;
+  uint16_t* vout = static_cast<uint16_t*>(V);
+  int* status = ws_status(workspace);
+  const uint16_t* x = static_cast<const uint16_t*>(X);
   const uint16_t* dn = static_cast<const uint16_t*>(down);
   const uint16_t* u = static_cast<const uint16_t*>(up);
-  cudaError_t e = cr::launch_lora_v_rows(static_cast<const uint16_t*>(X), ldx, adapter, dn, v, M, K, rank,
-                                         num_adapters, splits, ws_status(workspace), s);
-  if (e == cudaSuccess)
-    e = cr::launch_lora_y_rows(v, splits, adapter, u, scale, static_cast<const uint16_t*>(base), ldb,
-                               static_cast<uint16_t*>(Y), ldy, static_cast<uint16_t*>(V), M, N, rank, num_adapters, s);
-  return cuda_status(e);
+  const uint16_t* b = static_cast<const uint16_t*>(base);
+  uint16_t* y = static_cast<uint16_t*>(Y);
+  const int L = num_adapters;
+  if (M <= cr::kLoraRowsMaxM) {
+    const int splits = v_splits(M, K, rank, nsm);
+    cudaError_t e = cr::launch_lora_v_rows(x, ldx, adapter, dn, v, M, K, rank, L, splits, status, s);
+    if (e == cudaSuccess)
+      e = cr::launch_lora_y_rows(v, splits, adapter, u, scale, b, ldb, y, ldy, vout, M, N, rank, L, s);
+    return cuda_status(e);
+  }
+  int r = cr::launch_lora_v_mma(x, ldx, adapter, dn, v, vout, M, K, rank, L, status, nsm, s);
+  if (r == CR_OK) r = cr::launch_lora_y_mma(v, adapter, u, scale, b, ldb, y, ldy, M, N, rank, L, status, nsm, s);
+  return static_cast<cr_status>(r);
 }
 
 size_t cr_lora_backward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  return kWsHead + v_bytes(M, N, rank) + bytes_f32(static_cast<int64_t>(num_adapters) * rank * K) +
-         bytes_f32(static_cast<int64_t>(num_adapters) * rank * N);
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + grad_bytes(M, K, rank, num_adapters) + grad_bytes(M, N, rank, num_adapters);
 }
 
 cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* codes,
@@ -127,28 +141,42 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   }
   uint8_t* w = static_cast<uint8_t*>(workspace) + kWsHead;
   float* dv = reinterpret_cast<float*>(w);
-  float* gd = reinterpret_cast<float*>(w + v_bytes(M, N, rank));
-  float* gu = reinterpret_cast<float*>(w + v_bytes(M, N, rank) + bytes_f32(nd));
-  const int splits = cr::lora_row_splits(M, N, rank, nsm < kSizingSms ? nsm : kSizingSms);
-  cudaError_t e = cudaSuccess;
-  if (dX || d_down)
-    e = cr::launch_lora_v_rows(static_cast<const uint16_t*>(dY), lddy, adapter, static_cast<const uint16_t*>(up), dv, M,
-                               N, rank, L, splits, ws_status(workspace), s);
-  if (e == cudaSuccess && dX)
-    e = cr::launch_lora_y_rows(dv, splits, adapter, static_cast<const uint16_t*>(down), scale,
-                               static_cast<const uint16_t*>(dX_base), ldb, static_cast<uint16_t*>(dX), lddx, nullptr, M,
-                               K, rank, L, s);
-  if (e == cudaSuccess && d_down)
-    e = cr::launch_lora_grad_rows(codes ? codes : X, ldx, code_scales, dv, nullptr, splits, adapter, scale, gd, M, K,
-                                  rank, L, s);
-  if (e == cudaSuccess && d_down)
-    e = cr::launch_lora_grad_finish(gd, 1, 0, static_cast<uint16_t*>(d_down), nd, codes != nullptr, s);
-  if (e == cudaSuccess && d_up)
-    e = cr::launch_lora_grad_rows(dY, lddy, nullptr, nullptr, static_cast<const uint16_t*>(V), 1, adapter, scale, gu, M,
-                                  N, rank, L, s);
-  if (e == cudaSuccess && d_up)
-    e = cr::launch_lora_grad_finish(gu, 1, 0, static_cast<uint16_t*>(d_up), nu, false, s);
-  return cuda_status(e);
+  float* gd = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank));
+  float* gu = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank) + grad_bytes(M, K, rank, L));
+  if (nsm > kSizingSms) nsm = kSizingSms;
+  int* status = ws_status(workspace);
+  if (dX || d_down) {
+    st = static_cast<cr_status>(cr::launch_lora_v_mma(static_cast<const uint16_t*>(dY), lddy, adapter,
+                                                      static_cast<const uint16_t*>(up), dv, nullptr, M, N, rank, L,
+                                                      status, nsm, s));
+    if (st != CR_OK) return st;
+  } else if (cudaMemsetAsync(workspace, 0, 16, s) != cudaSuccess) {
+    return CR_ERR_CUDA;
+  }
+  if (dX) {
+    st = static_cast<cr_status>(cr::launch_lora_y_mma(dv, adapter, static_cast<const uint16_t*>(down), scale,
+                                                      static_cast<const uint16_t*>(dX_base), ldb,
+                                                      static_cast<uint16_t*>(dX), lddx, M, K, rank, L, status, nsm, s));
+    if (st != CR_OK) return st;
+  }
+  if (d_down) {
+    const int parts = cr::lora_grad_splits(M, K, L, nsm);
+    st = static_cast<cr_status>(cr::launch_lora_grad_mma(codes ? codes : X, ldx, code_scales, dv, nullptr, adapter,
+                                                         scale, gd, M, K, rank, L, parts, status, s));
+    if (st != CR_OK) return st;
+    if (cr::launch_lora_grad_finish(gd, parts, nd, static_cast<uint16_t*>(d_down), nd, codes != nullptr, s) !=
+        cudaSuccess)
+      return CR_ERR_CUDA;
+  }
+  if (d_up) {
+    const int parts = cr::lora_grad_splits(M, N, L, nsm);
+    st = static_cast<cr_status>(cr::launch_lora_grad_mma(dY, lddy, nullptr, nullptr, static_cast<const uint16_t*>(V),
+                                                         adapter, scale, gu, M, N, rank, L, parts, status, s));
+    if (st != CR_OK) return st;
+    if (cr::launch_lora_grad_finish(gu, parts, nu, static_cast<uint16_t*>(d_up), nu, false, s) != cudaSuccess)
+      return CR_ERR_CUDA;
+  }
+  return CR_OK;
 }
 
 cr_status cr_ckpt_save(const void* X, int M, int K, int64_t ldx, void* codes, float* scales, void* stream) {

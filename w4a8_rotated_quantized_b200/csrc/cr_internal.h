@@ -160,6 +160,8 @@ int launch_w4a4_gemm_multi_s32(const void* Xq, int num_proj, const void* const* 
 
 // ---- adapters beside a projection, their gradients, 8-bit checkpoints (lora_rows.cu, ckpt_kernels.cu) ----
 constexpr int kMaxRank = 128;
+// Rows up to which the row form runs (lora_rows.cu), above it the tensor-core form.
+constexpr int kLoraRowsMaxM = 64;
 // K splits of the row form's V product; V holds that many partial [M, rank] arrays.
 int lora_row_splits(int M, int K, int rank, int num_sms);
 // V partials of the rows' own adapters (zeros for rows without one).  Clears the status word.
@@ -169,11 +171,19 @@ cudaError_t launch_lora_v_rows(const uint16_t* X, int64_t ldx, const int32_t* ad
 cudaError_t launch_lora_y_rows(const float* V, int splits, const int32_t* adapter, const uint16_t* up,
                                const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy,
                                uint16_t* Vout, int M, int N, int rank, int L, cudaStream_t stream);
-// G float32 [L, rank, C] = scale[a] * sum over the adapter's rows of V^T Z; Z bf16 rows, or codes with
-// code_scale.  V: float32 partials (V32, splits) or bf16 (V16).
-cudaError_t launch_lora_grad_rows(const void* Z, int64_t ldz, const float* code_scale, const float* V32,
-                                  const uint16_t* V16, int splits, const int32_t* adapter, const float* scale, float* G,
-                                  int M, int C, int rank, int L, cudaStream_t stream);
+// The same products on the tensor cores, for batches (lora_mma.cu).  V float32 [M, rank], one array; Vout its
+// bf16 copy or null.
+int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, float* V,
+                      uint16_t* Vout, int M, int K, int rank, int L, int* status, int num_sms, cudaStream_t stream);
+int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up, const float* scale,
+                      const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, int M, int N, int rank, int L,
+                      int* status, int num_sms, cudaStream_t stream);
+// Partial sums G float32 [splits, L, rank, C] of scale[a] * sum over the adapter's rows of V^T Z; Z bf16
+// rows, or codes with code_scale (then in the checkpoint's rotated basis).  V: float32 or bf16 [M, rank].
+int lora_grad_splits(int M, int C, int L, int num_sms);
+int launch_lora_grad_mma(const void* Z, int64_t ldz, const float* code_scale, const float* V32, const uint16_t* V16,
+                         const int32_t* adapter, const float* scale, float* G, int M, int C, int rank, int L,
+                         int splits, int* status, cudaStream_t stream);
 // bf16 G = the partial sums added in order, rotated by H256 if `rotate` (then total is a multiple of 256).
 cudaError_t launch_lora_grad_finish(const float* parts_sum, int parts, int64_t part_stride, uint16_t* G, int64_t total,
                                     bool rotate, cudaStream_t stream);

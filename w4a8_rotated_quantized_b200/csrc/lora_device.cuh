@@ -34,6 +34,13 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// Two floats as bf16 pairs: the rounded values in `hi`, what they leave, rounded, in `lo`.  A non-finite
+// value's rest is NaN, which the sum keeps.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+
 // Row m's adapter, -1 where it has none (an index outside the pool); without indices every row has the first.
 __device__ __forceinline__ int row_adapter(const int32_t* __restrict__ adapter, int64_t m, int L) {
   if (!adapter) return 0;

@@ -1,0 +1,975 @@
+// lora_mma.cu -- low-rank adapters beside a projection on the tensor cores (tcgen05 kind::f16, float32
+// accumulators in TMEM): the three products of forward and backward, for batches of tokens.
+//
+//   v:    V[m, j]    = sum_k X[m, k] A[a][j, k]                      (also dV from dY and U)
+//   y:    Y[m, n]    = base[m, n] + s[a] sum_j V[m, j] U[a][j, n]    (also dX from dV and A)
+//   grad: G[a][j, c] = s[a] sum_{m of a} V[m, j] Z[m, c]             (d_up from dY; d_down from X or its codes)
+//
+// With ranks up to 128 each product does 2 r flops for every activation value it moves, so all three are
+// bound by memory; the tensor cores keep the arithmetic out of the way, and the tiles are laid out so that
+// every activation is read once, by TMA, with the next tiles already on their way.
+//
+// Rows name their adapters in any order.  A tile of tokens takes the list of the adapters that occur in it:
+// v multiplies by all of them at once (up to 256 rank rows side by side) and keeps each row's own columns;
+// y runs one short product for each and writes only the rows that named it; grad takes the tiles in which
+// its adapter occurs and clears the other rows in both operands.  No row's or adapter's values can reach
+// another's result that way, non-finite ones included.
+//
+// V stays float32 between the products.  As an operand it is split into two bf16 values (the rounded value
+// and the rounded rest: 16 bits of mantissa), so the one rounding that counts is the output's own.
+//
+// Every wait is bounded; on expiry a CTA records CR_ERR_TIMEOUT in the device status word and winds down.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "cr_device.cuh"
+#include "cr_internal.h"
+#include "lora_device.cuh"
+
+namespace cr {
+namespace {
+
+constexpr int TM = 128;             // tokens of a v or y tile
+constexpr int KB = 64;              // bf16 values of a 128-byte swizzle row
+constexpr int kSmemMax = 232448 - 1024;  // the base is aligned up to 1024
+constexpr int kBarBytes = 256;      // mbarriers and the TMEM slot
+constexpr int kListBytes = 2 * TM * 4;   // a tile's row adapters and the list of distinct ones
+
+inline __host__ __device__ int round16(int r) { return (r + 15) & ~15; }
+inline __host__ __device__ int tmem_cols_for(int c) { return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : c <= 256 ? 256 : 512; }
+
+__device__ __forceinline__ uint8_t* align_smem(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ void fail(volatile int* abort, int* status) {
+  record_status(status, CR_ERR_TIMEOUT);
+  *abort = 1;
+}
+
+// TMA loads of this CTA that nobody waits for any more must land before it exits.
+__device__ __forceinline__ void grace() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
+// The adapters of the tile's 128 rows into ids[] (-1: none, rows past M too) and the distinct ones, in order
+// of first appearance, into list[]; returns how many.  Called by all threads of the block (at least 128).
+__device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter, int64_t m0, int M, int L, int* ids,
+                                             int* list, int* counts) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (t < TM) ids[t] = m0 + t < M ? row_adapter(adapter, m0 + t, L) : -1;
+  if (!adapter) {
+    if (t == 0) list[0] = 0;
+    __syncthreads();
+    return 1;
+  }
+  __syncthreads();
+  bool first = false;
+  uint32_t firsts = 0;
+  if (t < TM) {
+    const int a = ids[t];
+    const uint32_t same = __match_any_sync(0xffffffffu, a);
+    first = a >= 0 && __ffs(same) - 1 == lane;
+    for (int i = 0; first && i < 32 * warp; ++i) first = ids[i] != a;
+    firsts = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) counts[warp] = __popc(firsts);
+  }
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < TM / 32; ++w) {
+    before += w < warp ? counts[w] : 0;
+    all += counts[w];
+  }
+  if (first) list[before + __popc(firsts & ((1u << lane) - 1))] = ids[t];
+  __syncthreads();
+  return all;
+}
+
+// ---------------------------------------------------------------------------------------------------
+// v: 128 tokens x (up to 256 / rank adapters side by side); the sum over k split over a cluster's CTAs,
+// whose partial sums are added in rank order through distributed shared memory.
+// ---------------------------------------------------------------------------------------------------
+
+struct VPlan {
+  int rp, cap, stages, stage, part_ld, off_part, off_list, off_bar, smem, cols;
+};
+inline __host__ __device__ VPlan v_plan(int rank, int L) {
+  VPlan p;
+  p.rp = round16(rank);
+  p.cap = 256 / p.rp;
+  if (p.cap > L) p.cap = L;
+  p.stage = TM * 128 + p.cap * p.rp * 128;
+  p.part_ld = p.rp + 4;  // rows 4 banks apart: eight rows' 16-byte pieces lie side by side
+  const int part = TM * p.part_ld * 4;
+  p.stages = (kSmemMax - part - kListBytes - kBarBytes) / p.stage;
+  if (p.stages > 8) p.stages = 8;
+  p.off_part = p.stages * p.stage;
+  p.off_list = p.off_part + part;
+  p.off_bar = p.off_list + kListBytes;
+  p.smem = p.off_bar + kBarBytes;
+  p.cols = tmem_cols_for(p.cap * p.rp);
+  return p;
+}
+
+constexpr int kVThreads = 192;  // warp 0 MMA, warp 1 TMA, warps 2-5 epilogue
+
+__global__ void __launch_bounds__(kVThreads, 1)
+    lora_v_mma_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_a,
+                      const int32_t* __restrict__ adapter, float* __restrict__ V, uint16_t* __restrict__ Vout, int M,
+                      int K, int rank, int L, int splits, int* __restrict__ status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = align_smem(smem_raw);
+  const VPlan p = v_plan(rank, L);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = static_cast<int>(cluster_ctarank());
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / splits) * TM;
+  float* part = reinterpret_cast<float*>(base + p.off_part);
+  int* ids = reinterpret_cast<int*>(base + p.off_list);
+  int* list = ids + TM;
+  auto full = [&](int s) { return smem_u32(base + p.off_bar) + 8u * s; };
+  auto empty = [&](int s) { return smem_u32(base + p.off_bar) + 64u + 8u * s; };
+  const uint32_t acc_full = smem_u32(base + p.off_bar) + 128u, acc_empty = acc_full + 8u;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 144);
+  volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 148);
+  int* counts = reinterpret_cast<int*>(base + p.off_bar + 160);
+
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = CR_OK;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 4);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1 && lane == 0) {
+    prefetch_tmap(&tmap_x);
+    prefetch_tmap(&tmap_a);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(slot), p.cols);
+    tmem_relinquish();
+  }
+  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+
+  const int nkb = (K + KB - 1) / KB;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * split / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- MMA issuer
+    bool ok = true, committed = false;
+    uint32_t ph = 0, last_bar = 0, last_ph = 0;
+    int s = 0, pass = 0;
+    for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
+      const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
+      const uint32_t idesc = idesc_bf16(TM, c * p.rp, false, false);
+      if (pass && !mbar_wait(acc_empty, (pass - 1) & 1, abort)) { ok = false; break; }
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(full(s), ph, abort)) { ok = false; break; }
+        __syncwarp();
+        tc_fence_after();
+        const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * p.stage));
+        const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * p.stage + TM * 128));
+#pragma unroll
+        for (int kk = 0; kk < KB / 16; ++kk)
+          umma_f16_ss_lane0(tmem, da + 2u * kk, db + 2u * kk, idesc, (kb != kb0 || kk) ? 1u : 0u, lane);
+        umma_commit_lane0(empty(s), lane);
+        last_bar = empty(s);
+        last_ph = ph;
+        committed = true;
+        if (++s == p.stages) { s = 0; ph ^= 1u; }
+      }
+      if (ok) umma_commit_lane0(acc_full, lane);
+    }
+    if (!ok) {
+      if (lane == 0) fail(abort, status);
+      volatile int never = 0;
+      if (committed) mbar_wait(last_bar, last_ph, &never);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int s = 0, f = 0;
+      uint32_t ph = 0;
+      for (int d0 = 0; ok && d0 < nd; d0 += p.cap) {
+        const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
+        for (int kb = kb0; kb < kb1; ++kb, ++f) {
+          if (f >= p.stages && !mbar_wait(empty(s), ph ^ 1u, abort)) { ok = false; break; }
+          const uint32_t dst = smem_u32(base + s * p.stage);
+          mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(TM + c * p.rp) * 128u);
+          tma_load_2d(dst, &tmap_x, kb * KB, static_cast<int32_t>(m0), full(s));
+          for (int i = 0; i < c; ++i)
+            tma_load_3d(dst + TM * 128 + i * p.rp * 128, &tmap_a, kb * KB, 0, list[d0 + i], full(s));
+          if (++s == p.stages) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {
+        fail(abort, status);
+        grace();
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue: own columns of each row
+    const int q = warp & 3;
+    const int row = 32 * q + lane;
+    const int mine = ids[row];
+    float* out = part + row * p.part_ld;
+    if (mine < 0)
+      for (int j = 0; j < p.rp; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool ok = true;
+    int pass = 0;
+    for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
+      const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
+      if (!mbar_wait_warp(acc_full, pass & 1, abort)) { ok = false; break; }
+      tc_fence_after();
+      for (int i = 0; i < c; ++i) {
+        const bool hit = mine == list[d0 + i];
+        if (!__any_sync(0xffffffffu, hit)) continue;
+        for (int j = 0; j < p.rp; j += 16) {
+          uint32_t r[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(i * p.rp + j), r);
+          tmem_ld_wait();
+          if (hit) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(out + j + e) = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
+                                                                    __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+    }
+    if (!ok) fail(abort, status);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // every split's partial sums are in its shared memory
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.cols);
+  }
+  // this CTA's share of the rows: the splits' sums added in order
+  const int rows = TM / splits, groups = rank >> 2;
+  const uint32_t part_addr = smem_u32(part);
+  for (int i = threadIdx.x; i < rows * groups; i += kVThreads) {
+    const int row = split * rows + i / groups, j = 4 * (i % groups);
+    if (m0 + row >= M) break;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < splits; ++c) {
+      const float4 u = ld_shared_cluster_f4(mapa_shared(part_addr + 4u * (row * p.part_ld + j), c));
+      t.x += u.x;
+      t.y += u.y;
+      t.z += u.z;
+      t.w += u.w;
+    }
+    *reinterpret_cast<float4*>(V + (m0 + row) * rank + j) = t;
+    if (Vout)
+      *reinterpret_cast<uint2*>(Vout + (m0 + row) * rank + j) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+  }
+  __syncwarp();
+  cluster_sync();  // nobody reads this CTA's shared memory any more
+}
+
+// ---------------------------------------------------------------------------------------------------
+// y: 128 tokens x 128 columns a tile.  The tile's base arrives by TMA in the buffer that its result leaves
+// from; V of the 128 rows, scaled and split into bf16 pairs, stays in shared memory for all column tiles.
+// ---------------------------------------------------------------------------------------------------
+
+constexpr int TN = 128;
+constexpr int kYTile = TM * TN * 2;  // 32 KB: two boxes of 64 columns x 128 rows
+struct YPlan {
+  int rp, groups, nb, nu, u, off_u, off_y, off_list, off_bar, smem;
+};
+inline __host__ __device__ YPlan y_plan(int rank) {
+  YPlan p;
+  p.rp = round16(rank);
+  p.groups = (p.rp + 63) / 64;
+  const int v = 2 * p.groups * TM * 128;  // rounded values, then rests
+  p.u = p.rp * 256;                       // two boxes of 64 columns x rank rows
+  p.nu = p.rp <= 64 ? 4 : 2;
+  p.off_u = v;
+  p.off_y = v + p.nu * p.u;
+  p.nb = (kSmemMax - p.off_y - kListBytes - kBarBytes) / kYTile;
+  if (p.nb > 5) p.nb = 5;
+  p.off_list = p.off_y + p.nb * kYTile;
+  p.off_bar = p.off_list + kListBytes;
+  p.smem = p.off_bar + kBarBytes;
+  return p;
+}
+constexpr int kYMmaThreads = 192;  // warp 0 MMA, warp 1 TMA, warps 2-5 V and epilogue
+
+__global__ void __launch_bounds__(kYMmaThreads, 1)
+    lora_y_mma_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_base,
+                      const __grid_constant__ CUtensorMap tmap_y, const float* __restrict__ V,
+                      const int32_t* __restrict__ adapter, const float* __restrict__ scale, int has_base, int M, int N,
+                      int rank, int L, int nsplit, int* __restrict__ status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = align_smem(smem_raw);
+  const YPlan p = y_plan(rank);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / nsplit) * TM;
+  const int part = blockIdx.x % nsplit;
+  const int tiles = (N + TN - 1) / TN;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * part / nsplit);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / nsplit);
+  int* ids = reinterpret_cast<int*>(base + p.off_list);
+  int* list = ids + TM;
+  const uint32_t bars = smem_u32(base + p.off_bar);
+  auto y_full = [&](int s) { return bars + 8u * s; };
+  auto y_empty = [&](int s) { return bars + 40u + 8u * s; };
+  auto u_full = [&](int s) { return bars + 80u + 8u * s; };
+  auto u_empty = [&](int s) { return bars + 112u + 8u * s; };
+  auto acc_full = [&](int b) { return bars + 144u + 8u * b; };
+  auto acc_empty = [&](int b) { return bars + 160u + 8u * b; };
+  const uint32_t v_ready = bars + 176u;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 184);
+  volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 188);
+  int* counts = reinterpret_cast<int*>(base + p.off_bar + 192);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.nb; ++s) {
+      mbar_init(y_full(s), 1);
+      mbar_init(y_empty(s), 1);
+    }
+    for (int s = 0; s < p.nu; ++s) {
+      mbar_init(u_full(s), 1);
+      mbar_init(u_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 4);
+    }
+    mbar_init(v_ready, 128);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1 && lane == 0) {
+    prefetch_tmap(&tmap_u);
+    if (has_base) prefetch_tmap(&tmap_base);
+    prefetch_tmap(&tmap_y);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(slot), 2 * TN);
+    tmem_relinquish();
+  }
+  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- MMA issuer
+    bool ok = nd == 0 || mbar_wait(v_ready, 0, abort);
+    bool committed = false;
+    uint32_t last_bar = 0, last_ph = 0, ph = 0;
+    int s = 0, f = 0;  // f: products issued; accumulator f & 1
+    const uint32_t idesc = idesc_bf16(TM, TN, false, true);
+    for (int t = t0; ok && t < t1; ++t) {
+      for (int i = 0; i < nd; ++i, ++f) {
+        const int b = f & 1;
+        if (f >= 2 && !mbar_wait(acc_empty(b), ((f >> 1) - 1) & 1, abort)) { ok = false; break; }
+        if (!mbar_wait(u_full(s), ph, abort)) { ok = false; break; }
+        __syncwarp();
+        tc_fence_after();
+        const uint64_t du = sw128_mnmajor_desc(smem_u32(base + p.off_u + s * p.u), p.rp * 128);
+        for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
+          for (int kk = 0; kk < p.rp / 16; ++kk) {
+            const uint64_t dv = sw128_kmajor_desc(smem_u32(base + (h * p.groups + (kk >> 2)) * TM * 128)) + 2u * (kk & 3);
+            umma_f16_ss_lane0(tmem + static_cast<uint32_t>(b * TN), dv, du + 128u * kk, idesc, (h | kk) ? 1u : 0u, lane);
+          }
+        umma_commit_lane0(u_empty(s), lane);
+        umma_commit_lane0(acc_full(b), lane);
+        last_bar = u_empty(s);
+        last_ph = ph;
+        committed = true;
+        if (++s == p.nu) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) fail(abort, status);
+      volatile int never = 0;
+      if (committed) mbar_wait(last_bar, last_ph, &never);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int s = 0, f = 0, y = 0;
+      uint32_t ph = 0, yph = 0;
+      for (int t = t0; ok && t < t1; ++t) {
+        if (t - t0 >= p.nb && !mbar_wait(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
+        const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
+        if (has_base) {
+          mbar_arrive_expect_tx(y_full(y), kYTile);
+          tma_load_2d(dst, &tmap_base, t * TN, static_cast<int32_t>(m0), y_full(y));
+          tma_load_2d(dst + kYTile / 2, &tmap_base, t * TN + 64, static_cast<int32_t>(m0), y_full(y));
+        } else {
+          mbar_arrive(y_full(y));
+        }
+        if (++y == p.nb) { y = 0; yph ^= 1u; }
+        for (int i = 0; i < nd; ++i, ++f) {
+          if (f >= p.nu && !mbar_wait(u_empty(s), ph ^ 1u, abort)) { ok = false; break; }
+          const uint32_t ud = smem_u32(base + p.off_u + s * p.u);
+          mbar_arrive_expect_tx(u_full(s), p.u);
+          tma_load_3d(ud, &tmap_u, t * TN, 0, list[i], u_full(s));
+          tma_load_3d(ud + p.u / 2, &tmap_u, t * TN + 64, 0, list[i], u_full(s));
+          if (++s == p.nu) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {
+        fail(abort, status);
+        grace();
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- V, then the epilogue
+    const int q = warp & 3, row = 32 * q + lane;
+    const int tid = threadIdx.x - 64;
+    if (nd > 0) {
+      const int per = p.rp >> 2;
+      for (int i = tid; i < TM * per; i += 128) {
+        const int r = i / per, j = 4 * (i - r * per);
+        const int a = ids[r];
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (a >= 0 && j < rank) {
+          const float4 f = *reinterpret_cast<const float4*>(V + (m0 + r) * rank + j);
+          const float sc = __ldg(scale + a);
+          v[0] = f.x * sc;
+          v[1] = f.y * sc;
+          v[2] = f.z * sc;
+          v[3] = f.w * sc;
+        }
+        uint32_t hi[2], lo[2];
+        split_bf16(v[0], v[1], hi[0], lo[0]);
+        split_bf16(v[2], v[3], hi[1], lo[1]);
+        const int piece = ((j & 63) >> 3) ^ (r & 7);
+        uint8_t* d = base + (j >> 6) * TM * 128 + r * 128 + piece * 16 + (j & 4) * 2;
+        *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(d + p.groups * TM * 128) = make_uint2(lo[0], lo[1]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(v_ready);
+    }
+    const int mine = ids[row];
+    bool ok = true;
+    int y = 0, f = 0;
+    uint32_t yph = 0;
+    for (int t = t0; ok && t < t1; ++t) {
+      uint8_t* tile = base + p.off_y + y * kYTile + row * 128;
+      if (!mbar_wait_warp(y_full(y), yph, abort)) { ok = false; break; }
+      if (!has_base && mine < 0) {  // no adapter, no base: zeros
+        for (int c = 0; c < 16; ++c)
+          *reinterpret_cast<uint4*>(tile + (c >> 3) * (kYTile / 2) + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      }
+      for (int i = 0; i < nd; ++i, ++f) {
+        const int b = f & 1;
+        if (!mbar_wait_warp(acc_full(b), (f >> 1) & 1, abort)) { ok = false; break; }
+        tc_fence_after();
+        const bool hit = mine == list[i];
+        if (__any_sync(0xffffffffu, hit)) {
+#pragma unroll 1
+          for (int ch = 0; ch < TN / 32; ++ch) {
+            uint32_t r[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * TN + 32 * ch), r);
+            tmem_ld_wait();
+            if (hit) {
+              uint8_t* d = tile + (ch >> 1) * (kYTile / 2);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(d + ((((ch & 1) * 4 + c) ^ (row & 7)) << 4));
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * c + e]);
+                if (has_base) {
+                  float bv[8];
+                  widen8(*at, bv);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) v[e] += bv[e];
+                }
+                *at = narrow8(v);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(b));
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      named_bar_sync(1, 128);
+      if (tid == 0) {
+        const uint32_t src = smem_u32(base + p.off_y + y * kYTile);
+        tma_store_2d(&tmap_y, t * TN, static_cast<int32_t>(m0), src);
+        if (t * TN + 64 < N) tma_store_2d(&tmap_y, t * TN + 64, static_cast<int32_t>(m0), src + kYTile / 2);
+        bulk_commit_group();
+        // the tile before this one has left its buffer
+        bulk_wait_group_read<1>();
+        if (t > t0) mbar_arrive(y_empty(y ? y - 1 : p.nb - 1));
+      }
+      if (++y == p.nb) { y = 0; yph ^= 1u; }
+    }
+    if (tid == 0) bulk_wait_group<0>();
+    if (!ok) fail(abort, status);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * TN);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// grad: 256 columns of Z against all ranks of one adapter, summed over tiles of 64 tokens.  Z's columns are
+// the product's M side and V its N side, both as they lie in memory (MN-major).  Token tiles are split over
+// CTAs; the partial sums are joined by the finish kernel.
+// ---------------------------------------------------------------------------------------------------
+
+constexpr int GM = 64;           // tokens of a tile
+constexpr int GC = 256;          // columns of a CTA
+constexpr int kZBox = GM * 128;  // 64 tokens x 64 columns, 8 KB
+constexpr int kZTile = 4 * kZBox;
+constexpr int kRawTile = GM * GC;  // the tile's codes, 16 KB
+constexpr int kMaxGradTiles = 4096;  // token tiles of one CTA (the bits of its tile mask)
+struct GPlan {
+  int rp, groups, v, stage, stages, raws, off_raw, off_mask, off_bar, smem, cols;
+};
+inline __host__ __device__ GPlan g_plan(int rank, bool codes) {
+  GPlan p;
+  p.rp = round16(rank);
+  p.groups = (p.rp + 63) / 64;
+  p.v = 2 * p.groups * GM * 128;
+  p.stage = kZTile + p.v;
+  p.raws = codes ? 3 : 0;
+  const int rest = kSmemMax - kMaxGradTiles / 8 - kBarBytes - p.raws * kRawTile;
+  p.stages = rest / p.stage;
+  if (p.stages > 4) p.stages = 4;
+  p.off_raw = p.stages * p.stage;
+  p.off_mask = p.off_raw + p.raws * kRawTile;
+  p.off_bar = p.off_mask + kMaxGradTiles / 8;
+  p.smem = p.off_bar + kBarBytes;
+  p.cols = tmem_cols_for(2 * p.rp);
+  return p;
+}
+constexpr int kGThreads = 320;  // warps 0-7 operands and epilogue, warp 8 MMA, warp 9 TMA
+
+// Four signed bytes -> bf16 pairs, exactly: the low 7 bits put into the mantissa of 128, less 128, or less
+// 256 where the sign bit is set.
+__device__ __forceinline__ uint2 bytes_to_bf16(uint32_t w) {
+  uint2 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = __byte_perm(w, 0u, h ? 0x4342 : 0x4140);
+    const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, t = (x & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&t));
+    (h ? o.y : o.x) = *reinterpret_cast<const uint32_t*>(&d);
+  }
+  return o;
+}
+
+// kV16: V is bf16 (exact as it is: one product); else float32, as pairs.
+template <bool kCodes, bool kV16>
+__global__ void __launch_bounds__(kGThreads, 1)
+    lora_grad_mma_kernel(const __grid_constant__ CUtensorMap tmap_z, const float* __restrict__ code_scale,
+                         const float* __restrict__ V32, const uint16_t* __restrict__ V16,
+                         const int32_t* __restrict__ adapter, const float* __restrict__ scale, float* __restrict__ G,
+                         int M, int C, int rank, int L, int splits, int* __restrict__ status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = align_smem(smem_raw);
+  const GPlan p = g_plan(rank, kCodes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int colblocks = (C + GC - 1) / GC;
+  const int c0 = (blockIdx.x % colblocks) * GC;
+  const int a = blockIdx.x / colblocks % L;
+  const int split = blockIdx.x / colblocks / L;
+  const int tiles = (M + GM - 1) / GM;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(base + p.off_mask);
+  const uint32_t bars = smem_u32(base + p.off_bar);
+  auto z_full = [&](int s) { return bars + 8u * s; };         // TMA: the tile's Z or codes
+  auto raw_empty = [&](int s) { return bars + 32u + 8u * s; };  // codes: converted
+  auto ready = [&](int s) { return bars + 64u + 8u * s; };    // operands complete
+  auto empty = [&](int s) { return bars + 96u + 8u * s; };    // MMA has read them
+  const uint32_t acc_full = bars + 128u;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 136);
+  volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 140);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(z_full(s), 1);
+      mbar_init(raw_empty(s), 8);
+      mbar_init(ready(s), 8);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < kMaxGradTiles / 32; i += kGThreads) mask[i] = 0;
+  if (warp == 9 && lane == 0) prefetch_tmap(&tmap_z);
+  if (warp == 8) {
+    tmem_alloc(smem_u32(slot), p.cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // the token tiles of this CTA in which its adapter occurs
+  for (int t = t0 + warp; t < t1; t += kGThreads / 32) {
+    bool any = !adapter;
+    if (adapter) {
+      const int64_t m = static_cast<int64_t>(t) * GM + lane;
+      const bool h0 = m < M && row_adapter(adapter, m, L) == a;
+      const bool h1 = m + 32 < M && row_adapter(adapter, m + 32, L) == a;
+      any = __any_sync(0xffffffffu, h0 || h1);
+    } else {
+      any = a == 0;
+    }
+    if (any && lane == 0) atomicOr(&mask[(t - t0) >> 5], 1u << ((t - t0) & 31));
+  }
+  __syncthreads();
+  const uint32_t tmem = *slot;
+  const int nt = t1 - t0;
+  // first marked tile at or after i (relative to t0), nt if none
+  auto next_tile = [&](int i) {
+    while (i < nt) {
+      const uint32_t w = mask[i >> 5] >> (i & 31);
+      if (w) {
+        i += __ffs(w) - 1;
+        return i < nt ? i : nt;
+      }
+      i = (i | 31) + 1;
+    }
+    return nt;
+  };
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- MMA issuer
+    bool ok = true, committed = false;
+    uint32_t ph = 0, last_bar = 0, last_ph = 0;
+    int s = 0;
+    const uint32_t idesc = idesc_bf16(128, p.rp, true, true);
+    for (int i = next_tile(0); i < nt; i = next_tile(i + 1)) {
+      if (!mbar_wait(ready(s), ph, abort)) { ok = false; break; }
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t z = smem_u32(base + s * p.stage);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kZBox, kZBox);
+        for (int h = 0; h < (kV16 ? 1 : 2); ++h) {
+          const uint64_t dv = sw128_mnmajor_desc(z + kZTile + h * p.groups * GM * 128, GM * 128);
+#pragma unroll
+          for (int kk = 0; kk < GM / 16; ++kk)
+            umma_f16_ss_lane0(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 128u * kk, idesc,
+                              (committed || h || kk) ? 1u : 0u, lane);
+        }
+      }
+      umma_commit_lane0(empty(s), lane);
+      last_bar = empty(s);
+      last_ph = ph;
+      committed = true;
+      if (++s == p.stages) { s = 0; ph ^= 1u; }
+    }
+    if (ok) umma_commit_lane0(acc_full, lane);
+    if (!ok) {
+      if (lane == 0) fail(abort, status);
+      volatile int never = 0;
+      if (committed) mbar_wait(last_bar, last_ph, &never);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int s = 0, f = 0;
+      uint32_t ph = 0;
+      const int ring = kCodes ? p.raws : p.stages;
+      for (int i = next_tile(0); i < nt; i = next_tile(i + 1), ++f) {
+        if (f >= ring && !mbar_wait(kCodes ? raw_empty(s) : empty(s), ph ^ 1u, abort)) { ok = false; break; }
+        const int y = (t0 + i) * GM;
+        if constexpr (kCodes) {
+          mbar_arrive_expect_tx(z_full(s), kRawTile);
+          tma_load_2d(smem_u32(base + p.off_raw + s * kRawTile), &tmap_z, c0, y, z_full(s));
+        } else {
+          const uint32_t z = smem_u32(base + s * p.stage);
+          mbar_arrive_expect_tx(z_full(s), kZTile);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tma_load_2d(z + b * kZBox, &tmap_z, c0 + 64 * b, y, z_full(s));
+        }
+        if (++s == ring) { s = 0; ph ^= 1u; }
+      }
+      if (!ok) {
+        fail(abort, status);
+        grace();
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- operands (8 warps)
+    const int tid = threadIdx.x;
+    const int per = p.rp >> 2;  // groups of four ranks of a row
+    constexpr int kMost = GM * (kMaxRank / 4) / 256;  // of a thread
+    const int n = GM * per / 256;                     // per >= 4: a whole number of passes
+    bool ok = true;
+    int s = 0, rs = 0;
+    uint32_t ph = 0, rph = 0;
+    int f = 0;
+    float4 v[kMost];   // the next tile's V, on its way (bf16: bits in x, y)
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k >= n) continue;
+        const int e = tid + 256 * k;
+        const int r = e / per, j = 4 * (e - r * per);
+        const int64_t m = static_cast<int64_t>(t0 + i) * GM + r;
+        if (m < M && j < rank && row_adapter(adapter, m, L) == a) {
+          if constexpr (kV16) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(V16 + m * rank + j));
+            v[k].x = __uint_as_float(w.x);
+            v[k].y = __uint_as_float(w.y);
+          } else {
+            v[k] = *reinterpret_cast<const float4*>(V32 + m * rank + j);
+            if constexpr (kCodes) {
+              const float cs = __ldg(code_scale + m * (C >> 8) + (c0 >> 8));
+              v[k].x *= cs;
+              v[k].y *= cs;
+              v[k].z *= cs;
+              v[k].w *= cs;
+            }
+          }
+        }
+      }
+    };
+    int i = next_tile(0);
+    if (i < nt) fetch(i);
+    while (i < nt) {
+      uint8_t* z = base + s * p.stage;
+      uint8_t* vt = z + kZTile;
+      if constexpr (kCodes) {
+        if (f >= p.stages && !mbar_wait_warp(empty(s), ph ^ 1u, abort)) { ok = false; break; }
+        if (!mbar_wait_warp(z_full(rs), rph, abort)) { ok = false; break; }
+        const uint8_t* raw = base + p.off_raw + rs * kRawTile;
+#pragma unroll
+        for (int k = 0; k < GM / 8; ++k) {  // a row of the tile for each warp
+          const int r = 8 * k + warp;
+          const int64_t m = static_cast<int64_t>(t0 + i) * GM + r;
+          const uint2 w = *reinterpret_cast<const uint2*>(raw + r * GC + 8 * lane);
+          const uint2 lo = bytes_to_bf16(w.x), hi = bytes_to_bf16(w.y);
+          *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
+              make_uint4(lo.x, lo.y, hi.x, hi.y);
+          (void)m;  // codes are finite: rows of other adapters meet zeros of V
+        }
+      } else {
+        if (!mbar_wait_warp(z_full(s), ph, abort)) { ok = false; break; }
+        if (adapter) {
+#pragma unroll 1
+          for (int k = 0; k < GM / 8; ++k) {
+            const int r = 8 * k + warp;
+            const int64_t m = static_cast<int64_t>(t0 + i) * GM + r;
+            if (m < M && row_adapter(adapter, m, L) != a)
+              *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        if (k >= n) continue;
+        const int e = tid + 256 * k;
+        const int r = e / per, j = 4 * (e - r * per);
+        uint8_t* d = vt + (j >> 6) * GM * 128 + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 4) * 2;
+        if constexpr (kV16) {
+          *reinterpret_cast<uint2*>(d) = make_uint2(__float_as_uint(v[k].x), __float_as_uint(v[k].y));
+        } else {
+          uint32_t hi[2], lo[2];
+          split_bf16(v[k].x, v[k].y, hi[0], lo[0]);
+          split_bf16(v[k].z, v[k].w, hi[1], lo[1]);
+          *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(d + p.groups * GM * 128) = make_uint2(lo[0], lo[1]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ready(s));
+        if (kCodes) mbar_arrive(raw_empty(rs));
+      }
+      i = next_tile(i + 1);
+      if (i < nt) fetch(i);
+      ++f;
+      if (++s == p.stages) { s = 0; ph ^= 1u; }
+      if (kCodes && ++rs == p.raws) { rs = 0; rph ^= 1u; }
+    }
+    // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
+    const int q = warp & 3, half = warp >> 2;
+    const int c = c0 + 128 * half + 32 * q + lane;
+    const float sc = __ldg(scale + a);
+    float* out = G + (static_cast<int64_t>(split) * L + a) * rank * C + c;
+    if (ok && f > 0) {
+      if (mbar_wait_warp(acc_full, 0, abort)) {
+        tc_fence_after();
+        for (int j = 0; j < p.rp; j += 16) {
+          uint32_t r[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * p.rp + j), r);
+          tmem_ld_wait();
+          if (c < C) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (j + e < rank) out[static_cast<int64_t>(j + e) * C] = sc * __uint_as_float(r[e]);
+          }
+        }
+      } else {
+        ok = false;
+      }
+    } else if (c < C) {
+      for (int j = 0; j < rank; ++j) out[static_cast<int64_t>(j) * C] = 0.f;
+    }
+    if (!ok) fail(abort, status);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.cols);
+  }
+}
+
+std::atomic<bool> g_attr_done[64];
+
+bool set_attrs() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (g_attr_done[dev].load()) return true;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const int most = kSmemMax + 1024;
+  if (cudaFuncSetAttribute(lora_v_mma_kernel, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_y_mma_kernel, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false, false>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false, true>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true, false>, attr, most) != cudaSuccess)
+    return false;
+  g_attr_done[dev].store(true);
+  return true;
+}
+
+const auto kBf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+const auto kSw128 = CU_TENSOR_MAP_SWIZZLE_128B;
+const auto kL2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+
+}  // namespace
+
+int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, float* V,
+                      uint16_t* Vout, int M, int K, int rank, int L, int* status, int num_sms, cudaStream_t stream) {
+  if (!set_attrs()) return CR_ERR_CUDA;
+  const VPlan p = v_plan(rank, L);
+  CUtensorMap tx, ta;
+  if (!make_tmap_2d(&tx, kBf, X, M, K, static_cast<uint64_t>(ldx) * 2, KB, TM, kSw128, kL2) ||
+      !make_tmap_3d(&ta, kBf, down, L, rank, K, static_cast<uint64_t>(K) * 2, KB, p.rp, kSw128, kL2))
+    return CR_ERR_CUDA;
+  const int64_t tiles = (static_cast<int64_t>(M) + TM - 1) / TM;
+  const int nkb = (K + KB - 1) / KB;
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= num_sms && nkb >= 4 * splits) splits *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), 1, 1);
+  cfg.blockDim = dim3(kVThreads, 1, 1);
+  cfg.dynamicSmemBytes = p.smem + 1024;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_v_mma_kernel, tx, ta, adapter, V, Vout, M, K, rank, L, splits, status) ==
+                 cudaSuccess
+             ? CR_OK
+             : CR_ERR_CUDA;
+}
+
+int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up, const float* scale,
+                      const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, int M, int N, int rank, int L,
+                      int* status, int num_sms, cudaStream_t stream) {
+  if (!set_attrs()) return CR_ERR_CUDA;
+  const YPlan p = y_plan(rank);
+  CUtensorMap tu, tb, ty;
+  memset(&tb, 0, sizeof(tb));
+  if (!make_tmap_3d(&tu, kBf, up, L, rank, N, static_cast<uint64_t>(N) * 2, 64, p.rp, kSw128, kL2) ||
+      !make_tmap_2d(&ty, kBf, Y, M, N, static_cast<uint64_t>(ldy) * 2, 64, TM, kSw128, CU_TENSOR_MAP_L2_PROMOTION_NONE) ||
+      (base && !make_tmap_2d(&tb, kBf, base, M, N, static_cast<uint64_t>(ldb) * 2, 64, TM, kSw128, kL2)))
+    return CR_ERR_CUDA;
+  const int64_t tiles_m = (static_cast<int64_t>(M) + TM - 1) / TM;
+  const int tiles_n = (N + TN - 1) / TN;
+  // column parts of a token tile: the fewest rounds of (column tiles + about two tiles' worth of prologue)
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= tiles_n && s <= 4 * num_sms; ++s) {
+    const int64_t cost = (tiles_m * s + num_sms - 1) / num_sms * ((tiles_n + s - 1) / s + 2);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  lora_y_mma_kernel<<<static_cast<unsigned>(tiles_m * best), kYMmaThreads, p.smem + 1024, stream>>>(
+      tu, tb, ty, V, adapter, scale, base != nullptr, M, N, rank, L, best, status);
+  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+}
+
+int lora_grad_splits(int M, int C, int L, int num_sms) {
+  const int64_t items = static_cast<int64_t>((C + GC - 1) / GC) * L;
+  const int tiles = (M + GM - 1) / GM;
+  int64_t s = num_sms / items;
+  if (s > (tiles + 3) / 4) s = (tiles + 3) / 4;
+  const int least = (tiles + kMaxGradTiles - 1) / kMaxGradTiles;
+  if (s < least) s = least;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+int launch_lora_grad_mma(const void* Z, int64_t ldz, const float* code_scale, const float* V32, const uint16_t* V16,
+                         const int32_t* adapter, const float* scale, float* G, int M, int C, int rank, int L,
+                         int splits, int* status, cudaStream_t stream) {
+  if (!set_attrs()) return CR_ERR_CUDA;
+  const bool codes = code_scale != nullptr;
+  const GPlan p = g_plan(rank, codes);
+  CUtensorMap tz;
+  const bool made = codes ? make_tmap_2d(&tz, CU_TENSOR_MAP_DATA_TYPE_UINT8, Z, M, C, C, GC, GM,
+                                         CU_TENSOR_MAP_SWIZZLE_NONE, kL2)
+                          : make_tmap_2d(&tz, kBf, Z, M, C, static_cast<uint64_t>(ldz) * 2, 64, GM, kSw128, kL2);
+  if (!made) return CR_ERR_CUDA;
+  const int64_t blocks = static_cast<int64_t>((C + GC - 1) / GC) * L * splits;
+  auto kern = codes ? lora_grad_mma_kernel<true, false> : V16 ? lora_grad_mma_kernel<false, true>
+                                                              : lora_grad_mma_kernel<false, false>;
+  kern<<<static_cast<unsigned>(blocks), kGThreads, p.smem + 1024, stream>>>(tz, code_scale, V32, V16, adapter, scale, G,
+                                                                            M, C, rank, L, splits, status);
+  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+}
+
+}  // namespace cr

@@ -110,40 +110,6 @@ __global__ void __launch_bounds__(kYThreads)
   *reinterpret_cast<uint4*>(Y + m * ldy + n) = narrow8(y);
 }
 
-// Adapter gradients, G[a][j, c] = s[a] sum over the rows m of adapter a of V[m, j] Z[m, c], in float32:
-// one thread for each column and 16 ranks.  Z is bf16 rows or 8-bit checkpoint codes (then in the
-// checkpoint's rotated basis).
-template <bool kCodes>
-__global__ void __launch_bounds__(128)
-    lora_grad_rows_kernel(const void* __restrict__ Z, int64_t ldz, const float* __restrict__ code_scale,
-                          const float* __restrict__ V32, const uint16_t* __restrict__ V16, int splits,
-                          const int32_t* __restrict__ adapter, const float* __restrict__ scale,
-                          float* __restrict__ G, int M, int C, int rank, int L) {
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  const int a = blockIdx.y;
-  const int j0 = 16 * blockIdx.z;
-  float acc[16] = {};
-  for (int64_t m = 0; m < M; ++m) {
-    if (row_adapter(adapter, m, L) != a || c >= C) continue;
-    float z;
-    if constexpr (kCodes)
-      z = static_cast<float>(static_cast<const int8_t*>(Z)[m * C + c]) * code_scale[m * (C >> 8) + (c >> 8)];
-    else
-      z = bf16_float(static_cast<const uint16_t*>(Z)[m * ldz + c]);
-    for (int i = 0; i < 16 && j0 + i < rank; ++i) {
-      float v = 0.f;
-      if (V16)
-        v = bf16_float(V16[m * rank + j0 + i]);
-      else
-        for (int sp = 0; sp < splits; ++sp) v += V32[(static_cast<int64_t>(sp) * M + m) * rank + j0 + i];
-      acc[i] = fmaf(v, z, acc[i]);
-    }
-  }
-  if (c >= C) return;
-  const float s = scale[a];
-  for (int i = 0; i < 16 && j0 + i < rank; ++i) G[(static_cast<int64_t>(a) * rank + j0 + i) * C + c] = s * acc[i];
-}
-
 }  // namespace
 
 int lora_row_splits(int M, int K, int rank, int num_sms) {
@@ -168,19 +134,6 @@ cudaError_t launch_lora_y_rows(const float* V, int splits, const int32_t* adapte
   const dim3 grid(static_cast<unsigned>(M), static_cast<unsigned>((N + 8 * kYThreads - 1) / (8 * kYThreads)));
   lora_y_rows_kernel<<<grid, kYThreads, 0, stream>>>(V, splits, adapter, up, scale, base, ldb, Y, ldy, Vout, M, N,
                                                      rank, L);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_lora_grad_rows(const void* Z, int64_t ldz, const float* code_scale, const float* V32,
-                                  const uint16_t* V16, int splits, const int32_t* adapter, const float* scale, float* G,
-                                  int M, int C, int rank, int L, cudaStream_t stream) {
-  const dim3 grid((C + 127) / 128, L, (rank + 15) / 16);
-  if (code_scale)
-    lora_grad_rows_kernel<true><<<grid, 128, 0, stream>>>(Z, ldz, code_scale, V32, V16, splits, adapter, scale, G, M, C,
-                                                          rank, L);
-  else
-    lora_grad_rows_kernel<false><<<grid, 128, 0, stream>>>(Z, ldz, code_scale, V32, V16, splits, adapter, scale, G, M,
-                                                           C, rank, L);
   return cudaGetLastError();
 }
 
