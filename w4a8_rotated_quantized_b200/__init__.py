@@ -33,5 +33,6 @@ def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
 
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found directly from now on
+        return value
     raise AttributeError(name)

@@ -673,67 +673,78 @@ def cr_selftest_wait_timeout(ws: torch.Tensor) -> None:
 # read with ``cr_read_device_status(ws=...)``.
 # ---------------------------------------------------------------------------
 
-class _on:
-    """Makes ``device`` current for the library call where it is not already."""
-
-    def __init__(self, device: torch.device):
-        self.to = device.index
-        self.back = None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.to:
-            torch.cuda.set_device(self.to)
-            self.back = now
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _run(name: str, dev: torch.device, *args) -> None:
+    """The library call on the current stream of ``dev``, with that device current."""
+    i = dev.index
+    if torch._C._cuda_getDevice() == i:
+        st = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != CR_OK:
+        raise ConvRotError(name, st)
 
 
-def _scratch(given: Optional[torch.Tensor], nbytes: int, device: torch.device) -> torch.Tensor:
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> Tuple[int, int, torch.Tensor]:
+    """(address, bytes, tensor) of the workspace; a bf16 buffer like ``like`` if none is given."""
     if given is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _dev(given, "workspace", torch.uint8, device)
+        given = like.new_empty((nbytes + 1) // 2)
+        return given.data_ptr(), nbytes, given
+    _dev(given, "workspace", torch.uint8, like.device)
     if given.dim() != 1 or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous 1-D uint8 tensor")
-    return given
+    return given.data_ptr(), given.numel(), given
+
+
+def _input(t: torch.Tensor, name: str) -> Tuple[int, int, int, torch.device]:
+    """The call's first operand, bf16 [M, C] on a CUDA device with dense columns: M, C, row stride, device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    M, C = t.shape
+    return M, C, _matrix(t, name, t.device, M, C), t.device
 
 
 def _matrix(t: torch.Tensor, name: str, device: torch.device, M: int, C: int) -> int:
     """A bf16 [M, C] matrix with dense columns; returns its row stride."""
-    _dev(t, name, torch.bfloat16, device)
-    if tuple(t.shape) != (M, C):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device:
+        raise TypeError(f"{name} must be a bfloat16 tensor on {device}")
+    if t.shape != (M, C):
         raise ValueError(f"{name} must have shape {(M, C)}, got {tuple(t.shape)}")
-    if M <= 1 or C == 0:  # the stride of a single row or of an empty tensor says nothing
-        if M == 1 and C > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have unit stride along the last dimension")
-        return C
-    return _rows(t, name)[2]
+    ld, unit = t.stride()
+    if C > 1 and M > 0 and unit != 1:
+        raise ValueError(f"{name} must have unit stride along the last dimension")
+    return C if M <= 1 or C == 0 else ld  # the stride of a single row or of an empty tensor says nothing
 
 
-def _out_matrix(out: Optional[torch.Tensor], name: str, device: torch.device, M: int, C: int) -> Tuple[torch.Tensor, int]:
+def _out_matrix(out: Optional[torch.Tensor], like: torch.Tensor, M: int, C: int) -> Tuple[torch.Tensor, int]:
     if out is None:
-        return torch.empty((M, C), dtype=torch.bfloat16, device=device), C
-    return out, _matrix(out, name, device, M, C)
+        return like.new_empty((M, C)), C
+    return out, _matrix(out, "out", like.device, M, C)
 
 
-def _adapters(adapter: Optional[torch.Tensor], down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor, M: int,
-              N: Optional[int], K: Optional[int], device: torch.device) -> Tuple[int, int, int, int]:
-    """The pool's factors down [L, r, K] and up [L, r, N], its scales [L] and the rows' adapters [M]."""
+def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: Tuple[int, ...]) -> int:
+    """The address of a contiguous tensor of exactly this shape, dtype and device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
+        _dense(t, name, dtype, device, shape)  # says what is wrong
+    return t.data_ptr()
+
+
+def _pool(down: torch.Tensor, up: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(adapters, rank, K, N) of the factors down [L, r, K] and up [L, r, N]."""
     for t, name in ((down, "down"), (up, "up")):
-        _dev(t, name, torch.bfloat16, device)
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
         if t.dim() != 3:
             raise ValueError(f"{name} must be 3-D [adapters, rank, columns]")
-    L, r = down.shape[0], down.shape[1]
-    K = down.shape[2] if K is None else K
-    N = up.shape[2] if N is None else N
-    _dense(down, "down", torch.bfloat16, device, (L, r, K))
-    _dense(up, "up", torch.bfloat16, device, (L, r, N))
-    _vec(scale, "scale", torch.float32, device, L)
-    if adapter is not None:
-        _vec(adapter, "adapter", torch.int32, device, M)
-    return L, r, N, K
+    L, r, K = down.shape
+    return L, r, K, up.shape[2]
 
 
 def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
@@ -746,26 +757,19 @@ def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale
     row uses adapter 0; without ``base`` the sum starts at zero.  ``out`` may be ``base`` itself.  With
     ``save_v`` returns (Y, V), V bf16 [M, r] = X down[a]^T for the backward pass.
     """
-    _bf16_cuda(X, "X")
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D [M, K]")
-    dev = X.device
-    M, K = X.shape
-    ldx = _matrix(X, "X", dev, M, K)
-    L, r, N, _ = _adapters(adapter, down, up, scale, M, None, K, dev)
+    M, K, ldx, dev = _input(X, "X")
+    L, r, _, N = _pool(down, up)
+    p_down = _exact(down, "down", torch.bfloat16, dev, (L, r, K))
+    p_up = _exact(up, "up", torch.bfloat16, dev, (L, r, N))
+    p_scale = _exact(scale, "scale", torch.float32, dev, (L,))
+    p_adapter = None if adapter is None else _exact(adapter, "adapter", torch.int32, dev, (M,))
     ldb = 0 if base is None else _matrix(base, "base", dev, M, N)
-    with _on(dev):
-        Y, ldy = _out_matrix(out, "out", dev, M, N)
-        V = torch.empty((M, r), dtype=torch.bfloat16, device=dev) if save_v else None
-        ws = _scratch(workspace, _lib.cr_lora_forward_workspace_size(M, N, K, r, L), dev)
-        _check("cr_lora_forward", _lib.cr_lora_forward(
-            X.data_ptr(), ldx, _addr(adapter), down.data_ptr(), up.data_ptr(), scale.data_ptr(), _addr(base), ldb,
-            Y.data_ptr(), ldy, _addr(V), M, N, K, r, L, ws.data_ptr(), ws.numel(), _stream(dev)))
+    Y, ldy = _out_matrix(out, X, M, N)
+    V = X.new_empty((M, r)) if save_v else None
+    ws, nws, keep = _scratch(workspace, _lib.cr_lora_forward_workspace_size(M, N, K, r, L), X)
+    _run("cr_lora_forward", dev, X.data_ptr(), ldx, p_adapter, p_down, p_up, p_scale, _addr(base), ldb, Y.data_ptr(), ldy,
+         _addr(V), M, N, K, r, L, ws, nws)
     return (Y, V) if save_v else Y
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch.Tensor, up: torch.Tensor,
@@ -778,57 +782,45 @@ def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch
     needed); ``V`` is what the forward kept (None if d_up is not needed).  dX starts at ``base`` (the
     projection's own input gradient; zero without it); ``out`` takes dX and may be ``base`` itself.
     """
-    _bf16_cuda(dY, "dY")
-    if dY.dim() != 2:
-        raise ValueError("dY must be 2-D [M, N]")
-    dev = dY.device
-    M, N = dY.shape
-    lddy = _matrix(dY, "dY", dev, M, N)
-    L, r, _, K = _adapters(adapter, down, up, scale, M, N, None, dev)
+    M, N, lddy, dev = _input(dY, "dY")
+    L, r, K, _ = _pool(down, up)
+    p_down = _exact(down, "down", torch.bfloat16, dev, (L, r, K))
+    p_up = _exact(up, "up", torch.bfloat16, dev, (L, r, N))
+    p_scale = _exact(scale, "scale", torch.float32, dev, (L,))
+    p_adapter = None if adapter is None else _exact(adapter, "adapter", torch.int32, dev, (M,))
     if need_down and X is None:
         raise ValueError("X (or its checkpoint) is needed for d_down")
     if need_up and V is None:
         raise ValueError("V is needed for d_up")
-    x = codes = code_scales = None
+    p_x = p_codes = p_scales = None
     ldx = 0
     if isinstance(X, (tuple, list)):
         if len(X) != 2:
             raise ValueError("a checkpoint is (codes, scales)")
-        codes, code_scales = X
-        _dense(codes, "codes", torch.int8, dev, (M, K))
-        _dense(code_scales, "scales", torch.float32, dev, (M, K // 256))
+        p_codes = _exact(X[0], "codes", torch.int8, dev, (M, K))
+        p_scales = _exact(X[1], "scales", torch.float32, dev, (M, K // 256))
     elif X is not None:
-        x, ldx = X, _matrix(X, "X", dev, M, K)
-    if V is not None:
-        _dense(V, "V", torch.bfloat16, dev, (M, r))
+        ldx = _matrix(X, "X", dev, M, K)
+        p_x = X.data_ptr()
+    p_v = None if V is None else _exact(V, "V", torch.bfloat16, dev, (M, r))
     ldb = 0 if base is None else _matrix(base, "base", dev, M, K)
     if out is not None and not need_dx:
         raise ValueError("out takes dX, which is not needed")
-    with _on(dev):
-        dX, lddx = _out_matrix(out, "out", dev, M, K) if need_dx else (None, 0)
-        dd = torch.empty_like(down) if need_down else None
-        du = torch.empty_like(up) if need_up else None
-        ws = _scratch(workspace, _lib.cr_lora_backward_workspace_size(M, N, K, r, L), dev)
-        _check("cr_lora_backward", _lib.cr_lora_backward(
-            dY.data_ptr(), lddy, _addr(x), ldx, _addr(codes), _addr(code_scales), _addr(V), _addr(adapter),
-            down.data_ptr(), up.data_ptr(), scale.data_ptr(), _addr(base), ldb, _addr(dX), lddx, _addr(dd), _addr(du),
-            M, N, K, r, L, ws.data_ptr(), ws.numel(), _stream(dev)))
+    dX, lddx = _out_matrix(out, dY, M, K) if need_dx else (None, 0)
+    dd = dY.new_empty((L, r, K)) if need_down else None
+    du = dY.new_empty((L, r, N)) if need_up else None
+    ws, nws, keep = _scratch(workspace, _lib.cr_lora_backward_workspace_size(M, N, K, r, L), dY)
+    _run("cr_lora_backward", dev, dY.data_ptr(), lddy, p_x, ldx, p_codes, p_scales, p_v, p_adapter, p_down, p_up, p_scale,
+         _addr(base), ldb, _addr(dX), lddx, _addr(dd), _addr(du), M, N, K, r, L, ws, nws)
     return dX, dd, du
 
 
 def cr_ckpt_save(X: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """X bf16 [M, K] in 8 bits: (codes int8 [M, K] of the rotated rows, scales float32 [M, K/256])."""
-    _bf16_cuda(X, "X")
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D [M, K]")
-    dev = X.device
-    M, K = X.shape
-    ldx = _matrix(X, "X", dev, M, K)
-    with _on(dev):
-        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
-        scales = torch.empty((M, K // 256), dtype=torch.float32, device=dev)
-        _check("cr_ckpt_save", _lib.cr_ckpt_save(X.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr(),
-                                                 _stream(dev)))
+    M, K, ldx, dev = _input(X, "X")
+    codes = X.new_empty((M, K), dtype=torch.int8)
+    scales = X.new_empty((M, K // 256), dtype=torch.float32)
+    _run("cr_ckpt_save", dev, X.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -837,11 +829,12 @@ def cr_ckpt_load(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.
     M, K = _codes(codes, "codes", torch.int8)
     _cuda(codes, "codes")
     dev = codes.device
-    _dense(scales, "scales", torch.float32, dev, (M, K // 256))
-    with _on(dev):
-        X, ldx = _out_matrix(out, "out", dev, M, K)
-        _check("cr_ckpt_load", _lib.cr_ckpt_load(codes.data_ptr(), scales.data_ptr(), M, K, X.data_ptr(), ldx,
-                                                 _stream(dev)))
+    p_scales = _exact(scales, "scales", torch.float32, dev, (M, K // 256))
+    if out is None:
+        X, ldx = codes.new_empty((M, K), dtype=torch.bfloat16), K
+    else:
+        X, ldx = out, _matrix(out, "out", dev, M, K)
+    _run("cr_ckpt_load", dev, codes.data_ptr(), p_scales, M, K, X.data_ptr(), ldx)
     return X
 
 
@@ -849,22 +842,13 @@ def cr_w4a4_grad_input(dY: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor
                        out: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Input gradient of the W4A4 layer with frozen weights: dX bf16 [M, K] = dY [M, N] . (w_scale * Wq H_group)."""
-    _bf16_cuda(dY, "dY")
-    if dY.dim() != 2:
-        raise ValueError("dY must be 2-D [M, N]")
-    dev = dY.device
-    M, N = dY.shape
-    lddy = _matrix(dY, "dY", dev, M, N)
-    _dev(Wq, "Wq", torch.uint8, dev)
-    if Wq.dim() != 2:
-        raise ValueError("Wq must be 2-D [N, K/2]")
+    M, N, lddy, dev = _input(dY, "dY")
+    if not isinstance(Wq, torch.Tensor) or Wq.dim() != 2:
+        raise TypeError("Wq must be a 2-D tensor [N, K/2]")
     K = 2 * Wq.shape[1]
-    _dense(Wq, "Wq", torch.uint8, dev, (N, K // 2))
-    _vec(w_scale, "w_scale", torch.float32, dev, N)
-    with _on(dev):
-        dX, lddx = _out_matrix(out, "out", dev, M, K)
-        ws = _scratch(workspace, _lib.cr_w4a4_grad_input_workspace_size(M, N, K, group), dev)
-        _check("cr_w4a4_grad_input", _lib.cr_w4a4_grad_input(
-            dY.data_ptr(), lddy, Wq.data_ptr(), w_scale.data_ptr(), dX.data_ptr(), lddx, M, N, K, group, ws.data_ptr(),
-            ws.numel(), _stream(dev)))
+    p_w = _exact(Wq, "Wq", torch.uint8, dev, (N, K // 2))
+    p_s = _exact(w_scale, "w_scale", torch.float32, dev, (N,))
+    dX, lddx = _out_matrix(out, dY, M, K)
+    ws, nws, keep = _scratch(workspace, _lib.cr_w4a4_grad_input_workspace_size(M, N, K, group), dY)
+    _run("cr_w4a4_grad_input", dev, dY.data_ptr(), lddy, p_w, p_s, dX.data_ptr(), lddx, M, N, K, group, ws, nws)
     return dX
