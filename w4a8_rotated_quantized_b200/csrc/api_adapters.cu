@@ -27,8 +27,9 @@ constexpr size_t kWsHead = 256;
 
 inline size_t bytes_f32(int64_t n) { return cr::round_up(static_cast<size_t>(n) * 4, 256); }
 
-// Sizes are sized for the SM count of a B200 whatever device is current, so that the size calls need none.
-constexpr int kSizingSms = 160;
+// Splits, and with them the workspace, go by a B200's SM count whatever device is current: the size calls ask
+// none, and the same call gives the same bits everywhere.
+constexpr int kSizingSms = 148;
 
 bool sizes_ok(int M, int N, int K, int rank, int L) {
   return M >= 0 && N >= 8 && N % 8 == 0 && N <= CR_MAX_K && K >= 8 && K % 8 == 0 && K <= CR_MAX_K && rank >= 4 &&
@@ -36,12 +37,12 @@ bool sizes_ok(int M, int N, int K, int rank, int L) {
 }
 
 // Row-form V holds a partial sum for each K split, the tensor-core form one array.
-int v_splits(int M, int K, int rank, int num_sms) {
-  return M <= cr::kLoraRowsMaxM ? cr::lora_row_splits(M > 0 ? M : 1, K, rank, num_sms) : 1;
+int v_splits(int M, int K, int rank) {
+  return M <= cr::kLoraRowsMaxM ? cr::lora_row_splits(M > 0 ? M : 1, K, rank, kSizingSms) : 1;
 }
 
-size_t grad_bytes(int M, int C, int rank, int L) {
-  return bytes_f32(static_cast<int64_t>(cr::lora_grad_splits(M > 0 ? M : 1, C, L, kSizingSms)) * L * rank * C);
+int grad_splits(int M, int N, int K, int rank, int L) {
+  return cr::lora_grad_splits(M > 0 ? M : 1, K, N, rank, L, kSizingSms);
 }
 
 cr_status check_rows(const void* p, int64_t ld, int cols) {
@@ -55,7 +56,7 @@ extern "C" {
 
 size_t cr_lora_forward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank * v_splits(M, K, rank, kSizingSms));
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank * v_splits(M, K, rank));
 }
 
 cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, const void* down, const void* up,
@@ -80,7 +81,6 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if (M == 0) return CR_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead);
-  if (nsm > kSizingSms) nsm = kSizingSms;
   uint16_t* vout = static_cast<uint16_t*>(V);
   int* status = ws_status(workspace);
   const uint16_t* x = static_cast<const uint16_t*>(X);
@@ -90,7 +90,7 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   uint16_t* y = static_cast<uint16_t*>(Y);
   const int L = num_adapters;
   if (M <= cr::kLoraRowsMaxM) {
-    const int splits = v_splits(M, K, rank, nsm);
+    const int splits = v_splits(M, K, rank);
     cudaError_t e = cr::launch_lora_v_rows(x, ldx, adapter, dn, v, M, K, rank, L, splits, status, s);
     if (e == cudaSuccess)
       e = cr::launch_lora_y_rows(v, splits, adapter, u, scale, b, ldb, y, ldy, vout, M, N, rank, L, s);
@@ -103,7 +103,8 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
 
 size_t cr_lora_backward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + grad_bytes(M, K, rank, num_adapters) + grad_bytes(M, N, rank, num_adapters);
+  const int64_t per = static_cast<int64_t>(grad_splits(M, N, K, rank, num_adapters)) * num_adapters * rank;
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + bytes_f32(per * K) + bytes_f32(per * N);
 }
 
 cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* codes,
@@ -141,9 +142,9 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   }
   uint8_t* w = static_cast<uint8_t*>(workspace) + kWsHead;
   float* dv = reinterpret_cast<float*>(w);
+  const int parts = grad_splits(M, N, K, rank, L);
   float* gd = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank));
-  float* gu = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank) + grad_bytes(M, K, rank, L));
-  if (nsm > kSizingSms) nsm = kSizingSms;
+  float* gu = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(gd) + bytes_f32(parts * nd));
   int* status = ws_status(workspace);
   if (dX || d_down) {
     st = static_cast<cr_status>(cr::launch_lora_v_mma(static_cast<const uint16_t*>(dY), lddy, adapter,
@@ -159,21 +160,13 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
                                                       static_cast<uint16_t*>(dX), lddx, M, K, rank, L, status, nsm, s));
     if (st != CR_OK) return st;
   }
-  if (d_down) {
-    const int parts = cr::lora_grad_splits(M, K, L, nsm);
-    st = static_cast<cr_status>(cr::launch_lora_grad_mma(codes ? codes : X, ldx, code_scales, dv, nullptr, adapter,
-                                                         scale, gd, M, K, rank, L, parts, status, s));
+  if (d_down || d_up) {
+    st = static_cast<cr_status>(cr::launch_lora_grad_mma(
+        codes ? codes : X, ldx, code_scales, dY, lddy, dv, static_cast<const uint16_t*>(V), adapter, scale,
+        d_down ? gd : nullptr, d_up ? gu : nullptr, M, K, N, rank, L, parts, status, s));
     if (st != CR_OK) return st;
-    if (cr::launch_lora_grad_finish(gd, parts, nd, static_cast<uint16_t*>(d_down), nd, codes != nullptr, s) !=
-        cudaSuccess)
-      return CR_ERR_CUDA;
-  }
-  if (d_up) {
-    const int parts = cr::lora_grad_splits(M, N, L, nsm);
-    st = static_cast<cr_status>(cr::launch_lora_grad_mma(dY, lddy, nullptr, nullptr, static_cast<const uint16_t*>(V),
-                                                         adapter, scale, gu, M, N, rank, L, parts, status, s));
-    if (st != CR_OK) return st;
-    if (cr::launch_lora_grad_finish(gu, parts, nu, static_cast<uint16_t*>(d_up), nu, false, s) != cudaSuccess)
+    if (cr::launch_lora_grad_finish(gd, gu, parts, static_cast<int64_t>(L) * rank, K, N, static_cast<uint16_t*>(d_down),
+                                    static_cast<uint16_t*>(d_up), codes != nullptr, s) != cudaSuccess)
       return CR_ERR_CUDA;
   }
   return CR_OK;

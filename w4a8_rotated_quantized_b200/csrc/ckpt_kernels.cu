@@ -136,45 +136,55 @@ __global__ void __launch_bounds__(32 * kWarps)
   store_unit_bf16(P, k0, s, W + u * 256);
 }
 
-// G[row, :] = sum of the `parts` partial sums, in order, rotated if they were taken against codes.
-template <bool kRotate>
+// Eight values of the partial sums, added in order.
+__device__ __forceinline__ void add_parts(const float* __restrict__ src, int parts, int64_t stride, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float4 f0 = __ldg(reinterpret_cast<const float4*>(src + p * stride));
+    const float4 f1 = __ldg(reinterpret_cast<const float4*>(src + p * stride + 4));
+    v[0] += f0.x; v[1] += f0.y; v[2] += f0.z; v[3] += f0.w;
+    v[4] += f1.x; v[5] += f1.y; v[6] += f1.z; v[7] += f1.w;
+  }
+}
+
+// The gradients' partial sums joined and rounded.  The first `rot_blocks` blocks take slices of 256 values
+// of the rotated d_down, the rest eight values a thread of what is left: d_down unrotated, then d_up.
 __global__ void __launch_bounds__(32 * kWarps)
-    lora_grad_finish_kernel(const float* __restrict__ parts_sum, int parts, int64_t part_stride,
-                            uint16_t* __restrict__ G, int64_t total) {
-  if constexpr (kRotate) {
-    const int64_t u = lane_unit(), units = total >> 8;
+    lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts, int64_t n_down,
+                            int64_t n_up, uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up, int rot_blocks) {
+  if (static_cast<int>(blockIdx.x) < rot_blocks) {
+    const int64_t u = lane_unit();
     const int k0 = (threadIdx.x & 31) >> 2, l = threadIdx.x & 3;
+    const bool in = u < n_down >> 8;
     Pairs P;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) P.w[i] = make_float2(0.f, 0.f);
-    if (u < units)
-      for (int p = 0; p < parts; ++p) {
-        const float* src = parts_sum + p * part_stride + u * 256 + 8 * l;
+    for (int k = 0; k < 8; ++k) {
+      float v[8];
+      add_parts(Gdown + u * 256 + 32 * (k ^ k0) + 8 * l, in ? parts : 0, n_down, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 f0 = __ldg(reinterpret_cast<const float4*>(src + 32 * (k ^ k0)));
-          const float4 f1 = __ldg(reinterpret_cast<const float4*>(src + 32 * (k ^ k0) + 4));
-          const float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (k < 4) P.w[8 * (k & 3) + e].x += v[e]; else P.w[8 * (k & 3) + e].y += v[e];
-          }
-        }
+      for (int e = 0; e < 8; ++e) {
+        if (k < 4) P.w[8 * (k & 3) + e].x = v[e]; else P.w[8 * (k & 3) + e].y = v[e];
       }
-    fwht256_mapped<4>(P);
-    if (u < units) store_unit_bf16(P, k0, 0.0625f, G + u * 256);
-  } else {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 32 * kWarps + threadIdx.x) * 8;
-    if (i >= total) return;
-    float v[8] = {};
-    for (int p = 0; p < parts; ++p) {
-      const float4 f0 = __ldg(reinterpret_cast<const float4*>(parts_sum + p * part_stride + i));
-      const float4 f1 = __ldg(reinterpret_cast<const float4*>(parts_sum + p * part_stride + i + 4));
-      v[0] += f0.x; v[1] += f0.y; v[2] += f0.z; v[3] += f0.w;
-      v[4] += f1.x; v[5] += f1.y; v[6] += f1.z; v[7] += f1.w;
     }
-    *reinterpret_cast<uint4*>(G + i) = narrow8(v);
+    fwht256_mapped<4>(P);
+    if (in) store_unit_bf16(P, k0, 0.0625f, d_down + u * 256);
+    return;
   }
+  int64_t i = (static_cast<int64_t>(blockIdx.x - rot_blocks) * 32 * kWarps + threadIdx.x) * 8;
+  float v[8];
+  if (!rot_blocks) {
+    if (i < n_down) {
+      add_parts(Gdown + i, parts, n_down, v);
+      *reinterpret_cast<uint4*>(d_down + i) = narrow8(v);
+      return;
+    }
+    i -= n_down;
+  }
+  if (i >= n_up) return;
+  add_parts(Gup + i, parts, n_up, v);
+  *reinterpret_cast<uint4*>(d_up + i) = narrow8(v);
 }
 
 unsigned unit_blocks(int64_t units) { return static_cast<unsigned>((units + 8 * kWarps - 1) / (8 * kWarps)); }
@@ -207,14 +217,14 @@ cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16
   return cudaGetLastError();
 }
 
-cudaError_t launch_lora_grad_finish(const float* parts_sum, int parts, int64_t part_stride, uint16_t* G, int64_t total,
-                                    bool rotate, cudaStream_t stream) {
-  if (rotate)
-    lora_grad_finish_kernel<true>
-        <<<unit_blocks(total / 256), 32 * kWarps, 0, stream>>>(parts_sum, parts, part_stride, G, total);
-  else
-    lora_grad_finish_kernel<false><<<static_cast<unsigned>((total + 256 * kWarps - 1) / (256 * kWarps)), 32 * kWarps, 0,
-                                     stream>>>(parts_sum, parts, part_stride, G, total);
+cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts, int64_t rows, int K, int N,
+                                    uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream) {
+  const int64_t n_down = d_down ? rows * K : 0, n_up = d_up ? rows * N : 0;
+  const unsigned rot = rotate && d_down ? unit_blocks(n_down / 256) : 0;
+  const int64_t plain = (rot ? 0 : n_down) + n_up;
+  const unsigned blocks = rot + static_cast<unsigned>((plain + 256 * kWarps - 1) / (256 * kWarps));
+  lora_grad_finish_kernel<<<blocks, 32 * kWarps, 0, stream>>>(Gdown, Gup, parts, n_down, n_up, d_down, d_up,
+                                                              static_cast<int>(rot));
   return cudaGetLastError();
 }
 

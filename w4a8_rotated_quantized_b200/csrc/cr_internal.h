@@ -178,15 +178,18 @@ int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, co
 int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up, const float* scale,
                       const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, int M, int N, int rank, int L,
                       int* status, int num_sms, cudaStream_t stream);
-// Partial sums G float32 [splits, L, rank, C] of scale[a] * sum over the adapter's rows of V^T Z; Z bf16
-// rows, or codes with code_scale (then in the checkpoint's rotated basis).  V: float32 or bf16 [M, rank].
-int lora_grad_splits(int M, int C, int L, int num_sms);
-int launch_lora_grad_mma(const void* Z, int64_t ldz, const float* code_scale, const float* V32, const uint16_t* V16,
-                         const int32_t* adapter, const float* scale, float* G, int M, int C, int rank, int L,
-                         int splits, int* status, cudaStream_t stream);
-// bf16 G = the partial sums added in order, rotated by H256 if `rotate` (then total is a multiple of 256).
-cudaError_t launch_lora_grad_finish(const float* parts_sum, int parts, int64_t part_stride, uint16_t* G, int64_t total,
-                                    bool rotate, cudaStream_t stream);
+// Both gradients' products in one launch: partial sums Gdown float32 [splits, L, rank, K] of scale[a] * sum
+// over the adapter's rows of dV^T X (X bf16 rows, or codes with code_scale: then in the checkpoint's rotated
+// basis) and Gup [splits, L, rank, N] of V^T dY; either may be null.  dV float32, V bf16, [M, rank].
+int lora_grad_splits(int M, int K, int N, int rank, int L, int num_sms);
+int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, const void* dY, int64_t lddy,
+                         const float* dV, const uint16_t* V, const int32_t* adapter, const float* scale, float* Gdown,
+                         float* Gup, int M, int K, int N, int rank, int L, int splits, int* status,
+                         cudaStream_t stream);
+// The partial sums added in order and rounded: d_down [rows, K] (rotated by H256 if `rotate`) and d_up
+// [rows, N], rows = L * rank; either may be null.
+cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts, int64_t rows, int K, int N,
+                                    uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream);
 cudaError_t launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes, float* scales,
                              cudaStream_t stream);
 cudaError_t launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uint16_t* X, int64_t ldx,

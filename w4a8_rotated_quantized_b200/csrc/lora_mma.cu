@@ -30,6 +30,7 @@
 
 #include "cr_device.cuh"
 #include "cr_internal.h"
+#include "grid_sync.cuh"
 #include "lora_device.cuh"
 
 namespace cr {
@@ -77,7 +78,13 @@ __device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter
     const int a = ids[t];
     const uint32_t same = __match_any_sync(0xffffffffu, a);
     first = a >= 0 && __ffs(same) - 1 == lane;
-    for (int i = 0; first && i < 32 * warp; ++i) first = ids[i] != a;
+    // against the rows of the warps before, four at a time
+#pragma unroll
+    for (int i = 0; i < TM - 32; i += 4)
+      if (i < 32 * warp) {
+        const int4 o = *reinterpret_cast<const int4*>(ids + i);
+        first = first && o.x != a && o.y != a && o.z != a && o.w != a;
+      }
     firsts = __ballot_sync(0xffffffffu, first);
     if (lane == 0) counts[warp] = __popc(firsts);
   }
@@ -99,19 +106,22 @@ __device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter
 // ---------------------------------------------------------------------------------------------------
 
 struct VPlan {
-  int rp, cap, stages, stage, part_ld, off_part, off_list, off_bar, smem, cols;
+  int rp, cap, ring, part_ld, off_part, off_list, off_bar, smem, cols;
 };
+constexpr int kVStages = 8;  // at most
 inline __host__ __device__ VPlan v_plan(int rank, int L) {
   VPlan p;
   p.rp = round16(rank);
   p.cap = 256 / p.rp;
   if (p.cap > L) p.cap = L;
-  p.stage = TM * 128 + p.cap * p.rp * 128;
   p.part_ld = p.rp + 4;  // rows 4 banks apart: eight rows' 16-byte pieces lie side by side
   const int part = TM * p.part_ld * 4;
-  p.stages = (kSmemMax - part - kListBytes - kBarBytes) / p.stage;
-  if (p.stages > 8) p.stages = 8;
-  p.off_part = p.stages * p.stage;
+  // the ring takes what is left, up to eight of the largest stages; a tile with few adapters cuts it into
+  // more and smaller ones
+  const int stage = TM * 128 + p.cap * p.rp * 128;
+  int room = (kSmemMax - part - kListBytes - kBarBytes) & ~1023;
+  p.ring = room < kVStages * stage ? room : kVStages * stage;
+  p.off_part = p.ring;
   p.off_list = p.off_part + part;
   p.off_bar = p.off_list + kListBytes;
   p.smem = p.off_bar + kBarBytes;
@@ -119,6 +129,7 @@ inline __host__ __device__ VPlan v_plan(int rank, int L) {
   return p;
 }
 
+constexpr int kVMostSplits = 16;  // CTAs of a cluster (over 8: asked for as not portable)
 constexpr int kVThreads = 192;  // warp 0 MMA, warp 1 TMA, warps 2-5 epilogue
 
 __global__ void __launch_bounds__(kVThreads, 1)
@@ -143,7 +154,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
 
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = CR_OK;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < kVStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
@@ -152,6 +163,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) griddep_launch_dependents();  // the y kernel may set itself up beside this one
   if (warp == 1 && lane == 0) {
     prefetch_tmap(&tmap_x);
     prefetch_tmap(&tmap_a);
@@ -166,6 +178,8 @@ __global__ void __launch_bounds__(kVThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *slot;
 
+  const int stage = (TM + (nd < p.cap ? nd : p.cap) * p.rp) * 128;
+  const int stages = p.ring / stage < kVStages ? p.ring / stage : kVStages;
   const int nkb = (K + KB - 1) / KB;
   const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
@@ -184,8 +198,8 @@ __global__ void __launch_bounds__(kVThreads, 1)
         if (!mbar_wait(full(s), ph, abort)) { ok = false; break; }
         __syncwarp();
         tc_fence_after();
-        const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * p.stage));
-        const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * p.stage + TM * 128));
+        const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * stage));
+        const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * stage + TM * 128));
 #pragma unroll
         for (int kk = 0; kk < KB / 16; ++kk)
           umma_f16_ss_lane0(tmem, da + 2u * kk, db + 2u * kk, idesc, (kb != kb0 || kk) ? 1u : 0u, lane);
@@ -193,7 +207,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
         last_bar = empty(s);
         last_ph = ph;
         committed = true;
-        if (++s == p.stages) { s = 0; ph ^= 1u; }
+        if (++s == stages) { s = 0; ph ^= 1u; }
       }
       if (ok) umma_commit_lane0(acc_full, lane);
     }
@@ -211,13 +225,13 @@ __global__ void __launch_bounds__(kVThreads, 1)
       for (int d0 = 0; ok && d0 < nd; d0 += p.cap) {
         const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
         for (int kb = kb0; kb < kb1; ++kb, ++f) {
-          if (f >= p.stages && !mbar_wait(empty(s), ph ^ 1u, abort)) { ok = false; break; }
-          const uint32_t dst = smem_u32(base + s * p.stage);
+          if (f >= stages && !mbar_wait(empty(s), ph ^ 1u, abort)) { ok = false; break; }
+          const uint32_t dst = smem_u32(base + s * stage);
           mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(TM + c * p.rp) * 128u);
           tma_load_2d(dst, &tmap_x, kb * KB, static_cast<int32_t>(m0), full(s));
           for (int i = 0; i < c; ++i)
             tma_load_3d(dst + TM * 128 + i * p.rp * 128, &tmap_a, kb * KB, 0, list[d0 + i], full(s));
-          if (++s == p.stages) { s = 0; ph ^= 1u; }
+          if (++s == stages) { s = 0; ph ^= 1u; }
         }
       }
       if (!ok) {
@@ -275,13 +289,19 @@ __global__ void __launch_bounds__(kVThreads, 1)
   for (int i = threadIdx.x; i < rows * groups; i += kVThreads) {
     const int row = split * rows + i / groups, j = 4 * (i % groups);
     if (m0 + row >= M) break;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < splits; ++c) {
-      const float4 u = ld_shared_cluster_f4(mapa_shared(part_addr + 4u * (row * p.part_ld + j), c));
-      t.x += u.x;
-      t.y += u.y;
-      t.z += u.z;
-      t.w += u.w;
+    float4 u[kVMostSplits];  // all on their way before the first is added
+#pragma unroll
+    for (int c = 0; c < kVMostSplits; ++c) {
+      u[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < splits) u[c] = ld_shared_cluster_f4(mapa_shared(part_addr + 4u * (row * p.part_ld + j), c));
+    }
+    float4 t = u[0];
+#pragma unroll
+    for (int c = 1; c < kVMostSplits; ++c) {
+      t.x += u[c].x;
+      t.y += u[c].y;
+      t.z += u[c].z;
+      t.w += u[c].w;
     }
     *reinterpret_cast<float4*>(V + (m0 + row) * rank + j) = t;
     if (Vout)
@@ -293,23 +313,23 @@ __global__ void __launch_bounds__(kVThreads, 1)
 
 // ---------------------------------------------------------------------------------------------------
 // y: 128 tokens x 128 columns a tile.  The tile's base arrives by TMA in the buffer that its result leaves
-// from; V of the 128 rows, scaled and split into bf16 pairs, stays in shared memory for all column tiles.
+// from.  V of the 128 rows, scaled and split into bf16 pairs, stays in TMEM as the product's A operand for
+// all column tiles: read from shared memory it would cost as many bytes there as U does, and at rank 128
+// those bytes, not memory's, set the pace (134 us against 110 us for 8192 x 12288).
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int TN = 128;
 constexpr int kYTile = TM * TN * 2;  // 32 KB: two boxes of 64 columns x 128 rows
+constexpr int kVCol = 2 * TN;        // TMEM: two accumulators, then V's rounded values, then the rests
 struct YPlan {
-  int rp, groups, nb, nu, u, off_u, off_y, off_list, off_bar, smem;
+  int rp, nb, nu, u, off_y, off_list, off_bar, smem;
 };
 inline __host__ __device__ YPlan y_plan(int rank) {
   YPlan p;
   p.rp = round16(rank);
-  p.groups = (p.rp + 63) / 64;
-  const int v = 2 * p.groups * TM * 128;  // rounded values, then rests
-  p.u = p.rp * 256;                       // two boxes of 64 columns x rank rows
-  p.nu = p.rp <= 64 ? 4 : 2;
-  p.off_u = v;
-  p.off_y = v + p.nu * p.u;
+  p.u = p.rp * 256;  // two boxes of 64 columns x rank rows
+  p.nu = p.rp <= 64 ? 4 : 3;
+  p.off_y = p.nu * p.u;
   p.nb = (kSmemMax - p.off_y - kListBytes - kBarBytes) / kYTile;
   if (p.nb > 5) p.nb = 5;
   p.off_list = p.off_y + p.nb * kYTile;
@@ -317,7 +337,8 @@ inline __host__ __device__ YPlan y_plan(int rank) {
   p.smem = p.off_bar + kBarBytes;
   return p;
 }
-constexpr int kYMmaThreads = 192;  // warp 0 MMA, warp 1 TMA, warps 2-5 V and epilogue
+// warp 0 MMA, warps 1 and 10 TMA (base, U), warps 2-9 V and epilogue (64 columns each four)
+constexpr int kYMmaThreads = 352;
 
 __global__ void __launch_bounds__(kYMmaThreads, 1)
     lora_y_mma_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_base,
@@ -350,7 +371,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nb; ++s) {
       mbar_init(y_full(s), 1);
-      mbar_init(y_empty(s), 1);
+      mbar_init(y_empty(s), 2);
     }
     for (int s = 0; s < p.nu; ++s) {
       mbar_init(u_full(s), 1);
@@ -358,9 +379,9 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4);
+      mbar_init(acc_empty(b), 8);
     }
-    mbar_init(v_ready, 128);
+    mbar_init(v_ready, 256);
     *abort = 0;
     fence_mbar_init();
   }
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     prefetch_tmap(&tmap_y);
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(slot), 2 * TN);
+    tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
   }
   const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts);
@@ -382,6 +403,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer
     bool ok = nd == 0 || mbar_wait(v_ready, 0, abort);
+    tc_fence_after();
     bool committed = false;
     uint32_t last_bar = 0, last_ph = 0, ph = 0;
     int s = 0, f = 0;  // f: products issued; accumulator f & 1
@@ -393,12 +415,12 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
         if (!mbar_wait(u_full(s), ph, abort)) { ok = false; break; }
         __syncwarp();
         tc_fence_after();
-        const uint64_t du = sw128_mnmajor_desc(smem_u32(base + p.off_u + s * p.u), p.rp * 128);
+        const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
         for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
-          for (int kk = 0; kk < p.rp / 16; ++kk) {
-            const uint64_t dv = sw128_kmajor_desc(smem_u32(base + (h * p.groups + (kk >> 2)) * TM * 128)) + 2u * (kk & 3);
-            umma_f16_ss_lane0(tmem + static_cast<uint32_t>(b * TN), dv, du + 128u * kk, idesc, (h | kk) ? 1u : 0u, lane);
-          }
+          for (int kk = 0; kk < p.rp / 16; ++kk)
+            umma_f16_ts_lane0(tmem + static_cast<uint32_t>(b * TN),
+                              tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
+                              (h | kk) ? 1u : 0u, lane);
         umma_commit_lane0(u_empty(s), lane);
         umma_commit_lane0(acc_full(b), lane);
         last_bar = u_empty(s);
@@ -413,12 +435,12 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       if (committed) mbar_wait(last_bar, last_ph, &never);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- TMA producer
+    // ---------------------------------------------------------------- TMA: base tiles
     if (lane == 0) {
       bool ok = true;
-      int s = 0, f = 0, y = 0;
-      uint32_t ph = 0, yph = 0;
-      for (int t = t0; ok && t < t1; ++t) {
+      int y = 0;
+      uint32_t yph = 0;
+      for (int t = t0; t < t1; ++t) {
         if (t - t0 >= p.nb && !mbar_wait(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
         const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
         if (has_base) {
@@ -429,9 +451,22 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
           mbar_arrive(y_full(y));
         }
         if (++y == p.nb) { y = 0; yph ^= 1u; }
+      }
+      if (!ok) {
+        fail(abort, status);
+        grace();
+      }
+    }
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- TMA: U tiles
+    if (lane == 0) {
+      bool ok = true;
+      int s = 0, f = 0;
+      uint32_t ph = 0;
+      for (int t = t0; ok && t < t1; ++t) {
         for (int i = 0; i < nd; ++i, ++f) {
           if (f >= p.nu && !mbar_wait(u_empty(s), ph ^ 1u, abort)) { ok = false; break; }
-          const uint32_t ud = smem_u32(base + p.off_u + s * p.u);
+          const uint32_t ud = smem_u32(base + s * p.u);
           mbar_arrive_expect_tx(u_full(s), p.u);
           tma_load_3d(ud, &tmap_u, t * TN, 0, list[i], u_full(s));
           tma_load_3d(ud + p.u / 2, &tmap_u, t * TN + 64, 0, list[i], u_full(s));
@@ -445,43 +480,45 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- V, then the epilogue
-    const int q = warp & 3, row = 32 * q + lane;
-    const int tid = threadIdx.x - 64;
+    const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
+    griddep_wait();  // V comes from the kernel before this one
+    const int mine = ids[row];
     if (nd > 0) {
-      const int per = p.rp >> 2;
-      for (int i = tid; i < TM * per; i += 128) {
-        const int r = i / per, j = 4 * (i - r * per);
-        const int a = ids[r];
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (a >= 0 && j < rank) {
-          const float4 f = *reinterpret_cast<const float4*>(V + (m0 + r) * rank + j);
-          const float sc = __ldg(scale + a);
-          v[0] = f.x * sc;
-          v[1] = f.y * sc;
-          v[2] = f.z * sc;
-          v[3] = f.w * sc;
+      // this warp's rows, every other 16 ranks
+      const float sc = mine >= 0 ? __ldg(scale + mine) : 0.f;
+      const float* src = V + (m0 + row) * rank;
+#pragma unroll 2
+      for (int g = half; g < p.rp / 16; g += 2) {
+        float4 f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (mine >= 0 && 16 * g + 4 * k < rank) f[k] = __ldcg(reinterpret_cast<const float4*>(src + 16 * g + 4 * k));
         }
-        uint32_t hi[2], lo[2];
-        split_bf16(v[0], v[1], hi[0], lo[0]);
-        split_bf16(v[2], v[3], hi[1], lo[1]);
-        const int piece = ((j & 63) >> 3) ^ (r & 7);
-        uint8_t* d = base + (j >> 6) * TM * 128 + r * 128 + piece * 16 + (j & 4) * 2;
-        *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(d + p.groups * TM * 128) = make_uint2(lo[0], lo[1]);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          split_bf16(f[k].x * sc, f[k].y * sc, hi[2 * k], lo[2 * k]);
+          split_bf16(f[k].z * sc, f[k].w * sc, hi[2 * k + 1], lo[2 * k + 1]);
+        }
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(kVCol + 8 * g);
+        tmem_st8(at, hi);
+        tmem_st8(at + static_cast<uint32_t>(p.rp / 2), lo);
       }
-      fence_proxy_async_smem();
+      tmem_st_wait();
+      tc_fence_before();
       mbar_arrive(v_ready);
     }
-    const int mine = ids[row];
+    const bool storer = (warp == 2 || warp == 6) && lane == 0;  // of this half's 64 columns
     bool ok = true;
     int y = 0, f = 0;
     uint32_t yph = 0;
     for (int t = t0; ok && t < t1; ++t) {
-      uint8_t* tile = base + p.off_y + y * kYTile + row * 128;
+      uint8_t* box = base + p.off_y + y * kYTile + half * (kYTile / 2);
+      uint8_t* tile = box + row * 128;
       if (!mbar_wait_warp(y_full(y), yph, abort)) { ok = false; break; }
       if (!has_base && mine < 0) {  // no adapter, no base: zeros
-        for (int c = 0; c < 16; ++c)
-          *reinterpret_cast<uint4*>(tile + (c >> 3) * (kYTile / 2) + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + (c << 4)) = make_uint4(0, 0, 0, 0);
       }
       for (int i = 0; i < nd; ++i, ++f) {
         const int b = f & 1;
@@ -489,27 +526,25 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
         tc_fence_after();
         const bool hit = mine == list[i];
         if (__any_sync(0xffffffffu, hit)) {
-#pragma unroll 1
-          for (int ch = 0; ch < TN / 32; ++ch) {
-            uint32_t r[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * TN + 32 * ch), r);
-            tmem_ld_wait();
-            if (hit) {
-              uint8_t* d = tile + (ch >> 1) * (kYTile / 2);
+          uint32_t r[2][32];
+          const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * TN + 64 * half);
+          tmem_ld32(src, r[0]);
+          tmem_ld32(src + 32, r[1]);
+          tmem_ld_wait();
+          if (hit) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint4* at = reinterpret_cast<uint4*>(d + ((((ch & 1) * 4 + c) ^ (row & 7)) << 4));
-                float v[8];
+            for (int c = 0; c < 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(tile + ((c ^ (row & 7)) << 4));
+              float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * c + e]);
-                if (has_base) {
-                  float bv[8];
-                  widen8(*at, bv);
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[c >> 2][8 * (c & 3) + e]);
+              if (has_base) {
+                float bv[8];
+                widen8(*at, bv);
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) v[e] += bv[e];
-                }
-                *at = narrow8(v);
+                for (int e = 0; e < 8; ++e) v[e] += bv[e];
               }
+              *at = narrow8(v);
             }
           }
         }
@@ -519,19 +554,17 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       }
       if (!ok) break;
       fence_proxy_async_smem();
-      named_bar_sync(1, 128);
-      if (tid == 0) {
-        const uint32_t src = smem_u32(base + p.off_y + y * kYTile);
-        tma_store_2d(&tmap_y, t * TN, static_cast<int32_t>(m0), src);
-        if (t * TN + 64 < N) tma_store_2d(&tmap_y, t * TN + 64, static_cast<int32_t>(m0), src + kYTile / 2);
+      named_bar_sync(1 + half, 128);
+      if (storer) {
+        if (t * TN + 64 * half < N) tma_store_2d(&tmap_y, t * TN + 64 * half, static_cast<int32_t>(m0), smem_u32(box));
         bulk_commit_group();
-        // the tile before this one has left its buffer
+        // the box before this one has left its buffer
         bulk_wait_group_read<1>();
         if (t > t0) mbar_arrive(y_empty(y ? y - 1 : p.nb - 1));
       }
       if (++y == p.nb) { y = 0; yph ^= 1u; }
     }
-    if (tid == 0) bulk_wait_group<0>();
+    if (storer) bulk_wait_group<0>();
     if (!ok) fail(abort, status);
   }
 
@@ -540,38 +573,39 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * TN);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 // ---------------------------------------------------------------------------------------------------
 // grad: 256 columns of Z against all ranks of one adapter, summed over tiles of 64 tokens.  Z's columns are
-// the product's M side and V its N side, both as they lie in memory (MN-major).  Token tiles are split over
-// CTAs; the partial sums are joined by the finish kernel.
+// the product's M side and V its N side, both as they lie in memory (MN-major).  One launch runs both
+// gradients' products (d_down and d_up); token tiles are split over CTAs and the partial sums joined by the
+// finish kernel.  Eight warps make the operands (V split into pairs; codes widened to bf16), with V two
+// tiles ahead in registers: an L2 round trip under load is longer than a tile.
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int GM = 64;           // tokens of a tile
 constexpr int GC = 256;          // columns of a CTA
 constexpr int kZBox = GM * 128;  // 64 tokens x 64 columns, 8 KB
 constexpr int kZTile = 4 * kZBox;
-constexpr int kRawTile = GM * GC;  // the tile's codes, 16 KB
-constexpr int kMaxGradTiles = 4096;  // token tiles of one CTA (the bits of its tile mask)
+constexpr int kRawTile = GM * GC;   // the tile's codes, 16 KB
+constexpr int kMaxGradTiles = 512;  // token tiles of one CTA (64-bit row masks in shared memory)
 struct GPlan {
-  int rp, groups, v, stage, stages, raws, off_raw, off_mask, off_bar, smem, cols;
+  int rp, groups, stage, stages, raws, off_raw, off_mask, off_bar, smem, cols;
 };
-inline __host__ __device__ GPlan g_plan(int rank, bool codes) {
+inline __host__ __device__ GPlan g_plan(int rank, bool codes, bool v16) {
   GPlan p;
   p.rp = round16(rank);
   p.groups = (p.rp + 63) / 64;
-  p.v = 2 * p.groups * GM * 128;
-  p.stage = kZTile + p.v;
+  p.stage = kZTile + (v16 ? 1 : 2) * p.groups * GM * 128;
   p.raws = codes ? 3 : 0;
-  const int rest = kSmemMax - kMaxGradTiles / 8 - kBarBytes - p.raws * kRawTile;
+  const int rest = kSmemMax - kMaxGradTiles * 8 - kBarBytes - p.raws * kRawTile;
   p.stages = rest / p.stage;
   if (p.stages > 4) p.stages = 4;
   p.off_raw = p.stages * p.stage;
   p.off_mask = p.off_raw + p.raws * kRawTile;
-  p.off_bar = p.off_mask + kMaxGradTiles / 8;
+  p.off_bar = p.off_mask + kMaxGradTiles * 8;
   p.smem = p.off_bar + kBarBytes;
   p.cols = tmem_cols_for(2 * p.rp);
   return p;
@@ -592,25 +626,24 @@ __device__ __forceinline__ uint2 bytes_to_bf16(uint32_t w) {
   return o;
 }
 
-// kV16: V is bf16 (exact as it is: one product); else float32, as pairs.
+// kV16: V is bf16 (exact as it is: one product); else float32, as pairs.  `block` of this product's blocks.
 template <bool kCodes, bool kV16>
-__global__ void __launch_bounds__(kGThreads, 1)
-    lora_grad_mma_kernel(const __grid_constant__ CUtensorMap tmap_z, const float* __restrict__ code_scale,
-                         const float* __restrict__ V32, const uint16_t* __restrict__ V16,
-                         const int32_t* __restrict__ adapter, const float* __restrict__ scale, float* __restrict__ G,
-                         int M, int C, int rank, int L, int splits, int* __restrict__ status) {
+__device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float* __restrict__ code_scale,
+                                          const void* __restrict__ V, const int32_t* __restrict__ adapter,
+                                          const float* __restrict__ scale, float* __restrict__ G, int M, int C,
+                                          int rank, int L, int splits, int block, int* __restrict__ status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align_smem(smem_raw);
-  const GPlan p = g_plan(rank, kCodes);
+  const GPlan p = g_plan(rank, kCodes, kV16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int colblocks = (C + GC - 1) / GC;
-  const int c0 = (blockIdx.x % colblocks) * GC;
-  const int a = blockIdx.x / colblocks % L;
-  const int split = blockIdx.x / colblocks / L;
+  const int c0 = (block % colblocks) * GC;
+  const int a = block / colblocks % L;
+  const int split = block / colblocks / L;
   const int tiles = (M + GM - 1) / GM;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
-  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(base + p.off_mask);
+  const int nt = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits) - t0;
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(base + p.off_mask);
   const uint32_t bars = smem_u32(base + p.off_bar);
   auto z_full = [&](int s) { return bars + 8u * s; };         // TMA: the tile's Z or codes
   auto raw_empty = [&](int s) { return bars + 32u + 8u * s; };  // codes: converted
@@ -631,42 +664,26 @@ __global__ void __launch_bounds__(kGThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < kMaxGradTiles / 32; i += kGThreads) mask[i] = 0;
   if (warp == 9 && lane == 0) prefetch_tmap(&tmap_z);
   if (warp == 8) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
   }
+  // the rows of this CTA's token tiles that name its adapter
+  for (int t = warp; t < nt; t += kGThreads / 32) {
+    const int64_t m = static_cast<int64_t>(t0 + t) * GM + lane;
+    const uint32_t lo = __ballot_sync(0xffffffffu, m < M && row_adapter(adapter, m, L) == a);
+    const uint32_t hi = __ballot_sync(0xffffffffu, m + 32 < M && row_adapter(adapter, m + 32, L) == a);
+    if (lane == 0) mask[t] = static_cast<unsigned long long>(hi) << 32 | lo;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the token tiles of this CTA in which its adapter occurs
-  for (int t = t0 + warp; t < t1; t += kGThreads / 32) {
-    bool any = !adapter;
-    if (adapter) {
-      const int64_t m = static_cast<int64_t>(t) * GM + lane;
-      const bool h0 = m < M && row_adapter(adapter, m, L) == a;
-      const bool h1 = m + 32 < M && row_adapter(adapter, m + 32, L) == a;
-      any = __any_sync(0xffffffffu, h0 || h1);
-    } else {
-      any = a == 0;
-    }
-    if (any && lane == 0) atomicOr(&mask[(t - t0) >> 5], 1u << ((t - t0) & 31));
-  }
-  __syncthreads();
   const uint32_t tmem = *slot;
-  const int nt = t1 - t0;
-  // first marked tile at or after i (relative to t0), nt if none
+  // first tile at or after i with such a row, nt if none
   auto next_tile = [&](int i) {
-    while (i < nt) {
-      const uint32_t w = mask[i >> 5] >> (i & 31);
-      if (w) {
-        i += __ffs(w) - 1;
-        return i < nt ? i : nt;
-      }
-      i = (i | 31) + 1;
-    }
-    return nt;
+    while (i < nt && mask[i] == 0) ++i;
+    return i;
   };
 
   if (warp == 8) {
@@ -683,6 +700,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kZBox, kZBox);
+#pragma unroll
         for (int h = 0; h < (kV16 ? 1 : 2); ++h) {
           const uint64_t dv = sw128_mnmajor_desc(z + kZTile + h * p.groups * GM * 128, GM * 128);
 #pragma unroll
@@ -732,67 +750,66 @@ __global__ void __launch_bounds__(kGThreads, 1)
   } else {
     // ---------------------------------------------------------------- operands (8 warps)
     const int tid = threadIdx.x;
-    const int per = p.rp >> 2;  // groups of four ranks of a row
-    constexpr int kMost = GM * (kMaxRank / 4) / 256;  // of a thread
-    const int n = GM * per / 256;                     // per >= 4: a whole number of passes
-    bool ok = true;
-    int s = 0, rs = 0;
-    uint32_t ph = 0, rph = 0;
-    int f = 0;
-    float4 v[kMost];   // the next tile's V, on its way (bf16: bits in x, y)
-    auto fetch = [&](int i) {
+    constexpr int kMost = GM * (kMaxRank / 4) / 256;  // groups of four ranks of a thread
+    const int n = p.rp >> 4;
+    int at[kMost], from[kMost];  // place in the V operand (its row in the bits above 15); offset from the tile's V
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int per = p.rp >> 2, e = tid + 256 * k;
+      const int r = e / per, j = 4 * (e - r * per);
+      at[k] = (j >> 6) * GM * 128 + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 4) * 2 + (r << 16);
+      from[k] = j < rank ? r * rank + j : -1;
+    }
+    struct Ahead {
+      float4 v[kMost];  // bf16: bits in x, y
+      float cs[kCodes ? kMost : 1];
+    };
+    auto fetch = [&](int i, Ahead& x) {
+      if (i >= nt) return;
+      const unsigned long long rows = mask[i];
+      const int64_t m0 = static_cast<int64_t>(t0 + i) * GM;
 #pragma unroll
       for (int k = 0; k < kMost; ++k) {
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        x.v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k >= n) continue;
-        const int e = tid + 256 * k;
-        const int r = e / per, j = 4 * (e - r * per);
-        const int64_t m = static_cast<int64_t>(t0 + i) * GM + r;
-        if (m < M && j < rank && row_adapter(adapter, m, L) == a) {
-          if constexpr (kV16) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(V16 + m * rank + j));
-            v[k].x = __uint_as_float(w.x);
-            v[k].y = __uint_as_float(w.y);
-          } else {
-            v[k] = *reinterpret_cast<const float4*>(V32 + m * rank + j);
-            if constexpr (kCodes) {
-              const float cs = __ldg(code_scale + m * (C >> 8) + (c0 >> 8));
-              v[k].x *= cs;
-              v[k].y *= cs;
-              v[k].z *= cs;
-              v[k].w *= cs;
-            }
-          }
+        const int r = at[k] >> 16;
+        if (!(rows >> r & 1) || from[k] < 0) continue;
+        if constexpr (kV16) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(V) + m0 * rank + from[k]));
+          x.v[k].x = __uint_as_float(w.x);
+          x.v[k].y = __uint_as_float(w.y);
+        } else {
+          x.v[k] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(V) + m0 * rank + from[k]));
+          if constexpr (kCodes) x.cs[k] = __ldg(code_scale + (m0 + r) * (C >> 8) + (c0 >> 8));
         }
       }
     };
-    int i = next_tile(0);
-    if (i < nt) fetch(i);
-    while (i < nt) {
+    bool ok = true;
+    int s = 0, rs = 0, f = 0;
+    uint32_t ph = 0, rph = 0;
+    auto make = [&](int i, Ahead& x) {
       uint8_t* z = base + s * p.stage;
-      uint8_t* vt = z + kZTile;
+      const unsigned long long rows = mask[i];
       if constexpr (kCodes) {
-        if (f >= p.stages && !mbar_wait_warp(empty(s), ph ^ 1u, abort)) { ok = false; break; }
-        if (!mbar_wait_warp(z_full(rs), rph, abort)) { ok = false; break; }
+        // codes are finite: those of other adapters' rows meet zeros of V
+        if (f >= p.stages && !mbar_wait_warp(empty(s), ph ^ 1u, abort)) return false;
+        if (!mbar_wait_warp(z_full(rs), rph, abort)) return false;
         const uint8_t* raw = base + p.off_raw + rs * kRawTile;
 #pragma unroll
         for (int k = 0; k < GM / 8; ++k) {  // a row of the tile for each warp
           const int r = 8 * k + warp;
-          const int64_t m = static_cast<int64_t>(t0 + i) * GM + r;
           const uint2 w = *reinterpret_cast<const uint2*>(raw + r * GC + 8 * lane);
           const uint2 lo = bytes_to_bf16(w.x), hi = bytes_to_bf16(w.y);
           *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
               make_uint4(lo.x, lo.y, hi.x, hi.y);
-          (void)m;  // codes are finite: rows of other adapters meet zeros of V
         }
       } else {
-        if (!mbar_wait_warp(z_full(s), ph, abort)) { ok = false; break; }
-        if (adapter) {
+        if (!mbar_wait_warp(z_full(s), ph, abort)) return false;
+        if (~rows) {
 #pragma unroll 1
           for (int k = 0; k < GM / 8; ++k) {
             const int r = 8 * k + warp;
-            const int64_t m = static_cast<int64_t>(t0 + i) * GM + r;
-            if (m < M && row_adapter(adapter, m, L) != a)
+            if (!(rows >> r & 1))
               *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
         }
@@ -800,15 +817,22 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
       for (int k = 0; k < kMost; ++k) {
         if (k >= n) continue;
-        const int e = tid + 256 * k;
-        const int r = e / per, j = 4 * (e - r * per);
-        uint8_t* d = vt + (j >> 6) * GM * 128 + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 4) * 2;
+        uint8_t* d = z + kZTile + (at[k] & 0xFFFF);
+        float4 v = x.v[k];
         if constexpr (kV16) {
-          *reinterpret_cast<uint2*>(d) = make_uint2(__float_as_uint(v[k].x), __float_as_uint(v[k].y));
+          *reinterpret_cast<uint2*>(d) = make_uint2(__float_as_uint(v.x), __float_as_uint(v.y));
         } else {
+          if constexpr (kCodes) {
+            if (rows >> (at[k] >> 16) & 1) {
+              v.x *= x.cs[k];
+              v.y *= x.cs[k];
+              v.z *= x.cs[k];
+              v.w *= x.cs[k];
+            }
+          }
           uint32_t hi[2], lo[2];
-          split_bf16(v[k].x, v[k].y, hi[0], lo[0]);
-          split_bf16(v[k].z, v[k].w, hi[1], lo[1]);
+          split_bf16(v.x, v.y, hi[0], lo[0]);
+          split_bf16(v.z, v.w, hi[1], lo[1]);
           *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(d + p.groups * GM * 128) = make_uint2(lo[0], lo[1]);
         }
@@ -819,11 +843,23 @@ __global__ void __launch_bounds__(kGThreads, 1)
         mbar_arrive(ready(s));
         if (kCodes) mbar_arrive(raw_empty(rs));
       }
-      i = next_tile(i + 1);
-      if (i < nt) fetch(i);
       ++f;
       if (++s == p.stages) { s = 0; ph ^= 1u; }
       if (kCodes && ++rs == p.raws) { rs = 0; rph ^= 1u; }
+      return true;
+    };
+    Ahead x, y;
+    int i = next_tile(0), i2 = next_tile(i + 1);
+    fetch(i, x);
+    fetch(i2, y);
+    while (i < nt) {
+      if (!(ok = make(i, x))) break;
+      i = next_tile(i2 + 1);
+      fetch(i, x);
+      if (i2 >= nt) break;
+      if (!(ok = make(i2, y))) break;
+      i2 = next_tile(i + 1);
+      fetch(i2, y);
     }
     // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
     const int q = warp & 3, half = warp >> 2;
@@ -861,6 +897,20 @@ __global__ void __launch_bounds__(kGThreads, 1)
   }
 }
 
+template <bool kCodes>
+__global__ void __launch_bounds__(kGThreads, 1)
+    lora_grad_mma_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_dy,
+                         const float* __restrict__ code_scale, const float* __restrict__ dV,
+                         const uint16_t* __restrict__ V, const int32_t* __restrict__ adapter,
+                         const float* __restrict__ scale, float* __restrict__ Gdown, float* __restrict__ Gup, int M,
+                         int K, int N, int rank, int L, int splits, int down_blocks, int* __restrict__ status) {
+  if (static_cast<int>(blockIdx.x) < down_blocks)
+    grad_body<kCodes, false>(tmap_x, code_scale, dV, adapter, scale, Gdown, M, K, rank, L, splits, blockIdx.x, status);
+  else
+    grad_body<false, true>(tmap_dy, nullptr, V, adapter, scale, Gup, M, N, rank, L, splits, blockIdx.x - down_blocks,
+                           status);
+}
+
 std::atomic<bool> g_attr_done[64];
 
 bool set_attrs() {
@@ -870,10 +920,10 @@ bool set_attrs() {
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   const int most = kSmemMax + 1024;
   if (cudaFuncSetAttribute(lora_v_mma_kernel, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_v_mma_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
       cudaFuncSetAttribute(lora_y_mma_kernel, attr, most) != cudaSuccess ||
-      cudaFuncSetAttribute(lora_grad_mma_kernel<false, false>, attr, most) != cudaSuccess ||
-      cudaFuncSetAttribute(lora_grad_mma_kernel<false, true>, attr, most) != cudaSuccess ||
-      cudaFuncSetAttribute(lora_grad_mma_kernel<true, false>, attr, most) != cudaSuccess)
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true>, attr, most) != cudaSuccess)
     return false;
   g_attr_done[dev].store(true);
   return true;
@@ -896,7 +946,7 @@ int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, co
   const int64_t tiles = (static_cast<int64_t>(M) + TM - 1) / TM;
   const int nkb = (K + KB - 1) / KB;
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= num_sms && nkb >= 4 * splits) splits *= 2;
+  while (splits < kVMostSplits && tiles * splits * 2 <= num_sms && nkb >= 4 * splits) splits *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -938,37 +988,66 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
       best = s;
     }
   }
-  lora_y_mma_kernel<<<static_cast<unsigned>(tiles_m * best), kYMmaThreads, p.smem + 1024, stream>>>(
-      tu, tb, ty, V, adapter, scale, base != nullptr, M, N, rank, L, best, status);
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  // a programmatic dependent of the v kernel: it starts, loads base and U while that one ends, and waits for
+  // it on the device before it reads V
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles_m * best), 1, 1);
+  cfg.blockDim = dim3(kYMmaThreads, 1, 1);
+  cfg.dynamicSmemBytes = p.smem + 1024;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_y_mma_kernel, tu, tb, ty, V, adapter, scale, static_cast<int>(base != nullptr), M,
+                            N, rank, L, best, status) == cudaSuccess
+             ? CR_OK
+             : CR_ERR_CUDA;
 }
 
-int lora_grad_splits(int M, int C, int L, int num_sms) {
-  const int64_t items = static_cast<int64_t>((C + GC - 1) / GC) * L;
+// Token splits of the gradient products.  In units of one tile's time (about half a microsecond): rounds of
+// CTAs, each with its tiles and about five tiles' worth of setting up and writing out, and the partial sums'
+// way to memory and back (about 2.5 MB a unit).
+int lora_grad_splits(int M, int K, int N, int rank, int L, int num_sms) {
+  const int64_t items = (static_cast<int64_t>((K + GC - 1) / GC) + (N + GC - 1) / GC) * L;
   const int tiles = (M + GM - 1) / GM;
-  int64_t s = num_sms / items;
-  if (s > (tiles + 3) / 4) s = (tiles + 3) / 4;
   const int least = (tiles + kMaxGradTiles - 1) / kMaxGradTiles;
-  if (s < least) s = least;
-  return s < 1 ? 1 : static_cast<int>(s);
+  int best = least < 1 ? 1 : least;
+  int64_t best_cost = INT64_MAX;
+  for (int s = best; s <= tiles && s <= best + 31; ++s) {
+    const int64_t rounds = (items * s + num_sms - 1) / num_sms;
+    const int64_t cost = rounds * ((tiles + s - 1) / s + 5) + static_cast<int64_t>(s) * L * rank * (K + N) / 312500;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
-int launch_lora_grad_mma(const void* Z, int64_t ldz, const float* code_scale, const float* V32, const uint16_t* V16,
-                         const int32_t* adapter, const float* scale, float* G, int M, int C, int rank, int L,
-                         int splits, int* status, cudaStream_t stream) {
+int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, const void* dY, int64_t lddy,
+                         const float* dV, const uint16_t* V, const int32_t* adapter, const float* scale, float* Gdown,
+                         float* Gup, int M, int K, int N, int rank, int L, int splits, int* status,
+                         cudaStream_t stream) {
   if (!set_attrs()) return CR_ERR_CUDA;
   const bool codes = code_scale != nullptr;
-  const GPlan p = g_plan(rank, codes);
-  CUtensorMap tz;
-  const bool made = codes ? make_tmap_2d(&tz, CU_TENSOR_MAP_DATA_TYPE_UINT8, Z, M, C, C, GC, GM,
-                                         CU_TENSOR_MAP_SWIZZLE_NONE, kL2)
-                          : make_tmap_2d(&tz, kBf, Z, M, C, static_cast<uint64_t>(ldz) * 2, 64, GM, kSw128, kL2);
-  if (!made) return CR_ERR_CUDA;
-  const int64_t blocks = static_cast<int64_t>((C + GC - 1) / GC) * L * splits;
-  auto kern = codes ? lora_grad_mma_kernel<true, false> : V16 ? lora_grad_mma_kernel<false, true>
-                                                              : lora_grad_mma_kernel<false, false>;
-  kern<<<static_cast<unsigned>(blocks), kGThreads, p.smem + 1024, stream>>>(tz, code_scale, V32, V16, adapter, scale, G,
-                                                                            M, C, rank, L, splits, status);
+  CUtensorMap tx, ty;
+  memset(&tx, 0, sizeof(tx));
+  memset(&ty, 0, sizeof(ty));
+  if (Gdown && !(codes ? make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, X, M, K, K, GC, GM, CU_TENSOR_MAP_SWIZZLE_NONE, kL2)
+                       : make_tmap_2d(&tx, kBf, X, M, K, static_cast<uint64_t>(ldx) * 2, 64, GM, kSw128, kL2)))
+    return CR_ERR_CUDA;
+  if (Gup && !make_tmap_2d(&ty, kBf, dY, M, N, static_cast<uint64_t>(lddy) * 2, 64, GM, kSw128, kL2)) return CR_ERR_CUDA;
+  const int64_t down = Gdown ? static_cast<int64_t>((K + GC - 1) / GC) * L * splits : 0;
+  const int64_t up = Gup ? static_cast<int64_t>((N + GC - 1) / GC) * L * splits : 0;
+  if (down + up > INT32_MAX) return CR_ERR_UNSUPPORTED_SHAPE;
+  const int s0 = g_plan(rank, codes, false).smem, s1 = g_plan(rank, false, true).smem;
+  const int smem = (s0 > s1 ? s0 : s1) + 1024;
+  auto kern = codes ? lora_grad_mma_kernel<true> : lora_grad_mma_kernel<false>;
+  kern<<<static_cast<unsigned>(down + up), kGThreads, smem, stream>>>(tx, ty, code_scale, dV, V, adapter, scale, Gdown,
+                                                                      Gup, M, K, N, rank, L, splits,
+                                                                      static_cast<int>(down), status);
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
