@@ -254,28 +254,31 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T on 16-bit operands, one CTA.  Only lane 0 of the converged warp issues.
-__device__ __forceinline__ void umma_f16_ss_lane0(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                  uint32_t accumulate, int lane) {
+// One thread of the converged warp, by the hardware's own choice.  A loop of tcgen05.mma inside a branch on it
+// issues one every 49 cycles; predicated on the lane inside the instruction's own assembly it takes 121,
+// which narrow products (N < 256) cannot hide.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
+  return ok != 0;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T on 16-bit operands, one CTA; one thread.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.eq.s32 e, %5, 0; "
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Same with A in TMEM: 8 columns hold 16 values along the sum, two to a 32-bit column.
-__device__ __forceinline__ void umma_f16_ts_lane0(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                  uint32_t accumulate, int lane) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.eq.s32 e, %5, 0; "
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_lane0(uint32_t bar, int lane) {
-  asm volatile(
-      "{ .reg .pred e; setp.eq.s32 e, %1, 0; "
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(lane)
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -438,13 +441,13 @@ __device__ __forceinline__ void umma_i8_pair_ss_lane0(uint32_t d_tmem, uint64_t 
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
       : "memory");
 }
-// Same on 16-bit operands.
-__device__ __forceinline__ void umma_f16_pair_ss_lane0(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                       uint32_t accumulate, int lane) {
+// D[tmem] (+)= A[smem] * B[smem]^T on 16-bit operands over the CTA pair; one thread of the leader.
+__device__ __forceinline__ void umma_f16_pair_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.eq.s32 e, %5, 0; "
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lane)
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit_pair_mc_lane0(uint32_t bar, uint16_t cta_mask, int lane) {

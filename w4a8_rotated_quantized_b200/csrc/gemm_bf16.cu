@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto tile_of = [&](int local) { return pair + local * npairs; };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ MMA issuer (leader CTA)
-    if (rank == 0) {
+    // ------------------------------------------------------------ MMA issuer (leader CTA, one thread)
+    if (rank == 0 && elect_one()) {
       bool ok = true;
       bool committed = false;
       uint32_t last_bar = 0, last_par = 0;
@@ -141,15 +141,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * ACC_COLS);
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait_from(sm.full(s), ph, next_full, abort)) { ok = false; break; }
-          __syncwarp();
           tc_fence_after();
           const uint64_t da = sw128_kmajor_desc(smem_u32(sm.a(s)));
           const uint64_t db = sw128_mnmajor_desc(smem_u32(sm.b(s)), B_GROUP);
           // 16 steps of the sum: 32 bytes along A's rows, 16 rows (2048 bytes) of W
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            umma_f16_pair_ss_lane0(d_tmem, da + 2u * kk, db + 128u * kk, IDESC, (kb | kk) ? 1u : 0u, lane);
-          umma_commit_pair_mc_lane0(sm.empty(s), 0x3, lane);
+            umma_f16_pair_ss(d_tmem, da + 2u * kk, db + 128u * kk, IDESC, (kb | kk) ? 1u : 0u);
+          umma_commit_pair_mc(sm.empty(s), 0x3);
           last_bar = sm.empty(s);
           last_par = ph;
           committed = true;
@@ -158,10 +157,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           next_full = mbar_test(sm.full(s), ph);
         }
         if (!ok) break;
-        umma_commit_pair_mc_lane0(sm.tmem_full(b), 0x3, lane);
+        umma_commit_pair_mc(sm.tmem_full(b), 0x3);
       }
       if (!ok) {
-        if (lane == 0) fail(sm, status);
+        fail(sm, status);
         if (committed) {
           volatile int never = 0;
           mbar_wait(last_bar, last_par, &never);  // the MMAs issued so far have finished reading

@@ -185,36 +185,37 @@ __global__ void __launch_bounds__(kVThreads, 1)
   const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- MMA issuer
-    bool ok = true, committed = false;
-    uint32_t ph = 0, last_bar = 0, last_ph = 0;
-    int s = 0, pass = 0;
-    for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
-      const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
-      const uint32_t idesc = idesc_bf16(TM, c * p.rp, false, false);
-      if (pass && !mbar_wait(acc_empty, (pass - 1) & 1, abort)) { ok = false; break; }
-      tc_fence_after();
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(full(s), ph, abort)) { ok = false; break; }
-        __syncwarp();
+    // ---------------------------------------------------------------- MMA issuer (one thread)
+    if (elect_one()) {
+      bool ok = true, committed = false;
+      uint32_t ph = 0, last_bar = 0, last_ph = 0;
+      int s = 0, pass = 0;
+      for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
+        const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
+        const uint32_t idesc = idesc_bf16(TM, c * p.rp, false, false);
+        if (pass && !mbar_wait(acc_empty, (pass - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * stage));
-        const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * stage + TM * 128));
-#pragma unroll
-        for (int kk = 0; kk < KB / 16; ++kk)
-          umma_f16_ss_lane0(tmem, da + 2u * kk, db + 2u * kk, idesc, (kb != kb0 || kk) ? 1u : 0u, lane);
-        umma_commit_lane0(empty(s), lane);
-        last_bar = empty(s);
-        last_ph = ph;
-        committed = true;
-        if (++s == stages) { s = 0; ph ^= 1u; }
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(full(s), ph, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * stage));
+          const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * stage + TM * 128));
+  #pragma unroll
+          for (int kk = 0; kk < KB / 16; ++kk)
+            umma_f16_ss(tmem, da + 2u * kk, db + 2u * kk, idesc, (kb != kb0 || kk) ? 1u : 0u);
+          umma_commit(empty(s));
+          last_bar = empty(s);
+          last_ph = ph;
+          committed = true;
+          if (++s == stages) { s = 0; ph ^= 1u; }
+        }
+        if (ok) umma_commit(acc_full);
       }
-      if (ok) umma_commit_lane0(acc_full, lane);
-    }
-    if (!ok) {
-      if (lane == 0) fail(abort, status);
-      volatile int never = 0;
-      if (committed) mbar_wait(last_bar, last_ph, &never);
+      if (!ok) {
+        fail(abort, status);
+        volatile int never = 0;
+        if (committed) mbar_wait(last_bar, last_ph, &never);
+      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- TMA producer
@@ -401,38 +402,39 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   const uint32_t tmem = *slot;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- MMA issuer
-    bool ok = nd == 0 || mbar_wait(v_ready, 0, abort);
-    tc_fence_after();
-    bool committed = false;
-    uint32_t last_bar = 0, last_ph = 0, ph = 0;
-    int s = 0, f = 0;  // f: products issued; accumulator f & 1
-    const uint32_t idesc = idesc_bf16(TM, TN, false, true);
-    for (int t = t0; ok && t < t1; ++t) {
-      for (int i = 0; i < nd; ++i, ++f) {
-        const int b = f & 1;
-        if (f >= 2 && !mbar_wait(acc_empty(b), ((f >> 1) - 1) & 1, abort)) { ok = false; break; }
-        if (!mbar_wait(u_full(s), ph, abort)) { ok = false; break; }
-        __syncwarp();
-        tc_fence_after();
-        const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
-        for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
-          for (int kk = 0; kk < p.rp / 16; ++kk)
-            umma_f16_ts_lane0(tmem + static_cast<uint32_t>(b * TN),
-                              tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
-                              (h | kk) ? 1u : 0u, lane);
-        umma_commit_lane0(u_empty(s), lane);
-        umma_commit_lane0(acc_full(b), lane);
-        last_bar = u_empty(s);
-        last_ph = ph;
-        committed = true;
-        if (++s == p.nu) { s = 0; ph ^= 1u; }
+    // ---------------------------------------------------------------- MMA issuer (one thread)
+    if (elect_one()) {
+      bool ok = nd == 0 || mbar_wait(v_ready, 0, abort);
+      tc_fence_after();
+      bool committed = false;
+      uint32_t last_bar = 0, last_ph = 0, ph = 0;
+      int s = 0, f = 0;  // f: products issued; accumulator f & 1
+      const uint32_t idesc = idesc_bf16(TM, TN, false, true);
+      for (int t = t0; ok && t < t1; ++t) {
+        for (int i = 0; i < nd; ++i, ++f) {
+          const int b = f & 1;
+          if (f >= 2 && !mbar_wait(acc_empty(b), ((f >> 1) - 1) & 1, abort)) { ok = false; break; }
+          if (!mbar_wait(u_full(s), ph, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
+          for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
+            for (int kk = 0; kk < p.rp / 16; ++kk)
+              umma_f16_ts(tmem + static_cast<uint32_t>(b * TN),
+                                tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
+                                (h | kk) ? 1u : 0u);
+          umma_commit(u_empty(s));
+          umma_commit(acc_full(b));
+          last_bar = u_empty(s);
+          last_ph = ph;
+          committed = true;
+          if (++s == p.nu) { s = 0; ph ^= 1u; }
+        }
       }
-    }
-    if (!ok) {
-      if (lane == 0) fail(abort, status);
-      volatile int never = 0;
-      if (committed) mbar_wait(last_bar, last_ph, &never);
+      if (!ok) {
+        fail(abort, status);
+        volatile int never = 0;
+        if (committed) mbar_wait(last_bar, last_ph, &never);
+      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- TMA: base tiles
@@ -687,39 +689,40 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   };
 
   if (warp == 8) {
-    // ---------------------------------------------------------------- MMA issuer
-    bool ok = true, committed = false;
-    uint32_t ph = 0, last_bar = 0, last_ph = 0;
-    int s = 0;
-    const uint32_t idesc = idesc_bf16(128, p.rp, true, true);
-    for (int i = next_tile(0); i < nt; i = next_tile(i + 1)) {
-      if (!mbar_wait(ready(s), ph, abort)) { ok = false; break; }
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t z = smem_u32(base + s * p.stage);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kZBox, kZBox);
-#pragma unroll
-        for (int h = 0; h < (kV16 ? 1 : 2); ++h) {
-          const uint64_t dv = sw128_mnmajor_desc(z + kZTile + h * p.groups * GM * 128, GM * 128);
-#pragma unroll
-          for (int kk = 0; kk < GM / 16; ++kk)
-            umma_f16_ss_lane0(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 128u * kk, idesc,
-                              (committed || h || kk) ? 1u : 0u, lane);
+    // ---------------------------------------------------------------- MMA issuer (one thread)
+    if (elect_one()) {
+      bool ok = true, committed = false;
+      uint32_t ph = 0, last_bar = 0, last_ph = 0;
+      int s = 0;
+      const uint32_t idesc = idesc_bf16(128, p.rp, true, true);
+      for (int i = next_tile(0); i < nt; i = next_tile(i + 1)) {
+        if (!mbar_wait(ready(s), ph, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t z = smem_u32(base + s * p.stage);
+  #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kZBox, kZBox);
+  #pragma unroll
+          for (int h = 0; h < (kV16 ? 1 : 2); ++h) {
+            const uint64_t dv = sw128_mnmajor_desc(z + kZTile + h * p.groups * GM * 128, GM * 128);
+  #pragma unroll
+            for (int kk = 0; kk < GM / 16; ++kk)
+              umma_f16_ss(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 128u * kk, idesc,
+                                (committed || h || kk) ? 1u : 0u);
+          }
         }
+        umma_commit(empty(s));
+        last_bar = empty(s);
+        last_ph = ph;
+        committed = true;
+        if (++s == p.stages) { s = 0; ph ^= 1u; }
       }
-      umma_commit_lane0(empty(s), lane);
-      last_bar = empty(s);
-      last_ph = ph;
-      committed = true;
-      if (++s == p.stages) { s = 0; ph ^= 1u; }
-    }
-    if (ok) umma_commit_lane0(acc_full, lane);
-    if (!ok) {
-      if (lane == 0) fail(abort, status);
-      volatile int never = 0;
-      if (committed) mbar_wait(last_bar, last_ph, &never);
+      if (ok) umma_commit(acc_full);
+      if (!ok) {
+        fail(abort, status);
+        volatile int never = 0;
+        if (committed) mbar_wait(last_bar, last_ph, &never);
+      }
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- TMA producer
