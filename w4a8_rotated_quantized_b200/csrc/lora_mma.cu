@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kVThreads, 1)
 
 constexpr int TN = 128;
 constexpr int kYTile = TM * TN * 2;  // 32 KB: two boxes of 64 columns x 128 rows
-constexpr int kVCol = 2 * TN;        // TMEM: two accumulators, then V's rounded values, then the rests
+constexpr int kAcc = 3;              // accumulators
+constexpr int kVCol = kAcc * TN;     // TMEM: the accumulators, then V's rounded values, then the rests
 struct YPlan {
   int rp, nb, nu, u, off_y, off_list, off_bar, smem;
 };
@@ -329,7 +330,7 @@ inline __host__ __device__ YPlan y_plan(int rank) {
   YPlan p;
   p.rp = round16(rank);
   p.u = p.rp * 256;  // two boxes of 64 columns x rank rows
-  p.nu = p.rp <= 64 ? 4 : 3;
+  p.nu = 4;
   p.off_y = p.nu * p.u;
   p.nb = (kSmemMax - p.off_y - kListBytes - kBarBytes) / kYTile;
   if (p.nb > 5) p.nb = 5;
@@ -363,11 +364,11 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   auto u_full = [&](int s) { return bars + 80u + 8u * s; };
   auto u_empty = [&](int s) { return bars + 112u + 8u * s; };
   auto acc_full = [&](int b) { return bars + 144u + 8u * b; };
-  auto acc_empty = [&](int b) { return bars + 160u + 8u * b; };
-  const uint32_t v_ready = bars + 176u;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 184);
-  volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 188);
-  int* counts = reinterpret_cast<int*>(base + p.off_bar + 192);
+  auto acc_empty = [&](int b) { return bars + 168u + 8u * b; };
+  const uint32_t v_ready = bars + 192u;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 200);
+  volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 204);
+  int* counts = reinterpret_cast<int*>(base + p.off_bar + 208);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nb; ++s) {
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       mbar_init(u_full(s), 1);
       mbar_init(u_empty(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAcc; ++b) {
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), 8);
     }
@@ -408,26 +409,30 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       tc_fence_after();
       bool committed = false;
       uint32_t last_bar = 0, last_ph = 0, ph = 0;
-      int s = 0, f = 0;  // f: products issued; accumulator f & 1
+      int s = 0, b = 0;  // the product's U stage and accumulator
+      uint32_t bph = 1;  // its accumulator is free: the phase before the first counts as completed
       const uint32_t idesc = idesc_bf16(TM, TN, false, true);
       for (int t = t0; ok && t < t1; ++t) {
-        for (int i = 0; i < nd; ++i, ++f) {
-          const int b = f & 1;
-          if (f >= 2 && !mbar_wait(acc_empty(b), ((f >> 1) - 1) & 1, abort)) { ok = false; break; }
+        for (int i = 0; i < nd; ++i) {
+          if (!mbar_wait(acc_empty(b), bph, abort)) { ok = false; break; }
           if (!mbar_wait(u_full(s), ph, abort)) { ok = false; break; }
           tc_fence_after();
           const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
+#pragma unroll
           for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
-            for (int kk = 0; kk < p.rp / 16; ++kk)
-              umma_f16_ts(tmem + static_cast<uint32_t>(b * TN),
-                                tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
-                                (h | kk) ? 1u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < kMaxRank / 16; ++kk)
+              if (kk < p.rp / 16)
+                umma_f16_ts(tmem + static_cast<uint32_t>(b * TN),
+                            tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
+                            (h | kk) ? 1u : 0u);
           umma_commit(u_empty(s));
           umma_commit(acc_full(b));
           last_bar = u_empty(s);
           last_ph = ph;
           committed = true;
           if (++s == p.nu) { s = 0; ph ^= 1u; }
+          if (++b == kAcc) { b = 0; bph ^= 1u; }
         }
       }
       if (!ok) {
@@ -513,8 +518,8 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     }
     const bool storer = (warp == 2 || warp == 6) && lane == 0;  // of this half's 64 columns
     bool ok = true;
-    int y = 0, f = 0;
-    uint32_t yph = 0;
+    int y = 0, b = 0;
+    uint32_t yph = 0, bph = 0;
     for (int t = t0; ok && t < t1; ++t) {
       uint8_t* box = base + p.off_y + y * kYTile + half * (kYTile / 2);
       uint8_t* tile = box + row * 128;
@@ -522,9 +527,8 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       if (!has_base && mine < 0) {  // no adapter, no base: zeros
         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + (c << 4)) = make_uint4(0, 0, 0, 0);
       }
-      for (int i = 0; i < nd; ++i, ++f) {
-        const int b = f & 1;
-        if (!mbar_wait_warp(acc_full(b), (f >> 1) & 1, abort)) { ok = false; break; }
+      for (int i = 0; i < nd; ++i) {
+        if (!mbar_wait_warp(acc_full(b), bph, abort)) { ok = false; break; }
         tc_fence_after();
         const bool hit = mine == list[i];
         if (__any_sync(0xffffffffu, hit)) {
@@ -553,6 +557,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(b));
+        if (++b == kAcc) { b = 0; bph ^= 1u; }
       }
       if (!ok) break;
       fence_proxy_async_smem();
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
 // grad: 256 columns of Z against all ranks of one adapter, summed over tiles of 64 tokens.  Z's columns are
 // the product's M side and V its N side, both as they lie in memory (MN-major).  One launch runs both
 // gradients' products (d_down and d_up); token tiles are split over CTAs and the partial sums joined by the
-// finish kernel.  Eight warps make the operands (V split into pairs; codes widened to bf16), with V two
+// finish kernel.  Sixteen warps make the operands (V split into pairs; codes widened to bf16), with V two
 // tiles ahead in registers: an L2 round trip under load is longer than a tile.
 // ---------------------------------------------------------------------------------------------------
 
@@ -612,7 +617,8 @@ inline __host__ __device__ GPlan g_plan(int rank, bool codes, bool v16) {
   p.cols = tmem_cols_for(2 * p.rp);
   return p;
 }
-constexpr int kGThreads = 320;  // warps 0-7 operands and epilogue, warp 8 MMA, warp 9 TMA
+constexpr int kGWarps = 16;               // make the operands and, at the end, write the sums
+constexpr int kGThreads = 32 * (kGWarps + 2);  // then the MMA's and TMA's warps
 
 // Four signed bytes -> bf16 pairs, exactly: the low 7 bits put into the mantissa of 128, less 128, or less
 // 256 where the sign bit is set.
@@ -628,8 +634,9 @@ __device__ __forceinline__ uint2 bytes_to_bf16(uint32_t w) {
   return o;
 }
 
-// kV16: V is bf16 (exact as it is: one product); else float32, as pairs.  `block` of this product's blocks.
-template <bool kCodes, bool kV16>
+// kV16: V is bf16 (exact as it is: one product); else float32, as pairs.  kN: groups of four ranks of a tile's
+// V that each thread takes, at most.  `block` of this product's blocks.
+template <bool kCodes, bool kV16, int kN>
 __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float* __restrict__ code_scale,
                                           const void* __restrict__ V, const int32_t* __restrict__ adapter,
                                           const float* __restrict__ scale, float* __restrict__ G, int M, int C,
@@ -658,16 +665,16 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4; ++s) {
       mbar_init(z_full(s), 1);
-      mbar_init(raw_empty(s), 8);
-      mbar_init(ready(s), 8);
+      mbar_init(raw_empty(s), kGWarps);
+      mbar_init(ready(s), kGWarps);
       mbar_init(empty(s), 1);
     }
     mbar_init(acc_full, 1);
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9 && lane == 0) prefetch_tmap(&tmap_z);
-  if (warp == 8) {
+  if (warp == kGWarps + 1 && lane == 0) prefetch_tmap(&tmap_z);
+  if (warp == kGWarps) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
   }
@@ -688,7 +695,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     return i;
   };
 
-  if (warp == 8) {
+  if (warp == kGWarps) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
     if (elect_one()) {
       bool ok = true, committed = false;
@@ -724,7 +731,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         if (committed) mbar_wait(last_bar, last_ph, &never);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kGWarps + 1) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
       bool ok = true;
@@ -751,39 +758,38 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       }
     }
   } else {
-    // ---------------------------------------------------------------- operands (8 warps)
+    // ---------------------------------------------------------------- operands
     const int tid = threadIdx.x;
-    constexpr int kMost = GM * (kMaxRank / 4) / 256;  // groups of four ranks of a thread
-    const int n = p.rp >> 4;
-    int at[kMost], from[kMost];  // place in the V operand (its row in the bits above 15); offset from the tile's V
+    int at[kN], from[kN];  // place in the V operand (its row in the bits above 15); offset from the tile's V
 #pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-      const int per = p.rp >> 2, e = tid + 256 * k;
+    for (int k = 0; k < kN; ++k) {
+      const int per = p.rp >> 2, e = tid + 32 * kGWarps * k;
       const int r = e / per, j = 4 * (e - r * per);
-      at[k] = (j >> 6) * GM * 128 + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 4) * 2 + (r << 16);
-      from[k] = j < rank ? r * rank + j : -1;
+      // an entry past the tile's rows goes nowhere
+      at[k] = r < GM ? (j >> 6) * GM * 128 + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 4) * 2 + (r << 16) : -1;
+      from[k] = r < GM && j < rank ? r * rank + j : -1;
     }
     struct Ahead {
-      float4 v[kMost];  // bf16: bits in x, y
-      float cs[kCodes ? kMost : 1];
+      float4 v[kN];  // bf16: bits in x, y
+      float cs[kCodes ? kN : 1];
     };
     auto fetch = [&](int i, Ahead& x) {
       if (i >= nt) return;
       const unsigned long long rows = mask[i];
       const int64_t m0 = static_cast<int64_t>(t0 + i) * GM;
 #pragma unroll
-      for (int k = 0; k < kMost; ++k) {
+      for (int k = 0; k < kN; ++k) {
         x.v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k >= n) continue;
+        if constexpr (kCodes) x.cs[k] = 0.f;
         const int r = at[k] >> 16;
-        if (!(rows >> r & 1) || from[k] < 0) continue;
+        if (from[k] < 0 || !(rows >> r & 1)) continue;
         if constexpr (kV16) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(V) + m0 * rank + from[k]));
+          const uint2 w = ldg_here_u2(static_cast<const uint16_t*>(V) + m0 * rank + from[k]);
           x.v[k].x = __uint_as_float(w.x);
           x.v[k].y = __uint_as_float(w.y);
         } else {
-          x.v[k] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(V) + m0 * rank + from[k]));
-          if constexpr (kCodes) x.cs[k] = __ldg(code_scale + (m0 + r) * (C >> 8) + (c0 >> 8));
+          x.v[k] = ldg_here_f4(static_cast<const float*>(V) + m0 * rank + from[k]);
+          if constexpr (kCodes) x.cs[k] = ldg_here_f1(code_scale + (m0 + r) * (C >> 8) + (c0 >> 8));
         }
       }
     };
@@ -799,8 +805,8 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         if (!mbar_wait_warp(z_full(rs), rph, abort)) return false;
         const uint8_t* raw = base + p.off_raw + rs * kRawTile;
 #pragma unroll
-        for (int k = 0; k < GM / 8; ++k) {  // a row of the tile for each warp
-          const int r = 8 * k + warp;
+        for (int k = 0; k < GM / kGWarps; ++k) {  // a row of the tile for each warp
+          const int r = kGWarps * k + warp;
           const uint2 w = *reinterpret_cast<const uint2*>(raw + r * GC + 8 * lane);
           const uint2 lo = bytes_to_bf16(w.x), hi = bytes_to_bf16(w.y);
           *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
@@ -810,28 +816,26 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         if (!mbar_wait_warp(z_full(s), ph, abort)) return false;
         if (~rows) {
 #pragma unroll 1
-          for (int k = 0; k < GM / 8; ++k) {
-            const int r = 8 * k + warp;
+          for (int k = 0; k < GM / kGWarps; ++k) {
+            const int r = kGWarps * k + warp;
             if (!(rows >> r & 1))
               *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
         }
       }
 #pragma unroll
-      for (int k = 0; k < kMost; ++k) {
-        if (k >= n) continue;
+      for (int k = 0; k < kN; ++k) {
+        if (at[k] < 0) continue;
         uint8_t* d = z + kZTile + (at[k] & 0xFFFF);
         float4 v = x.v[k];
         if constexpr (kV16) {
           *reinterpret_cast<uint2*>(d) = make_uint2(__float_as_uint(v.x), __float_as_uint(v.y));
         } else {
           if constexpr (kCodes) {
-            if (rows >> (at[k] >> 16) & 1) {
-              v.x *= x.cs[k];
-              v.y *= x.cs[k];
-              v.z *= x.cs[k];
-              v.w *= x.cs[k];
-            }
+            v.x *= x.cs[k];  // 0 for both in a row that is not the adapter's
+            v.y *= x.cs[k];
+            v.z *= x.cs[k];
+            v.w *= x.cs[k];
           }
           uint32_t hi[2], lo[2];
           split_bf16(v.x, v.y, hi[0], lo[0]);
@@ -865,14 +869,15 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       fetch(i2, y);
     }
     // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
-    const int q = warp & 3, half = warp >> 2;
+    const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 ranks
     const int c = c0 + 128 * half + 32 * q + lane;
     const float sc = __ldg(scale + a);
     float* out = G + (static_cast<int64_t>(split) * L + a) * rank * C + c;
     if (ok && f > 0) {
       if (mbar_wait_warp(acc_full, 0, abort)) {
         tc_fence_after();
-        for (int j = 0; j < p.rp; j += 16) {
+#pragma unroll 1
+        for (int j = 16 * part; j < p.rp; j += 32) {
           uint32_t r[16];
           tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * p.rp + j), r);
           tmem_ld_wait();
@@ -886,7 +891,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         ok = false;
       }
     } else if (c < C) {
-      for (int j = 0; j < rank; ++j) out[static_cast<int64_t>(j) * C] = 0.f;
+      for (int j = part; j < rank; j += 2) out[static_cast<int64_t>(j) * C] = 0.f;
     }
     if (!ok) fail(abort, status);
   }
@@ -894,13 +899,13 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kGWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, p.cols);
   }
 }
 
-template <bool kCodes>
+template <bool kCodes, int kN>
 __global__ void __launch_bounds__(kGThreads, 1)
     lora_grad_mma_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_dy,
                          const float* __restrict__ code_scale, const float* __restrict__ dV,
@@ -908,9 +913,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
                          const float* __restrict__ scale, float* __restrict__ Gdown, float* __restrict__ Gup, int M,
                          int K, int N, int rank, int L, int splits, int down_blocks, int* __restrict__ status) {
   if (static_cast<int>(blockIdx.x) < down_blocks)
-    grad_body<kCodes, false>(tmap_x, code_scale, dV, adapter, scale, Gdown, M, K, rank, L, splits, blockIdx.x, status);
+    grad_body<kCodes, false, kN>(tmap_x, code_scale, dV, adapter, scale, Gdown, M, K, rank, L, splits, blockIdx.x, status);
   else
-    grad_body<false, true>(tmap_dy, nullptr, V, adapter, scale, Gup, M, N, rank, L, splits, blockIdx.x - down_blocks,
+    grad_body<false, true, kN>(tmap_dy, nullptr, V, adapter, scale, Gup, M, N, rank, L, splits, blockIdx.x - down_blocks,
                            status);
 }
 
@@ -925,8 +930,12 @@ bool set_attrs() {
   if (cudaFuncSetAttribute(lora_v_mma_kernel, attr, most) != cudaSuccess ||
       cudaFuncSetAttribute(lora_v_mma_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
       cudaFuncSetAttribute(lora_y_mma_kernel, attr, most) != cudaSuccess ||
-      cudaFuncSetAttribute(lora_grad_mma_kernel<false>, attr, most) != cudaSuccess ||
-      cudaFuncSetAttribute(lora_grad_mma_kernel<true>, attr, most) != cudaSuccess)
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false, 1>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false, 2>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false, 4>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true, 1>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true, 2>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true, 4>, attr, most) != cudaSuccess)
     return false;
   g_attr_done[dev].store(true);
   return true;
@@ -1047,7 +1056,10 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
   if (down + up > INT32_MAX) return CR_ERR_UNSUPPORTED_SHAPE;
   const int s0 = g_plan(rank, codes, false).smem, s1 = g_plan(rank, false, true).smem;
   const int smem = (s0 > s1 ? s0 : s1) + 1024;
-  auto kern = codes ? lora_grad_mma_kernel<true> : lora_grad_mma_kernel<false>;
+  // a thread's share of a tile's V: 64 rows of up to 32 ranks make one group of four for each thread
+  auto kern = rank <= 32 ? (codes ? lora_grad_mma_kernel<true, 1> : lora_grad_mma_kernel<false, 1>)
+              : rank <= 64 ? (codes ? lora_grad_mma_kernel<true, 2> : lora_grad_mma_kernel<false, 2>)
+                           : (codes ? lora_grad_mma_kernel<true, 4> : lora_grad_mma_kernel<false, 4>);
   kern<<<static_cast<unsigned>(down + up), kGThreads, smem, stream>>>(tx, ty, code_scale, dV, V, adapter, scale, Gdown,
                                                                       Gup, M, K, N, rank, L, splits,
                                                                       static_cast<int>(down), status);
