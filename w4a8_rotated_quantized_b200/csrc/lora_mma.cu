@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(kVThreads, 1)
       for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
         const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
         const uint32_t idesc = idesc_bf16(TM, c * p.rp, false, false);
-        if (pass && !mbar_wait(acc_empty, (pass - 1) & 1, abort)) { ok = false; break; }
+        if (pass && !mbar_sleep(acc_empty, (pass - 1) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(full(s), ph, abort)) { ok = false; break; }
+          if (!mbar_sleep(full(s), ph, abort)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * stage));
           const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * stage + TM * 128));
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
       if (!ok) {
         fail(abort, status);
         volatile int never = 0;
-        if (committed) mbar_wait(last_bar, last_ph, &never);
+        if (committed) mbar_sleep(last_bar, last_ph, &never);
       }
     }
   } else if (warp == 1) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
       for (int d0 = 0; ok && d0 < nd; d0 += p.cap) {
         const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
         for (int kb = kb0; kb < kb1; ++kb, ++f) {
-          if (f >= stages && !mbar_wait(empty(s), ph ^ 1u, abort)) { ok = false; break; }
+          if (f >= stages && !mbar_sleep(empty(s), ph ^ 1u, abort)) { ok = false; break; }
           const uint32_t dst = smem_u32(base + s * stage);
           mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(TM + c * p.rp) * 128u);
           tma_load_2d(dst, &tmap_x, kb * KB, static_cast<int32_t>(m0), full(s));
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
     int pass = 0;
     for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
       const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
-      if (!mbar_wait_warp(acc_full, pass & 1, abort)) { ok = false; break; }
+      if (!mbar_sleep_warp(acc_full, pass & 1, abort)) { ok = false; break; }
       tc_fence_after();
       for (int i = 0; i < c; ++i) {
         const bool hit = mine == list[d0 + i];
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
     if (elect_one()) {
-      bool ok = nd == 0 || mbar_wait(v_ready, 0, abort);
+      bool ok = nd == 0 || mbar_sleep(v_ready, 0, abort);
       tc_fence_after();
       bool committed = false;
       uint32_t last_bar = 0, last_ph = 0, ph = 0;
@@ -414,8 +414,8 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       const uint32_t idesc = idesc_bf16(TM, TN, false, true);
       for (int t = t0; ok && t < t1; ++t) {
         for (int i = 0; i < nd; ++i) {
-          if (!mbar_wait(acc_empty(b), bph, abort)) { ok = false; break; }
-          if (!mbar_wait(u_full(s), ph, abort)) { ok = false; break; }
+          if (!mbar_sleep(acc_empty(b), bph, abort)) { ok = false; break; }
+          if (!mbar_sleep(u_full(s), ph, abort)) { ok = false; break; }
           tc_fence_after();
           const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
 #pragma unroll
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       if (!ok) {
         fail(abort, status);
         volatile int never = 0;
-        if (committed) mbar_wait(last_bar, last_ph, &never);
+        if (committed) mbar_sleep(last_bar, last_ph, &never);
       }
     }
   } else if (warp == 1) {
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       int y = 0;
       uint32_t yph = 0;
       for (int t = t0; t < t1; ++t) {
-        if (t - t0 >= p.nb && !mbar_wait(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
+        if (t - t0 >= p.nb && !mbar_sleep(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
         const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
         if (has_base) {
           mbar_arrive_expect_tx(y_full(y), kYTile);
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       uint32_t ph = 0;
       for (int t = t0; ok && t < t1; ++t) {
         for (int i = 0; i < nd; ++i, ++f) {
-          if (f >= p.nu && !mbar_wait(u_empty(s), ph ^ 1u, abort)) { ok = false; break; }
+          if (f >= p.nu && !mbar_sleep(u_empty(s), ph ^ 1u, abort)) { ok = false; break; }
           const uint32_t ud = smem_u32(base + s * p.u);
           mbar_arrive_expect_tx(u_full(s), p.u);
           tma_load_3d(ud, &tmap_u, t * TN, 0, list[i], u_full(s));
@@ -523,12 +523,12 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     for (int t = t0; ok && t < t1; ++t) {
       uint8_t* box = base + p.off_y + y * kYTile + half * (kYTile / 2);
       uint8_t* tile = box + row * 128;
-      if (!mbar_wait_warp(y_full(y), yph, abort)) { ok = false; break; }
+      if (!mbar_sleep_warp(y_full(y), yph, abort)) { ok = false; break; }
       if (!has_base && mine < 0) {  // no adapter, no base: zeros
         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + (c << 4)) = make_uint4(0, 0, 0, 0);
       }
       for (int i = 0; i < nd; ++i) {
-        if (!mbar_wait_warp(acc_full(b), bph, abort)) { ok = false; break; }
+        if (!mbar_sleep_warp(acc_full(b), bph, abort)) { ok = false; break; }
         tc_fence_after();
         const bool hit = mine == list[i];
         if (__any_sync(0xffffffffu, hit)) {
@@ -588,8 +588,10 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
 // grad: 256 columns of Z against all ranks of one adapter, summed over tiles of 64 tokens.  Z's columns are
 // the product's M side and V its N side, both as they lie in memory (MN-major).  One launch runs both
 // gradients' products (d_down and d_up); token tiles are split over CTAs and the partial sums joined by the
-// finish kernel.  Sixteen warps make the operands (V split into pairs; codes widened to bf16), with V two
-// tiles ahead in registers: an L2 round trip under load is longer than a tile.
+// finish kernel.  Two sets of eight warps make the operands of alternate tiles (V split into pairs; codes
+// widened to bf16): a set's chain of loads, conversions, stores and signals is longer than a tile's time, and
+// each set's next V is on its way in registers meanwhile.  V's rounded values and rests lie side by side as
+// twice as many columns of one product, which costs the same up to 64 columns: the MMAs' issue bounds those.
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int GM = 64;           // tokens of a tile
@@ -599,25 +601,26 @@ constexpr int kZTile = 4 * kZBox;
 constexpr int kRawTile = GM * GC;   // the tile's codes, 16 KB
 constexpr int kMaxGradTiles = 512;  // token tiles of one CTA (64-bit row masks in shared memory)
 struct GPlan {
-  int rp, groups, stage, stages, raws, off_raw, off_mask, off_bar, smem, cols;
+  int rp, vcols, stage, stages, off_raw, off_mask, off_bar, smem, cols;
 };
+constexpr int kRaws = 3;  // tiles of codes on their way
 inline __host__ __device__ GPlan g_plan(int rank, bool codes, bool v16) {
   GPlan p;
   p.rp = round16(rank);
-  p.groups = (p.rp + 63) / 64;
-  p.stage = kZTile + (v16 ? 1 : 2) * p.groups * GM * 128;
-  p.raws = codes ? 3 : 0;
-  const int rest = kSmemMax - kMaxGradTiles * 8 - kBarBytes - p.raws * kRawTile;
-  p.stages = rest / p.stage;
+  p.vcols = v16 ? p.rp : 2 * p.rp;
+  p.stage = kZTile + (p.vcols + 63) / 64 * GM * 128;
+  const int raw = codes ? kRaws * kRawTile : 0;
+  p.stages = (kSmemMax - kMaxGradTiles * 8 - kBarBytes - raw) / p.stage;
   if (p.stages > 4) p.stages = 4;
   p.off_raw = p.stages * p.stage;
-  p.off_mask = p.off_raw + p.raws * kRawTile;
+  p.off_mask = p.off_raw + raw;
   p.off_bar = p.off_mask + kMaxGradTiles * 8;
   p.smem = p.off_bar + kBarBytes;
-  p.cols = tmem_cols_for(2 * p.rp);
+  p.cols = tmem_cols_for(2 * p.vcols);
   return p;
 }
-constexpr int kGWarps = 16;               // make the operands and, at the end, write the sums
+constexpr int kGSet = 8;                  // warps of a set
+constexpr int kGWarps = 2 * kGSet;        // make the operands and, at the end, write the sums
 constexpr int kGThreads = 32 * (kGWarps + 2);  // then the MMA's and TMA's warps
 
 // Four signed bytes -> bf16 pairs, exactly: the low 7 bits put into the mantissa of 128, less 128, or less
@@ -665,8 +668,8 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4; ++s) {
       mbar_init(z_full(s), 1);
-      mbar_init(raw_empty(s), kGWarps);
-      mbar_init(ready(s), kGWarps);
+      mbar_init(raw_empty(s), kGSet);
+      mbar_init(ready(s), kGSet);
       mbar_init(empty(s), 1);
     }
     mbar_init(acc_full, 1);
@@ -701,22 +704,19 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       bool ok = true, committed = false;
       uint32_t ph = 0, last_bar = 0, last_ph = 0;
       int s = 0;
-      const uint32_t idesc = idesc_bf16(128, p.rp, true, true);
+      const uint32_t idesc = idesc_bf16(128, p.vcols, true, true);
       for (int i = next_tile(0); i < nt; i = next_tile(i + 1)) {
-        if (!mbar_wait(ready(s), ph, abort)) { ok = false; break; }
+        if (!mbar_sleep(ready(s), ph, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t z = smem_u32(base + s * p.stage);
   #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kZBox, kZBox);
-  #pragma unroll
-          for (int h = 0; h < (kV16 ? 1 : 2); ++h) {
-            const uint64_t dv = sw128_mnmajor_desc(z + kZTile + h * p.groups * GM * 128, GM * 128);
-  #pragma unroll
-            for (int kk = 0; kk < GM / 16; ++kk)
-              umma_f16_ss(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 128u * kk, idesc,
-                                (committed || h || kk) ? 1u : 0u);
-          }
+            const uint64_t dv = sw128_mnmajor_desc(z + kZTile, GM * 128);
+#pragma unroll
+          for (int kk = 0; kk < GM / 16; ++kk)
+            umma_f16_ss(tmem + static_cast<uint32_t>(half * p.vcols), dz + 128u * kk, dv + 128u * kk, idesc,
+                        (committed || kk) ? 1u : 0u);
         }
         umma_commit(empty(s));
         last_bar = empty(s);
@@ -728,7 +728,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       if (!ok) {
         fail(abort, status);
         volatile int never = 0;
-        if (committed) mbar_wait(last_bar, last_ph, &never);
+        if (committed) mbar_sleep(last_bar, last_ph, &never);
       }
     }
   } else if (warp == kGWarps + 1) {
@@ -737,9 +737,9 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       bool ok = true;
       int s = 0, f = 0;
       uint32_t ph = 0;
-      const int ring = kCodes ? p.raws : p.stages;
+      const int ring = kCodes ? kRaws : p.stages;
       for (int i = next_tile(0); i < nt; i = next_tile(i + 1), ++f) {
-        if (f >= ring && !mbar_wait(kCodes ? raw_empty(s) : empty(s), ph ^ 1u, abort)) { ok = false; break; }
+        if (f >= ring && !mbar_sleep(kCodes ? raw_empty(s) : empty(s), ph ^ 1u, abort)) { ok = false; break; }
         const int y = (t0 + i) * GM;
         if constexpr (kCodes) {
           mbar_arrive_expect_tx(z_full(s), kRawTile);
@@ -759,14 +759,18 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     }
   } else {
     // ---------------------------------------------------------------- operands
-    const int tid = threadIdx.x;
-    int at[kN], from[kN];  // place in the V operand (its row in the bits above 15); offset from the tile's V
+    const int set = warp / kGSet, sw = warp % kGSet;
+    const int tid = threadIdx.x - set * 32 * kGSet;
+    // places of a thread's fours in the V operand, as values (its row in the bits above 15) and as rests;
+    // offsets from the tile's V.  A four past the tile's rows goes nowhere.
+    int at[kN], rest[kV16 ? 1 : kN], from[kN];
+    auto place = [](int r, int c) { return (c >> 6) * GM * 128 + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 4) * 2; };
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int per = p.rp >> 2, e = tid + 32 * kGWarps * k;
+      const int per = p.rp >> 2, e = tid + 32 * kGSet * k;
       const int r = e / per, j = 4 * (e - r * per);
-      // an entry past the tile's rows goes nowhere
-      at[k] = r < GM ? (j >> 6) * GM * 128 + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 4) * 2 + (r << 16) : -1;
+      at[k] = r < GM ? place(r, j) + (r << 16) : -1;
+      if constexpr (!kV16) rest[k] = place(r, p.rp + j);
       from[k] = r < GM && j < rank ? r * rank + j : -1;
     }
     struct Ahead {
@@ -794,30 +798,31 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       }
     };
     bool ok = true;
-    int s = 0, rs = 0, f = 0;
+    // the set's tiles are every other one: its stage of each ring, with the rounds that it has gone
+    int s = set, rs = set, f = set;
     uint32_t ph = 0, rph = 0;
     auto make = [&](int i, Ahead& x) {
       uint8_t* z = base + s * p.stage;
       const unsigned long long rows = mask[i];
       if constexpr (kCodes) {
         // codes are finite: those of other adapters' rows meet zeros of V
-        if (f >= p.stages && !mbar_wait_warp(empty(s), ph ^ 1u, abort)) return false;
-        if (!mbar_wait_warp(z_full(rs), rph, abort)) return false;
+        if (f >= p.stages && !mbar_sleep_warp(empty(s), ph ^ 1u, abort)) return false;
+        if (!mbar_sleep_warp(z_full(rs), rph, abort)) return false;
         const uint8_t* raw = base + p.off_raw + rs * kRawTile;
 #pragma unroll
-        for (int k = 0; k < GM / kGWarps; ++k) {  // a row of the tile for each warp
-          const int r = kGWarps * k + warp;
+        for (int k = 0; k < GM / kGSet; ++k) {  // a row of the tile for each warp
+          const int r = kGSet * k + sw;
           const uint2 w = *reinterpret_cast<const uint2*>(raw + r * GC + 8 * lane);
           const uint2 lo = bytes_to_bf16(w.x), hi = bytes_to_bf16(w.y);
           *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
               make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
       } else {
-        if (!mbar_wait_warp(z_full(s), ph, abort)) return false;
+        if (!mbar_sleep_warp(z_full(s), ph, abort)) return false;
         if (~rows) {
 #pragma unroll 1
-          for (int k = 0; k < GM / kGWarps; ++k) {
-            const int r = kGWarps * k + warp;
+          for (int k = 0; k < GM / kGSet; ++k) {
+            const int r = kGSet * k + sw;
             if (!(rows >> r & 1))
               *reinterpret_cast<uint4*>(z + (lane >> 3) * kZBox + r * 128 + ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
@@ -841,7 +846,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
           split_bf16(v.x, v.y, hi[0], lo[0]);
           split_bf16(v.z, v.w, hi[1], lo[1]);
           *reinterpret_cast<uint2*>(d) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(d + p.groups * GM * 128) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(z + kZTile + rest[k]) = make_uint2(lo[0], lo[1]);
         }
       }
       fence_proxy_async_smem();
@@ -850,41 +855,42 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         mbar_arrive(ready(s));
         if (kCodes) mbar_arrive(raw_empty(rs));
       }
-      ++f;
-      if (++s == p.stages) { s = 0; ph ^= 1u; }
-      if (kCodes && ++rs == p.raws) { rs = 0; rph ^= 1u; }
+      f += 2;
+      if ((s += 2) >= p.stages) { s -= p.stages; ph ^= 1u; }
+      if (kCodes && (rs += 2) >= kRaws) { rs -= kRaws; rph ^= 1u; }
       return true;
     };
-    Ahead x, y;
-    int i = next_tile(0), i2 = next_tile(i + 1);
+    Ahead x;
+    const int first = next_tile(0);
+    int i = set ? next_tile(first + 1) : first;
     fetch(i, x);
-    fetch(i2, y);
     while (i < nt) {
       if (!(ok = make(i, x))) break;
-      i = next_tile(i2 + 1);
+      i = next_tile(next_tile(i + 1) + 1);
       fetch(i, x);
-      if (i2 >= nt) break;
-      if (!(ok = make(i2, y))) break;
-      i2 = next_tile(i + 1);
-      fetch(i2, y);
     }
     // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
     const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 ranks
     const int c = c0 + 128 * half + 32 * q + lane;
     const float sc = __ldg(scale + a);
     float* out = G + (static_cast<int64_t>(split) * L + a) * rank * C + c;
-    if (ok && f > 0) {
-      if (mbar_wait_warp(acc_full, 0, abort)) {
+    if (ok && first < nt) {
+      if (mbar_sleep_warp(acc_full, 0, abort)) {
         tc_fence_after();
 #pragma unroll 1
         for (int j = 16 * part; j < p.rp; j += 32) {
-          uint32_t r[16];
-          tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * p.rp + j), r);
+          uint32_t r[16], l[16];
+          const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * p.vcols + j);
+          tmem_ld16(src, r);
+          if constexpr (!kV16) tmem_ld16(src + static_cast<uint32_t>(p.rp), l);
           tmem_ld_wait();
           if (c < C) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (j + e < rank) out[static_cast<int64_t>(j + e) * C] = sc * __uint_as_float(r[e]);
+            for (int e = 0; e < 16; ++e) {
+              float t = __uint_as_float(r[e]);
+              if constexpr (!kV16) t += __uint_as_float(l[e]);
+              if (j + e < rank) out[static_cast<int64_t>(j + e) * C] = sc * t;
+            }
           }
         }
       } else {
@@ -933,9 +939,11 @@ bool set_attrs() {
       cudaFuncSetAttribute(lora_grad_mma_kernel<false, 1>, attr, most) != cudaSuccess ||
       cudaFuncSetAttribute(lora_grad_mma_kernel<false, 2>, attr, most) != cudaSuccess ||
       cudaFuncSetAttribute(lora_grad_mma_kernel<false, 4>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<false, 8>, attr, most) != cudaSuccess ||
       cudaFuncSetAttribute(lora_grad_mma_kernel<true, 1>, attr, most) != cudaSuccess ||
       cudaFuncSetAttribute(lora_grad_mma_kernel<true, 2>, attr, most) != cudaSuccess ||
-      cudaFuncSetAttribute(lora_grad_mma_kernel<true, 4>, attr, most) != cudaSuccess)
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true, 4>, attr, most) != cudaSuccess ||
+      cudaFuncSetAttribute(lora_grad_mma_kernel<true, 8>, attr, most) != cudaSuccess)
     return false;
   g_attr_done[dev].store(true);
   return true;
@@ -1056,10 +1064,11 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
   if (down + up > INT32_MAX) return CR_ERR_UNSUPPORTED_SHAPE;
   const int s0 = g_plan(rank, codes, false).smem, s1 = g_plan(rank, false, true).smem;
   const int smem = (s0 > s1 ? s0 : s1) + 1024;
-  // a thread's share of a tile's V: 64 rows of up to 32 ranks make one group of four for each thread
-  auto kern = rank <= 32 ? (codes ? lora_grad_mma_kernel<true, 1> : lora_grad_mma_kernel<false, 1>)
-              : rank <= 64 ? (codes ? lora_grad_mma_kernel<true, 2> : lora_grad_mma_kernel<false, 2>)
-                           : (codes ? lora_grad_mma_kernel<true, 4> : lora_grad_mma_kernel<false, 4>);
+  // a thread's share of a tile's V: 64 rows of 16 ranks make one group of four for each thread of a set
+  auto kern = rank <= 16   ? (codes ? lora_grad_mma_kernel<true, 1> : lora_grad_mma_kernel<false, 1>)
+              : rank <= 32 ? (codes ? lora_grad_mma_kernel<true, 2> : lora_grad_mma_kernel<false, 2>)
+              : rank <= 64 ? (codes ? lora_grad_mma_kernel<true, 4> : lora_grad_mma_kernel<false, 4>)
+                           : (codes ? lora_grad_mma_kernel<true, 8> : lora_grad_mma_kernel<false, 8>);
   kern<<<static_cast<unsigned>(down + up), kGThreads, smem, stream>>>(tx, ty, code_scale, dV, V, adapter, scale, Gdown,
                                                                       Gup, M, K, N, rank, L, splits,
                                                                       static_cast<int>(down), status);
