@@ -41,8 +41,19 @@ int v_splits(int M, int K, int rank) {
   return M <= cr::kLoraRowsMaxM ? cr::lora_row_splits(M > 0 ? M : 1, K, rank, kSizingSms) : 1;
 }
 
-int grad_splits(int M, int N, int K, int rank, int L) {
-  return cr::lora_grad_splits(M > 0 ? M : 1, K, N, rank, L, kSizingSms);
+struct GradSplits {
+  int down = 0, up = 0;
+};
+GradSplits grad_splits(int M, int N, int K, int rank, int L, bool codes) {
+  GradSplits g;
+  cr::lora_grad_splits(M > 0 ? M : 1, K, N, rank, L, codes, kSizingSms, &g.down, &g.up);
+  return g;
+}
+
+size_t backward_bytes(int M, int N, int K, int rank, int L, bool codes) {
+  const GradSplits g = grad_splits(M, N, K, rank, L, codes);
+  const int64_t per = static_cast<int64_t>(L) * rank;
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + bytes_f32(g.down * per * K) + bytes_f32(g.up * per * N);
 }
 
 cr_status check_rows(const void* p, int64_t ld, int cols) {
@@ -103,8 +114,10 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
 
 size_t cr_lora_backward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  const int64_t per = static_cast<int64_t>(grad_splits(M, N, K, rank, num_adapters)) * num_adapters * rank;
-  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + bytes_f32(per * K) + bytes_f32(per * N);
+  // X as rows or as a checkpoint: the larger of the two
+  const size_t rows = backward_bytes(M, N, K, rank, num_adapters, false);
+  const size_t codes = backward_bytes(M, N, K, rank, num_adapters, true);
+  return rows > codes ? rows : codes;
 }
 
 cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* codes,
@@ -126,7 +139,7 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   if (!aligned(codes, 16) || !aligned(code_scales, 4) || !aligned(V, 8) || !aligned(adapter, 4) || !aligned(down, 16) ||
       !aligned(up, 16) || !aligned(scale, 4) || !aligned(d_down, 16) || !aligned(d_up, 16))
     return CR_ERR_MISALIGNED;
-  if (!workspace || workspace_bytes < cr_lora_backward_workspace_size(M, N, K, rank, num_adapters) ||
+  if (!workspace || workspace_bytes < backward_bytes(M, N, K, rank, num_adapters, codes != nullptr) ||
       !aligned(workspace, 256))
     return CR_ERR_WORKSPACE;
   int nsm = 0;
@@ -142,9 +155,9 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   }
   uint8_t* w = static_cast<uint8_t*>(workspace) + kWsHead;
   float* dv = reinterpret_cast<float*>(w);
-  const int parts = grad_splits(M, N, K, rank, L);
+  const GradSplits parts = grad_splits(M, N, K, rank, L, codes != nullptr);
   float* gd = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank));
-  float* gu = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(gd) + bytes_f32(parts * nd));
+  float* gu = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(gd) + bytes_f32(parts.down * nd));
   int* status = ws_status(workspace);
   if (dX || d_down) {
     st = static_cast<cr_status>(cr::launch_lora_v_mma(static_cast<const uint16_t*>(dY), lddy, adapter,
@@ -163,9 +176,9 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   if (d_down || d_up) {
     st = static_cast<cr_status>(cr::launch_lora_grad_mma(
         codes ? codes : X, ldx, code_scales, dY, lddy, dv, static_cast<const uint16_t*>(V), adapter, scale,
-        d_down ? gd : nullptr, d_up ? gu : nullptr, M, K, N, rank, L, parts, status, s));
+        d_down ? gd : nullptr, d_up ? gu : nullptr, M, K, N, rank, L, parts.down, parts.up, status, s));
     if (st != CR_OK) return st;
-    if (cr::launch_lora_grad_finish(gd, gu, parts, static_cast<int64_t>(L) * rank, K, N, static_cast<uint16_t*>(d_down),
+    if (cr::launch_lora_grad_finish(gd, gu, parts.down, parts.up, static_cast<int64_t>(L) * rank, K, N, static_cast<uint16_t*>(d_down),
                                     static_cast<uint16_t*>(d_up), codes != nullptr, s) != cudaSuccess)
       return CR_ERR_CUDA;
   }

@@ -152,7 +152,7 @@ __device__ __forceinline__ void add_parts(const float* __restrict__ src, int par
 // The gradients' partial sums joined and rounded.  The first `rot_blocks` blocks take slices of 256 values
 // of the rotated d_down, the rest eight values a thread of what is left: d_down unrotated, then d_up.
 __global__ void __launch_bounds__(32 * kWarps)
-    lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts, int64_t n_down,
+    lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts_down, int parts_up, int64_t n_down,
                             int64_t n_up, uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up, int rot_blocks) {
   if (static_cast<int>(blockIdx.x) < rot_blocks) {
     const int64_t u = lane_unit();
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float v[8];
-      add_parts(Gdown + u * 256 + 32 * (k ^ k0) + 8 * l, in ? parts : 0, n_down, v);
+      add_parts(Gdown + u * 256 + 32 * (k ^ k0) + 8 * l, in ? parts_down : 0, n_down, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (k < 4) P.w[8 * (k & 3) + e].x = v[e]; else P.w[8 * (k & 3) + e].y = v[e];
@@ -176,14 +176,14 @@ __global__ void __launch_bounds__(32 * kWarps)
   float v[8];
   if (!rot_blocks) {
     if (i < n_down) {
-      add_parts(Gdown + i, parts, n_down, v);
+      add_parts(Gdown + i, parts_down, n_down, v);
       *reinterpret_cast<uint4*>(d_down + i) = narrow8(v);
       return;
     }
     i -= n_down;
   }
   if (i >= n_up) return;
-  add_parts(Gup + i, parts, n_up, v);
+  add_parts(Gup + i, parts_up, n_up, v);
   *reinterpret_cast<uint4*>(d_up + i) = narrow8(v);
 }
 
@@ -217,13 +217,13 @@ cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16
   return cudaGetLastError();
 }
 
-cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts, int64_t rows, int K, int N,
+cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts_down, int parts_up, int64_t rows, int K, int N,
                                     uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream) {
   const int64_t n_down = d_down ? rows * K : 0, n_up = d_up ? rows * N : 0;
   const unsigned rot = rotate && d_down ? unit_blocks(n_down / 256) : 0;
   const int64_t plain = (rot ? 0 : n_down) + n_up;
   const unsigned blocks = rot + static_cast<unsigned>((plain + 256 * kWarps - 1) / (256 * kWarps));
-  lora_grad_finish_kernel<<<blocks, 32 * kWarps, 0, stream>>>(Gdown, Gup, parts, n_down, n_up, d_down, d_up,
+  lora_grad_finish_kernel<<<blocks, 32 * kWarps, 0, stream>>>(Gdown, Gup, parts_down, parts_up, n_down, n_up, d_down, d_up,
                                                               static_cast<int>(rot));
   return cudaGetLastError();
 }

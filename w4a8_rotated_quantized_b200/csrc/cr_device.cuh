@@ -134,6 +134,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Warp-wide: every lane waits.  (A wait by one lane whose answer is broadcast may leave the warp split behind
+// it, and all that follows is then issued twice.)
 __device__ __forceinline__ bool mbar_sleep_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_sleep(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
@@ -379,13 +381,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
+// The two halves of it: the first says that this thread has come so far, the second waits for all others'.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_cluster_f4(uint32_t cluster_addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(a), "f"(b), "f"(c), "f"(d)
                : "memory");
-  return v;
 }
 // Arrive on a barrier that may live in the peer CTA (address from mapa_shared).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {

@@ -178,17 +178,17 @@ int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, co
 int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up, const float* scale,
                       const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, int M, int N, int rank, int L,
                       int* status, int num_sms, cudaStream_t stream);
-// Both gradients' products in one launch: partial sums Gdown float32 [splits, L, rank, K] of scale[a] * sum
+// Both gradients' products in one launch: partial sums Gdown float32 [splits_down, L, rank, K] of scale[a] * sum
 // over the adapter's rows of dV^T X (X bf16 rows, or codes with code_scale: then in the checkpoint's rotated
-// basis) and Gup [splits, L, rank, N] of V^T dY; either may be null.  dV float32, V bf16, [M, rank].
-int lora_grad_splits(int M, int K, int N, int rank, int L, int num_sms);
+// basis) and Gup [splits_up, L, rank, N] of V^T dY; either may be null.  dV float32, V bf16, [M, rank].
+void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_sms, int* down, int* up);
 int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, const void* dY, int64_t lddy,
                          const float* dV, const uint16_t* V, const int32_t* adapter, const float* scale, float* Gdown,
-                         float* Gup, int M, int K, int N, int rank, int L, int splits, int* status,
+                         float* Gup, int M, int K, int N, int rank, int L, int splits_down, int splits_up, int* status,
                          cudaStream_t stream);
 // The partial sums added in order and rounded: d_down [rows, K] (rotated by H256 if `rotate`) and d_up
 // [rows, N], rows = L * rank; either may be null.
-cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts, int64_t rows, int K, int N,
+cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts_down, int parts_up, int64_t rows, int K, int N,
                                     uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream);
 cudaError_t launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes, float* scales,
                              cudaStream_t stream);

@@ -61,34 +61,35 @@ __device__ __forceinline__ void grace() {
 }
 
 // The adapters of the tile's 128 rows into ids[] (-1: none, rows past M too) and the distinct ones, in order
-// of first appearance, into list[]; returns how many.  Called by all threads of the block (at least 128).
+// of first appearance, into list[]; returns how many.  Warps 2-5 do it, a thread for each row; `threads`
+// threads call it (these and others) and meet at barrier 3.
 __device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter, int64_t m0, int M, int L, int* ids,
-                                             int* list, int* counts) {
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  if (t < TM) ids[t] = m0 + t < M ? row_adapter(adapter, m0 + t, L) : -1;
+                                             int* list, int* counts, int threads) {
+  const int t = static_cast<int>(threadIdx.x) - 64, warp = t >> 5, lane = t & 31;
+  const bool mine = t >= 0 && t < TM;
+  if (mine) ids[t] = m0 + t < M ? row_adapter(adapter, m0 + t, L) : -1;
   if (!adapter) {
     if (t == 0) list[0] = 0;
-    __syncthreads();
+    named_bar_sync(3, threads);
     return 1;
   }
-  __syncthreads();
+  named_bar_sync(3, threads);
   bool first = false;
   uint32_t firsts = 0;
-  if (t < TM) {
+  if (mine) {
     const int a = ids[t];
     const uint32_t same = __match_any_sync(0xffffffffu, a);
     first = a >= 0 && __ffs(same) - 1 == lane;
     // against the rows of the warps before, four at a time
-#pragma unroll
-    for (int i = 0; i < TM - 32; i += 4)
-      if (i < 32 * warp) {
-        const int4 o = *reinterpret_cast<const int4*>(ids + i);
-        first = first && o.x != a && o.y != a && o.z != a && o.w != a;
-      }
+#pragma unroll 4
+    for (int i = 0; i < 32 * warp; i += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(ids + i);
+      first = first && o.x != a && o.y != a && o.z != a && o.w != a;
+    }
     firsts = __ballot_sync(0xffffffffu, first);
     if (lane == 0) counts[warp] = __popc(firsts);
   }
-  __syncthreads();
+  named_bar_sync(3, threads);
   int before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < TM / 32; ++w) {
@@ -96,13 +97,13 @@ __device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter
     all += counts[w];
   }
   if (first) list[before + __popc(firsts & ((1u << lane) - 1))] = ids[t];
-  __syncthreads();
+  named_bar_sync(3, threads);
   return all;
 }
 
 // ---------------------------------------------------------------------------------------------------
 // v: 128 tokens x (up to 256 / rank adapters side by side); the sum over k split over a cluster's CTAs,
-// whose partial sums are added in rank order through distributed shared memory.
+// whose partial sums go to the CTA that adds up their row, in rank order, through distributed shared memory.
 // ---------------------------------------------------------------------------------------------------
 
 struct VPlan {
@@ -125,7 +126,7 @@ inline __host__ __device__ VPlan v_plan(int rank, int L) {
   p.off_list = p.off_part + part;
   p.off_bar = p.off_list + kListBytes;
   p.smem = p.off_bar + kBarBytes;
-  p.cols = tmem_cols_for(p.cap * p.rp);
+  p.cols = tmem_cols_for(p.cap * p.rp + 16);  // the epilogue reads 32 columns at a time
   return p;
 }
 
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 148);
   int* counts = reinterpret_cast<int*>(base + p.off_bar + 160);
 
+  cluster_arrive();  // this CTA has started: its shared memory may be written to
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = CR_OK;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kVStages; ++s) {
@@ -172,14 +174,16 @@ __global__ void __launch_bounds__(kVThreads, 1)
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
   }
-  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts);
+  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts, kVThreads);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_wait();
   const uint32_t tmem = *slot;
 
   const int stage = (TM + (nd < p.cap ? nd : p.cap) * p.rp) * 128;
   const int stages = p.ring / stage < kVStages ? p.ring / stage : kVStages;
+  const int rows = TM / splits;  // that this CTA adds up
   const int nkb = (K + KB - 1) / KB;
   const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
@@ -245,9 +249,10 @@ __global__ void __launch_bounds__(kVThreads, 1)
     const int q = warp & 3;
     const int row = 32 * q + lane;
     const int mine = ids[row];
-    float* out = part + row * p.part_ld;
+    // this split's place for the row, in the CTA that adds up the row
+    const uint32_t out = mapa_shared(smem_u32(part) + 4u * ((split * rows + row % rows) * p.part_ld), row / rows);
     if (mine < 0)
-      for (int j = 0; j < p.rp; j += 4) *reinterpret_cast<float4*>(out + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < p.rp; j += 4) st_shared_cluster_f4(out + 4u * j, 0.f, 0.f, 0.f, 0.f);
     bool ok = true;
     int pass = 0;
     for (int d0 = 0; ok && d0 < nd; d0 += p.cap, ++pass) {
@@ -257,15 +262,17 @@ __global__ void __launch_bounds__(kVThreads, 1)
       for (int i = 0; i < c; ++i) {
         const bool hit = mine == list[d0 + i];
         if (!__any_sync(0xffffffffu, hit)) continue;
-        for (int j = 0; j < p.rp; j += 16) {
-          uint32_t r[16];
-          tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(i * p.rp + j), r);
+#pragma unroll 1
+        for (int j = 0; j < p.rp; j += 32) {
+          uint32_t r[32];  // (past the last 16 ranks: columns that nobody keeps)
+          tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(i * p.rp + j), r);
           tmem_ld_wait();
           if (hit) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(out + j + e) = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
-                                                                    __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+            for (int e = 0; e < 32; e += 4)
+              if (e < 16 || j + 16 < p.rp)
+                st_shared_cluster_f4(out + 4u * (j + e), __uint_as_float(r[e]), __uint_as_float(r[e + 1]),
+                                     __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
           }
         }
       }
@@ -279,37 +286,30 @@ __global__ void __launch_bounds__(kVThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // every split's partial sums are in its shared memory
+  cluster_sync();  // every split's partial sums have arrived
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, p.cols);
   }
-  // this CTA's share of the rows: the splits' sums added in order
-  const int rows = TM / splits, groups = rank >> 2;
-  const uint32_t part_addr = smem_u32(part);
+  // this CTA's rows: the splits' sums added in order
+  const int groups = rank >> 2;
   for (int i = threadIdx.x; i < rows * groups; i += kVThreads) {
-    const int row = split * rows + i / groups, j = 4 * (i % groups);
-    if (m0 + row >= M) break;
-    float4 u[kVMostSplits];  // all on their way before the first is added
-#pragma unroll
-    for (int c = 0; c < kVMostSplits; ++c) {
-      u[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < splits) u[c] = ld_shared_cluster_f4(mapa_shared(part_addr + 4u * (row * p.part_ld + j), c));
+    const int r = i / groups, j = 4 * (i - r * groups);
+    const int64_t m = m0 + split * rows + r;
+    if (m >= M) break;
+    const float* src = part + r * p.part_ld + j;
+    float4 t = *reinterpret_cast<const float4*>(src);
+#pragma unroll 4
+    for (int c = 1; c < splits; ++c) {
+      const float4 u = *reinterpret_cast<const float4*>(src + c * rows * p.part_ld);
+      t.x += u.x;
+      t.y += u.y;
+      t.z += u.z;
+      t.w += u.w;
     }
-    float4 t = u[0];
-#pragma unroll
-    for (int c = 1; c < kVMostSplits; ++c) {
-      t.x += u[c].x;
-      t.y += u[c].y;
-      t.z += u[c].z;
-      t.w += u[c].w;
-    }
-    *reinterpret_cast<float4*>(V + (m0 + row) * rank + j) = t;
-    if (Vout)
-      *reinterpret_cast<uint2*>(Vout + (m0 + row) * rank + j) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+    *reinterpret_cast<float4*>(V + m * rank + j) = t;
+    if (Vout) *reinterpret_cast<uint2*>(Vout + m * rank + j) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
   }
-  __syncwarp();
-  cluster_sync();  // nobody reads this CTA's shared memory any more
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -396,11 +396,12 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
   }
-  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  // (base tiles need no adapters: their warp goes on)
+  const int nd = warp == 1 ? 0 : tile_adapters(adapter, m0, M, L, ids, list, counts, kYMmaThreads - 32);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -777,23 +778,26 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       float4 v[kN];  // bf16: bits in x, y
       float cs[kCodes ? kN : 1];
     };
+    const uint32_t* mask32 = reinterpret_cast<const uint32_t*>(mask);
     auto fetch = [&](int i, Ahead& x) {
       if (i >= nt) return;
-      const unsigned long long rows = mask[i];
       const int64_t m0 = static_cast<int64_t>(t0 + i) * GM;
+      const uint8_t* v = static_cast<const uint8_t*>(V) + m0 * rank * (kV16 ? 2 : 4);
+      const float* cs = kCodes ? code_scale + m0 * (C >> 8) + (c0 >> 8) : nullptr;
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         x.v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if constexpr (kCodes) x.cs[k] = 0.f;
         const int r = at[k] >> 16;
-        if (from[k] < 0 || !(rows >> r & 1)) continue;
-        if constexpr (kV16) {
-          const uint2 w = ldg_here_u2(static_cast<const uint16_t*>(V) + m0 * rank + from[k]);
-          x.v[k].x = __uint_as_float(w.x);
-          x.v[k].y = __uint_as_float(w.y);
-        } else {
-          x.v[k] = ldg_here_f4(static_cast<const float*>(V) + m0 * rank + from[k]);
-          if constexpr (kCodes) x.cs[k] = ldg_here_f1(code_scale + (m0 + r) * (C >> 8) + (c0 >> 8));
+        if (from[k] >= 0 && (mask32[2 * i + (r >> 5)] >> (r & 31) & 1)) {
+          if constexpr (kV16) {
+            const uint2 w = ldg_here_u2(v + from[k] * 2);
+            x.v[k].x = __uint_as_float(w.x);
+            x.v[k].y = __uint_as_float(w.y);
+          } else {
+            x.v[k] = ldg_here_f4(reinterpret_cast<const float*>(v) + from[k]);
+            if constexpr (kCodes) x.cs[k] = ldg_here_f1(cs + r * (C >> 8));
+          }
         }
       }
     };
@@ -803,7 +807,6 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     uint32_t ph = 0, rph = 0;
     auto make = [&](int i, Ahead& x) {
       uint8_t* z = base + s * p.stage;
-      const unsigned long long rows = mask[i];
       if constexpr (kCodes) {
         // codes are finite: those of other adapters' rows meet zeros of V
         if (f >= p.stages && !mbar_sleep_warp(empty(s), ph ^ 1u, abort)) return false;
@@ -819,6 +822,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         }
       } else {
         if (!mbar_sleep_warp(z_full(s), ph, abort)) return false;
+        const unsigned long long rows = mask[i];
         if (~rows) {
 #pragma unroll 1
           for (int k = 0; k < GM / kGSet; ++k) {
@@ -917,11 +921,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
                          const float* __restrict__ code_scale, const float* __restrict__ dV,
                          const uint16_t* __restrict__ V, const int32_t* __restrict__ adapter,
                          const float* __restrict__ scale, float* __restrict__ Gdown, float* __restrict__ Gup, int M,
-                         int K, int N, int rank, int L, int splits, int down_blocks, int* __restrict__ status) {
+                         int K, int N, int rank, int L, int splits_down, int splits_up, int down_blocks,
+                         int* __restrict__ status) {
   if (static_cast<int>(blockIdx.x) < down_blocks)
-    grad_body<kCodes, false, kN>(tmap_x, code_scale, dV, adapter, scale, Gdown, M, K, rank, L, splits, blockIdx.x, status);
+    grad_body<kCodes, false, kN>(tmap_x, code_scale, dV, adapter, scale, Gdown, M, K, rank, L, splits_down, blockIdx.x,
+                                status);
   else
-    grad_body<false, true, kN>(tmap_dy, nullptr, V, adapter, scale, Gup, M, N, rank, L, splits, blockIdx.x - down_blocks,
+    grad_body<false, true, kN>(tmap_dy, nullptr, V, adapter, scale, Gup, M, N, rank, L, splits_up, blockIdx.x - down_blocks,
                            status);
 }
 
@@ -1026,29 +1032,39 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
              : CR_ERR_CUDA;
 }
 
-// Token splits of the gradient products.  In units of one tile's time (about half a microsecond): rounds of
-// CTAs, each with its tiles and about five tiles' worth of setting up and writing out, and the partial sums'
-// way to memory and back (about 2.5 MB a unit).
-int lora_grad_splits(int M, int K, int N, int rank, int L, int num_sms) {
-  const int64_t items = (static_cast<int64_t>((K + GC - 1) / GC) + (N + GC - 1) / GC) * L;
+// Token splits of the two gradient products, down's and up's.  In units of one bf16 tile's time on an SM (about
+// a third of a microsecond; a tile of codes takes about 1.5): each CTA has its tiles and about eight tiles'
+// worth of setting up and writing out; the partial sums go to memory and back (about 1.6 MB a unit).  Up's
+// splits follow from down's so that both kinds of CTA take as long.
+void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_sms, int* down, int* up) {
+  const int64_t cd = static_cast<int64_t>((K + GC - 1) / GC) * L, cu = static_cast<int64_t>((N + GC - 1) / GC) * L;
   const int tiles = (M + GM - 1) / GM;
-  const int least = (tiles + kMaxGradTiles - 1) / kMaxGradTiles;
-  int best = least < 1 ? 1 : least;
-  int64_t best_cost = INT64_MAX;
-  for (int s = best; s <= tiles && s <= best + 31; ++s) {
-    const int64_t rounds = (items * s + num_sms - 1) / num_sms;
-    const int64_t cost = rounds * ((tiles + s - 1) / s + 5) + static_cast<int64_t>(s) * L * rank * (K + N) / 312500;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
+  const int least = tiles > kMaxGradTiles ? (tiles + kMaxGradTiles - 1) / kMaxGradTiles : 1;
+  int64_t best = INT64_MAX;
+  *down = *up = least;
+  for (int sd = least; sd <= least + 15 && sd <= (tiles > least ? tiles : least); ++sd) {
+    const int64_t td = ((tiles + sd - 1) / sd + 8) * (codes ? 6 : 4);  // quarters of a unit
+    int64_t room = td / 4 - 8;
+    if (room < 1) room = 1;
+    int64_t su = (tiles + room - 1) / room;
+    if (su < least) su = least;
+    if (su > least + 15) su = least + 15;
+    const int64_t tu = ((tiles + su - 1) / su + 8) * 4;
+    const int64_t most = td > tu ? td : tu, ctas = cd * sd + cu * su;
+    // one round: the longest CTA; more: the work spread over the SMs and half of a CTA left over
+    const int64_t time = ctas <= num_sms ? most : (cd * sd * td + cu * su * tu) / num_sms + most / 2;
+    const int64_t cost = time + (sd * K + su * N) * static_cast<int64_t>(L) * rank / 50000;
+    if (cost < best) {
+      best = cost;
+      *down = sd;
+      *up = static_cast<int>(su);
     }
   }
-  return best;
 }
 
 int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, const void* dY, int64_t lddy,
                          const float* dV, const uint16_t* V, const int32_t* adapter, const float* scale, float* Gdown,
-                         float* Gup, int M, int K, int N, int rank, int L, int splits, int* status,
+                         float* Gup, int M, int K, int N, int rank, int L, int splits_down, int splits_up, int* status,
                          cudaStream_t stream) {
   if (!set_attrs()) return CR_ERR_CUDA;
   const bool codes = code_scale != nullptr;
@@ -1059,8 +1075,8 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
                        : make_tmap_2d(&tx, kBf, X, M, K, static_cast<uint64_t>(ldx) * 2, 64, GM, kSw128, kL2)))
     return CR_ERR_CUDA;
   if (Gup && !make_tmap_2d(&ty, kBf, dY, M, N, static_cast<uint64_t>(lddy) * 2, 64, GM, kSw128, kL2)) return CR_ERR_CUDA;
-  const int64_t down = Gdown ? static_cast<int64_t>((K + GC - 1) / GC) * L * splits : 0;
-  const int64_t up = Gup ? static_cast<int64_t>((N + GC - 1) / GC) * L * splits : 0;
+  const int64_t down = Gdown ? static_cast<int64_t>((K + GC - 1) / GC) * L * splits_down : 0;
+  const int64_t up = Gup ? static_cast<int64_t>((N + GC - 1) / GC) * L * splits_up : 0;
   if (down + up > INT32_MAX) return CR_ERR_UNSUPPORTED_SHAPE;
   const int s0 = g_plan(rank, codes, false).smem, s1 = g_plan(rank, false, true).smem;
   const int smem = (s0 > s1 ? s0 : s1) + 1024;
@@ -1070,7 +1086,7 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
               : rank <= 64 ? (codes ? lora_grad_mma_kernel<true, 4> : lora_grad_mma_kernel<false, 4>)
                            : (codes ? lora_grad_mma_kernel<true, 8> : lora_grad_mma_kernel<false, 8>);
   kern<<<static_cast<unsigned>(down + up), kGThreads, smem, stream>>>(tx, ty, code_scale, dV, V, adapter, scale, Gdown,
-                                                                      Gup, M, K, N, rank, L, splits,
+                                                                      Gup, M, K, N, rank, L, splits_down, splits_up,
                                                                       static_cast<int>(down), status);
   return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
