@@ -258,8 +258,8 @@ def test_checkpoint(M, K, pad):
     codes, scales = cr().cr_ckpt_save(strided(x, pad))
     want, s, t = ao.ckpt_save(f64(x))
     got_s = scales.cpu().numpy()
-    # 12 float32 roundings on the way through the transform, each at most 2^-24 of the slice's sum of magnitudes / 16
-    err = 12 * 2.0 ** -24 * np.abs(f64(x)).reshape(M, -1, 256).sum(-1) / 16
+    # float32 sums of 256 products with +-1, then an exact 1/16
+    err = ao.steps(256) * np.abs(f64(x)).reshape(M, -1, 256).sum(-1) / 16
     assert (np.abs(got_s.astype(np.float64) - s) <= err / 127 + 2.0 ** -24 * s).all()
     c = codes.cpu().numpy().astype(np.int32)
     # a code may differ where y / s lies as near to a border as those roundings (and the scale's own) reach

@@ -194,8 +194,9 @@ cr_status cr_ckpt_save(const void* X, int M, int K, int64_t ldx, void* codes, fl
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
   if (M == 0) return CR_OK;
-  return cuda_status(cr::launch_ckpt_save(static_cast<const uint16_t*>(X), M, K, ldx, static_cast<int8_t*>(codes),
-                                          scales, static_cast<cudaStream_t>(stream)));
+  return static_cast<cr_status>(cr::launch_ckpt_save(static_cast<const uint16_t*>(X), M, K, ldx,
+                                                     static_cast<int8_t*>(codes), scales, nsm,
+                                                     static_cast<cudaStream_t>(stream)));
 }
 
 cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, void* X, int64_t ldx, void* stream) {
@@ -207,8 +208,9 @@ cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, voi
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
   if (M == 0) return CR_OK;
-  return cuda_status(cr::launch_ckpt_load(static_cast<const int8_t*>(codes), scales, M, K, static_cast<uint16_t*>(X),
-                                          ldx, static_cast<cudaStream_t>(stream)));
+  return static_cast<cr_status>(cr::launch_ckpt_load(static_cast<const int8_t*>(codes), scales, M, K,
+                                                     static_cast<uint16_t*>(X), ldx, nsm,
+                                                     static_cast<cudaStream_t>(stream)));
 }
 
 size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group) {

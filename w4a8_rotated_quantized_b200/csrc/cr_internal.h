@@ -190,12 +190,12 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
 // [rows, N], rows = L * rank; either may be null.
 cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts_down, int parts_up, int64_t rows, int K, int N,
                                     uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream);
-cudaError_t launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes, float* scales,
-                             cudaStream_t stream);
-cudaError_t launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uint16_t* X, int64_t ldx,
-                             cudaStream_t stream);
+int launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes, float* scales, int num_sms,
+                     cudaStream_t stream);
+int launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uint16_t* X, int64_t ldx, int num_sms,
+                     cudaStream_t stream);
 
-// ---- the W4A4 layer's input gradient (ckpt_kernels.cu, gemm_bf16.cu) ----
+// ---- the W4A4 layer's input gradient (grad_values.cu, gemm_bf16.cu) ----
 // W bf16 [N, K] = w_scale[n] * (q[n, :] H_group).  Clears the status word.
 cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16_t* W, int N, int K, int group,
                                  int* status, cudaStream_t stream);

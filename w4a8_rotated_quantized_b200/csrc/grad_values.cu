@@ -1,9 +1,5 @@
-// ckpt_kernels.cu -- streaming kernels around the rotation that go from or to codes:
+// grad_values.cu -- streaming kernels of the backward pass around the rotation:
 //
-// * 8-bit activation checkpoints: for each row and slice of 256 columns y = x H256, one float32 scale
-//   s = max(amax|y| / 127, 2^-100) and codes c = rne(y / s); back, x^ = (c s) H256.  A scale for each
-//   slice of each row costs 1/64 byte a value and keeps a loud channel's or a loud token's range away
-//   from the others (the rotation spreads a loud channel over its own slice only).
 // * packed INT4 weights as bf16 values, w^[n, :] = s_w[n] (q[n, :] H_g), for the input gradient's product.
 // * adapter gradients: partial sums of the product kernels added in order, rotated back where they were
 //   taken against checkpoint codes (sum_m v[m] x^[m] = (sum_m v[m] s[m] c[m]) H256: the transform runs
@@ -28,86 +24,56 @@ namespace {
 #include "act_device.cuh"
 
 constexpr int kWarps = 4;
-constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100: below it 1/s would leave float32's range
 
 // The warp's first slice and this lane's: slices are numbered row by row, `upr` to a row.
 __device__ __forceinline__ int64_t lane_unit() {
   return (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * 8 + ((threadIdx.x & 31) >> 2);
 }
 
-__global__ void __launch_bounds__(32 * kWarps)
-    ckpt_save_kernel(const uint16_t* __restrict__ X, int64_t ldx, int8_t* __restrict__ codes,
-                     float* __restrict__ scales, int64_t units, int upr) {
-  const int64_t u = lane_unit();
-  const int k0 = (threadIdx.x & 31) >> 2;
-  Raw raw;
-  if (u < units) {
-    const int64_t row = u / upr;
-    load_unit_mapped(X + row * ldx + (u - row * upr) * 256, k0, raw);
-  } else {
-    zero_raw(raw);
-  }
-  Pairs P;
-  widen_pairs(raw, P);
-  fwht256_mapped<4>(P);
-  // the largest magnitude by bit pattern, so that a NaN or infinity wins and marks the slice
-  uint32_t top = 0;
+// Eight biased values in the low bytes (of x: elements 0-3, of y: 4-7) as floats less `bias`: a byte put into
+// the mantissa of 2^23 reads as 2^23 plus it.  (The conversion instructions run at a sixteenth of this rate.)
+__device__ __forceinline__ void bytes_to_floats(uint2 q, float bias, float2 (&v)[4]) {
+  const float2 b2 = make_float2(-8388608.f - bias, -8388608.f - bias);
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    top = max(top, max(__float_as_uint(P.w[i].x) & 0x7FFFFFFFu, __float_as_uint(P.w[i].y) & 0x7FFFFFFFu));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  if (u >= units) return;
-  const bool finite = top < 0x7F800000u;
-  // the values are 16 times the rotated ones; 1/16 is exact
-  const float s16 = fmaxf(__fdiv_rn(__uint_as_float(top), 127.f), 16.f * kMinScale);
-  if ((threadIdx.x & 3) == 0) scales[u] = finite ? s16 * 0.0625f : __uint_as_float(0x7FC00000u);
-  if (!finite) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) P.w[i] = make_float2(0.f, 0.f);
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = e < 2 ? q.x : q.y;
+    v[e] = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + 2 * (e & 1))),
+                            __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441 + 2 * (e & 1)))), b2);
   }
-  const float s = finite ? s16 : 1.f;
-  const float r = __frcp_rn(s);
-  codes_to_unit_global<kFmtByte8>(P, k0, make_float2(r, r), make_float2(-s, -s),
-                                  reinterpret_cast<uint8_t*>(codes) + u * 256);
+}
+
+// The eight values of slot k into the pairs.
+__device__ __forceinline__ void put8(Pairs& P, int k, const float2 (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2& a = P.w[8 * (k & 3) + 2 * e];
+    float2& b = P.w[8 * (k & 3) + 2 * e + 1];
+    if (k < 4) {
+      a.x = v[e].x;
+      b.x = v[e].y;
+    } else {
+      a.y = v[e].x;
+      b.y = v[e].y;
+    }
+  }
 }
 
 // Pairs of the lane's 64 values of a slice to bf16, times `f`: piece p = k ^ k0 at elements 32p + 8l.
 __device__ __forceinline__ void store_unit_bf16(const Pairs& P, int k0, float f, uint16_t* __restrict__ unit) {
   const int l = threadIdx.x & 3;
+  const float2 f2 = make_float2(f, f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = f * (k < 4 ? P.w[8 * (k & 3) + e].x : P.w[8 * (k & 3) + e].y);
-    *reinterpret_cast<uint4*>(unit + 32 * (k ^ k0) + 8 * l) = narrow8(v);
-  }
-}
-
-__global__ void __launch_bounds__(32 * kWarps)
-    ckpt_load_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scales, uint16_t* __restrict__ X,
-                     int64_t ldx, int64_t units, int upr) {
-  const int64_t u = lane_unit();
-  const int k0 = (threadIdx.x & 31) >> 2, l = threadIdx.x & 3;
-  uint2 q[8];
-  float s = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    q[k] = u < units ? __ldg(reinterpret_cast<const uint2*>(codes + u * 256 + 32 * (k ^ k0) + 8 * l)) : make_uint2(0, 0);
-  if (u < units) s = __ldg(scales + u);
-  Pairs P;
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
+  for (int k = 0; k < 4; ++k) {
+    float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t w = e < 4 ? q[k].x : q[k].y;
-      const float v = static_cast<float>(static_cast<int8_t>(w >> (8 * (e & 3))));
-      if (k < 4) P.w[8 * (k & 3) + e].x = v; else P.w[8 * (k & 3) + e].y = v;
+      const float2 t = __fmul2_rn(P.w[8 * k + e], f2);
+      lo[e] = t.x;
+      hi[e] = t.y;
     }
-  fwht256_mapped<4>(P);  // integers up to 256 * 127: exact
-  if (u >= units) return;
-  const int64_t row = u / upr;
-  store_unit_bf16(P, k0, s * 0.0625f, X + row * ldx + (u - row * upr) * 256);
+    *reinterpret_cast<uint4*>(unit + 32 * (k ^ k0) + 8 * l) = narrow8(lo);
+    *reinterpret_cast<uint4*>(unit + 32 * ((k + 4) ^ k0) + 8 * l) = narrow8(hi);
+  }
 }
 
 // Packed INT4 weights to bf16 values in the unrotated basis.  Rounding the weights once to bf16 lets the
@@ -124,11 +90,11 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t w = u < units ? __ldg(reinterpret_cast<const uint32_t*>(Wq + u * 128 + 16 * (k ^ k0) + 4 * l)) : 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = static_cast<float>(static_cast<int32_t>(w << (28 - 4 * e)) >> 28);
-      if (k < 4) P.w[8 * (k & 3) + e].x = v; else P.w[8 * (k & 3) + e].y = v;
-    }
+    // nibbles to bytes, biased by 8: even elements, odd elements, then in order
+    const uint32_t ev = (w & 0x0F0F0F0Fu) ^ 0x08080808u, od = ((w >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+    float2 v[4];
+    bytes_to_floats(make_uint2(__byte_perm(ev, od, 0x5140), __byte_perm(ev, od, 0x7362)), 8.f, v);
+    put8(P, k, v);
   }
   fwht256_mapped<kDig>(P);
   if (u >= units) return;
@@ -151,11 +117,12 @@ __device__ __forceinline__ void add_parts(const float* __restrict__ src, int par
 
 // The gradients' partial sums joined and rounded.  The first `rot_blocks` blocks take slices of 256 values
 // of the rotated d_down, the rest eight values a thread of what is left: d_down unrotated, then d_up.
-__global__ void __launch_bounds__(32 * kWarps)
+// One warp a block: few, small pieces of work, each a round trip to L2.
+__global__ void __launch_bounds__(32)
     lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts_down, int parts_up, int64_t n_down,
                             int64_t n_up, uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up, int rot_blocks) {
   if (static_cast<int>(blockIdx.x) < rot_blocks) {
-    const int64_t u = lane_unit();
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 2);
     const int k0 = (threadIdx.x & 31) >> 2, l = threadIdx.x & 3;
     const bool in = u < n_down >> 8;
     Pairs P;
@@ -172,7 +139,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (in) store_unit_bf16(P, k0, 0.0625f, d_down + u * 256);
     return;
   }
-  int64_t i = (static_cast<int64_t>(blockIdx.x - rot_blocks) * 32 * kWarps + threadIdx.x) * 8;
+  int64_t i = (static_cast<int64_t>(blockIdx.x - rot_blocks) * 32 + threadIdx.x) * 8;
   float v[8];
   if (!rot_blocks) {
     if (i < n_down) {
@@ -191,20 +158,6 @@ unsigned unit_blocks(int64_t units) { return static_cast<unsigned>((units + 8 * 
 
 }  // namespace
 
-cudaError_t launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes, float* scales,
-                             cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(M) * (K / 256);
-  ckpt_save_kernel<<<unit_blocks(units), 32 * kWarps, 0, stream>>>(X, ldx, codes, scales, units, K / 256);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uint16_t* X, int64_t ldx,
-                             cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(M) * (K / 256);
-  ckpt_load_kernel<<<unit_blocks(units), 32 * kWarps, 0, stream>>>(codes, scales, X, ldx, units, K / 256);
-  return cudaGetLastError();
-}
-
 cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16_t* W, int N, int K, int group,
                                  int* status, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(N) * (K / 256);
@@ -220,10 +173,10 @@ cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16
 cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts_down, int parts_up, int64_t rows, int K, int N,
                                     uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream) {
   const int64_t n_down = d_down ? rows * K : 0, n_up = d_up ? rows * N : 0;
-  const unsigned rot = rotate && d_down ? unit_blocks(n_down / 256) : 0;
+  const unsigned rot = rotate && d_down ? static_cast<unsigned>((n_down / 256 + 7) / 8) : 0;
   const int64_t plain = (rot ? 0 : n_down) + n_up;
-  const unsigned blocks = rot + static_cast<unsigned>((plain + 256 * kWarps - 1) / (256 * kWarps));
-  lora_grad_finish_kernel<<<blocks, 32 * kWarps, 0, stream>>>(Gdown, Gup, parts_down, parts_up, n_down, n_up, d_down, d_up,
+  const unsigned blocks = rot + static_cast<unsigned>((plain + 255) / 256);
+  lora_grad_finish_kernel<<<blocks, 32, 0, stream>>>(Gdown, Gup, parts_down, parts_up, n_down, n_up, d_down, d_up,
                                                               static_cast<int>(rot));
   return cudaGetLastError();
 }
