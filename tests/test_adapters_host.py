@@ -115,7 +115,9 @@ def test_refusals_by_code():
     assert gi(group=32) == 2 and gi(group=1024) == 2 and gi(N=260) == 2 and gi(K=384) == 2
     assert gi(lddy=268) == 3 and gi(dX=odd) == 3
     need = lib.cr_w4a4_grad_input_workspace_size(40, 264, 512, 256)
-    assert need >= 264 * 512 * 2 and gi(n=need) in DEV and gi(n=need - 1) == 5
+    assert need >= 40 * 512 * 4 and gi(n=need) in DEV and gi(n=need - 1) == 5
+    need = lib.cr_w4a4_grad_input_workspace_size(4000, 264, 512, 256)
+    assert need >= 264 * 512 * 2 and gi(M=4000, n=need) in DEV and gi(M=4000, n=need - 1) == 5
 
 
 def test_binding_wants_cuda_bf16():

@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconvrot_b200.so")
 SOURCES = ["api.cu", "act_kernels.cu", "gemm_w4a4.cu", "gemm_w4a4_pair.cu", "gemm_w4a4_small.cu", "gemm_i8.cu",
            "gemm_w4a8.cu", "gemm_a8w4.cu", "tmap.cu", "noalloc.cu",
-           "selftest.cu", "api_adapters.cu", "lora_rows.cu", "lora_mma.cu", "grad_values.cu", "ckpt_mma.cu", "gemm_bf16.cu"]
+           "selftest.cu", "api_adapters.cu", "lora_rows.cu", "lora_mma.cu", "grad_values.cu", "ckpt_mma.cu", "gemm_bf16.cu",
+           "grad_input_few.cu"]
 HEADERS = [os.path.join(ROOT, "include", "convrot.h")] + [
     os.path.join(CSRC, f) for f in ("cr_device.cuh", "cr_internal.h", "act_device.cuh", "grid_sync.cuh", "lora_device.cuh")
 ]

@@ -214,9 +214,11 @@ cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, voi
 }
 
 size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group) {
-  (void)M;
   (void)group;
-  if (N < 0 || K < 0) return kWsHead;
+  if (M < 0 || N <= 0 || K < 256 || K % 256 != 0) return kWsHead;
+  if (M > 0 && M <= cr::kGradInputFewMaxM)
+    return kWsHead + cr::round_up(cr::grad_input_few_operand_rows(M) * N * 2, 256) +
+           bytes_f32(static_cast<int64_t>(M) * K * cr::grad_input_few_splits(M, N, K, kSizingSms));
   return kWsHead + cr::round_up(static_cast<size_t>(N) * static_cast<size_t>(K) * 2, 256);
 }
 
@@ -241,6 +243,14 @@ cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const
     return cuda_status(cudaMemset2DAsync(dX, static_cast<size_t>(lddx) * 2, 0, static_cast<size_t>(K) * 2,
                                          static_cast<size_t>(M), s));
   uint16_t* w = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWsHead);
+  if (M <= cr::kGradInputFewMaxM) {
+    float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead +
+                                           cr::round_up(cr::grad_input_few_operand_rows(M) * N * 2, 256));
+    return static_cast<cr_status>(cr::launch_grad_input_few(
+        static_cast<const uint16_t*>(dY), lddy, static_cast<const uint8_t*>(Wq), w_scale, w, sums,
+        static_cast<uint16_t*>(dX), lddx, M, N, K, group, cr::grad_input_few_splits(M, N, K, kSizingSms),
+        ws_status(workspace), s));
+  }
   cudaError_t e = cr::launch_weight_values(static_cast<const uint8_t*>(Wq), w_scale, w, N, K, group,
                                            ws_status(workspace), s);
   if (e != cudaSuccess) return CR_ERR_CUDA;

@@ -203,6 +203,15 @@ cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16
 int launch_gemm_bf16(const void* A, int64_t lda, const void* W, void* Y, int64_t ldy, int M, int N, int K, int* status,
                      int num_sms, cudaStream_t stream);
 
+// The same gradient for few tokens, straight from the packed weights (grad_input_few.cu): V holds the product's
+// bf16 [operand_rows, N] operand, P `splits` partial sums float32 [M, K].
+constexpr int kGradInputFewMaxM = 256;
+int grad_input_few_splits(int M, int N, int K, int num_sms);
+size_t grad_input_few_operand_rows(int M);
+int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, const float* w_scale, uint16_t* V,
+                          float* P, uint16_t* dX, int64_t lddx, int M, int N, int K, int group, int splits, int* status,
+                          cudaStream_t stream);
+
 // Supported device = compute capability 10.0 (api.cu): CR_OK and its SM count, or the status to return.
 int check_current_device(int* num_sms);
 
