@@ -456,7 +456,9 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  * pointers 16 bytes, V 8 bytes, leading dimensions % 8 == 0.
  * Workspace: of at least the size returned by the matching size call, 256-byte
  * aligned; none of it needs to be zero before: the call writes its status word
- * (the first 16 bytes, read with cr_read_device_status) itself.
+ * (the first 16 bytes, read with cr_read_device_status) itself.  The forward
+ * call of few rows needs none (its size call returns 0) and may be given NULL;
+ * it has no device-side waits to report on.
  */
 #define CR_MAX_RANK 128
 #define CR_MAX_ADAPTERS 4096

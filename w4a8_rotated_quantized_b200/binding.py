@@ -689,9 +689,25 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> Tuple[int, int, torch.Tensor]:
-    """(address, bytes, tensor) of the workspace; a bf16 buffer like ``like`` if none is given."""
+_sizes: dict = {}
+
+
+def _ws_size(name: str, *dims: int) -> int:
+    """The library's workspace size for these dimensions, kept for the next call with the same ones."""
+    key = (name, dims)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = _sizes[key] = getattr(_lib, name)(*dims)
+    return n
+
+
+def _scratch(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor):
+    """(address, bytes, tensor) of the workspace; a bf16 buffer like ``like`` if none is given and one is needed."""
     if given is None:
+        if nbytes == 0:
+            return None, 0, None
         given = like.new_empty((nbytes + 1) // 2)
         return given.data_ptr(), nbytes, given
     _dev(given, "workspace", torch.uint8, like.device)
@@ -766,7 +782,7 @@ def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale
     ldb = 0 if base is None else _matrix(base, "base", dev, M, N)
     Y, ldy = _out_matrix(out, X, M, N)
     V = X.new_empty((M, r)) if save_v else None
-    ws, nws, keep = _scratch(workspace, _lib.cr_lora_forward_workspace_size(M, N, K, r, L), X)
+    ws, nws, keep = _scratch(workspace, _ws_size("cr_lora_forward_workspace_size", M, N, K, r, L), X)
     _run("cr_lora_forward", dev, X.data_ptr(), ldx, p_adapter, p_down, p_up, p_scale, _addr(base), ldb, Y.data_ptr(), ldy,
          _addr(V), M, N, K, r, L, ws, nws)
     return (Y, V) if save_v else Y
@@ -809,7 +825,7 @@ def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch
     dX, lddx = _out_matrix(out, dY, M, K) if need_dx else (None, 0)
     dd = dY.new_empty((L, r, K)) if need_down else None
     du = dY.new_empty((L, r, N)) if need_up else None
-    ws, nws, keep = _scratch(workspace, _lib.cr_lora_backward_workspace_size(M, N, K, r, L), dY)
+    ws, nws, keep = _scratch(workspace, _ws_size("cr_lora_backward_workspace_size", M, N, K, r, L), dY)
     _run("cr_lora_backward", dev, dY.data_ptr(), lddy, p_x, ldx, p_codes, p_scales, p_v, p_adapter, p_down, p_up, p_scale,
          _addr(base), ldb, _addr(dX), lddx, _addr(dd), _addr(du), M, N, K, r, L, ws, nws)
     return dX, dd, du
@@ -849,6 +865,6 @@ def cr_w4a4_grad_input(dY: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor
     p_w = _exact(Wq, "Wq", torch.uint8, dev, (N, K // 2))
     p_s = _exact(w_scale, "w_scale", torch.float32, dev, (N,))
     dX, lddx = _out_matrix(out, dY, M, K)
-    ws, nws, keep = _scratch(workspace, _lib.cr_w4a4_grad_input_workspace_size(M, N, K, group), dY)
+    ws, nws, keep = _scratch(workspace, _ws_size("cr_w4a4_grad_input_workspace_size", M, N, K, group), dY)
     _run("cr_w4a4_grad_input", dev, dY.data_ptr(), lddy, p_w, p_s, dX.data_ptr(), lddx, M, N, K, group, ws, nws)
     return dX

@@ -36,11 +36,6 @@ bool sizes_ok(int M, int N, int K, int rank, int L) {
          rank <= CR_MAX_RANK && rank % 4 == 0 && L >= 1 && L <= CR_MAX_ADAPTERS;
 }
 
-// Row-form V holds a partial sum for each K split, the tensor-core form one array.
-int v_splits(int M, int K, int rank) {
-  return M <= cr::kLoraRowsMaxM ? cr::lora_row_splits(M > 0 ? M : 1, K, rank, kSizingSms) : 1;
-}
-
 struct GradSplits {
   int down = 0, up = 0;
 };
@@ -67,7 +62,8 @@ extern "C" {
 
 size_t cr_lora_forward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank * v_splits(M, K, rank));
+  if (M <= cr::kLoraRowsMaxM) return 0;
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank);
 }
 
 cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, const void* down, const void* up,
@@ -84,9 +80,8 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if (st != CR_OK) return st;
   if (!aligned(down, 16) || !aligned(up, 16) || !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(V, 8))
     return CR_ERR_MISALIGNED;
-  if (!workspace || workspace_bytes < cr_lora_forward_workspace_size(M, N, K, rank, num_adapters) ||
-      !aligned(workspace, 256))
-    return CR_ERR_WORKSPACE;
+  const size_t need = cr_lora_forward_workspace_size(M, N, K, rank, num_adapters);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return CR_ERR_WORKSPACE;
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
   if (M == 0) return CR_OK;
@@ -100,13 +95,9 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   const uint16_t* b = static_cast<const uint16_t*>(base);
   uint16_t* y = static_cast<uint16_t*>(Y);
   const int L = num_adapters;
-  if (M <= cr::kLoraRowsMaxM) {
-    const int splits = v_splits(M, K, rank);
-    cudaError_t e = cr::launch_lora_v_rows(x, ldx, adapter, dn, v, M, K, rank, L, splits, status, s);
-    if (e == cudaSuccess)
-      e = cr::launch_lora_y_rows(v, splits, adapter, u, scale, b, ldb, y, ldy, vout, M, N, rank, L, s);
-    return cuda_status(e);
-  }
+  if (M <= cr::kLoraRowsMaxM)
+    return static_cast<cr_status>(
+        cr::launch_lora_rows(x, ldx, adapter, dn, u, scale, b, ldb, y, ldy, vout, M, N, K, rank, L, s));
   int r = cr::launch_lora_v_mma(x, ldx, adapter, dn, v, vout, M, K, rank, L, status, nsm, s);
   if (r == CR_OK) r = cr::launch_lora_y_mma(v, adapter, u, scale, b, ldb, y, ldy, M, N, rank, L, status, nsm, s);
   return static_cast<cr_status>(r);

@@ -162,17 +162,12 @@ int launch_w4a4_gemm_multi_s32(const void* Xq, int num_proj, const void* const* 
 constexpr int kMaxRank = 128;
 // Rows up to which the row form runs (lora_rows.cu), above it the tensor-core form.
 constexpr int kLoraRowsMaxM = 64;
-// K splits of the row form's V product; V holds that many partial [M, rank] arrays.
-int lora_row_splits(int M, int K, int rank, int num_sms);
-// V partials of the rows' own adapters (zeros for rows without one).  Clears the status word.
-cudaError_t launch_lora_v_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, float* V,
-                               int M, int K, int rank, int L, int splits, int* status, cudaStream_t stream);
-// Y = base + scale[a] * V . up[a]; the unscaled V, splits added, also to Vout (bf16 [M, rank]) if given.
-cudaError_t launch_lora_y_rows(const float* V, int splits, const int32_t* adapter, const uint16_t* up,
-                               const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy,
-                               uint16_t* Vout, int M, int N, int rank, int L, cudaStream_t stream);
-// The same products on the tensor cores, for batches (lora_mma.cu).  V float32 [M, rank], one array; Vout its
-// bf16 copy or null.
+// Forward for few rows in one launch (lora_rows.cu).
+int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, const uint16_t* up,
+                     const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, uint16_t* Vout,
+                     int M, int N, int K, int rank, int L, cudaStream_t stream);
+// The products on the tensor cores, for batches (lora_mma.cu).  V float32 [M, rank] of the rows' own adapters
+// (zeros for rows without one), Vout its bf16 copy or null; the v product clears the status word.
 int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, float* V,
                       uint16_t* Vout, int M, int K, int rank, int L, int* status, int num_sms, cudaStream_t stream);
 int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up, const float* scale,
