@@ -84,9 +84,9 @@ def test_refusals_by_code():
     assert fwd(ldx=516) == 3 and fwd(X=odd) == 3 and fwd(Y=odd) == 3 and fwd(dn=odd) == 3 and fwd(up=odd) == 3
     assert fwd(base=odd) == 3 and fwd(V=P((1 << 20) + 4)) == 3 and fwd(ad=P((1 << 20) + 2)) == 3
     assert lib.cr_lora_forward_workspace_size(40, 264, 512, 8, 2) == 0 and fwd(w=n0, n=0) in DEV  # few rows: none
-    need = lib.cr_lora_forward_workspace_size(400, 264, 512, 8, 2)
-    assert fwd(M=400, n=need) in DEV and fwd(M=400, n=need - 1) == 5 and fwd(M=400, w=n0) == 5
-    assert fwd(M=400, w=P((1 << 21) + 128)) == 5
+    need = lib.cr_lora_forward_workspace_size(4000, 264, 512, 8, 2)
+    assert fwd(M=4000, n=need) in DEV and fwd(M=4000, n=need - 1) == 5 and fwd(M=4000, w=n0) == 5
+    assert fwd(M=4000, w=P((1 << 21) + 128)) == 5
 
     def bwd(dY=A, X=A, ldx=512, c=n0, cs=n0, V=A, ad=A, dn=A, up=A, sc=A, base=A, ldb=512, dX=A, lddx=512, dd=A, du=A,
             M=40, N=264, K=512, r=8, L=2, w=ws, n=wsn):

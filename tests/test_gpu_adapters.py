@@ -91,6 +91,11 @@ SHAPES = [  # M, K, N, rank, adapters, rows
     (777, 512, 256, 8, 5, "runs"),
     (1100, 3072, 1544, 64, 1, "all"),
     (2049, 1280, 776, 128, 4, "runs"),
+    (1500, 264, 1032, 12, 40, "rows"),
+    (1300, 256, 520, 128, 9, "rows"),
+    (9, 65536, 8, 4, 2, "rows"),
+    (70, 32768, 16, 8, 70, "rows"),
+    (3, 256, 65536, 8, 2, "rows"),
     (200, 256, 256, 16, 3, "none"),
     (40, 256, 256, 32, 20, "none"),
 ]
@@ -420,16 +425,20 @@ def test_other_stream_and_captured_graphs():
 
 
 def test_own_workspace_and_status():
-    d = make(300, 512, 264, 16, 2, "runs", seed=31)
+    d = make(3000, 512, 264, 16, 2, "runs", seed=31)
     from w4a8_rotated_quantized_b200 import binding
 
-    n = binding._lib.cr_lora_forward_workspace_size(300, 264, 512, 16, 2)
+    n = binding._lib.cr_lora_forward_workspace_size(3000, 264, 512, 16, 2)
+    assert binding._lib.cr_lora_forward_workspace_size(3, 264, 512, 16, 2) == 0
     ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # nothing needs to be zero before
     want = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"])
     got = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], workspace=ws)
     assert torch.equal(got, want) and cr().cr_read_device_status(ws=ws) == 0
     with pytest.raises(cr().ConvRotError):
         cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], workspace=ws[:256])
+    ws.fill_(255)  # few rows: needs none, and says so in one that it is given
+    few = cr().cr_lora_forward(d["X"][:3], d["down"], d["up"], d["scale"], adapter=d["adapter"][:3], workspace=ws[:256])
+    assert torch.isfinite(few).all() and cr().cr_read_device_status(ws=ws) == 0
 
 
 def test_refusals():

@@ -752,15 +752,23 @@ def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device,
     return t.data_ptr()
 
 
-def _pool(down: torch.Tensor, up: torch.Tensor) -> Tuple[int, int, int, int]:
-    """(adapters, rank, K, N) of the factors down [L, r, K] and up [L, r, N]."""
-    for t, name in ((down, "down"), (up, "up")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a tensor")
-        if t.dim() != 3:
-            raise ValueError(f"{name} must be 3-D [adapters, rank, columns]")
-    L, r, K = down.shape
-    return L, r, K, up.shape[2]
+def _factors(down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor, adapter: Optional[torch.Tensor],
+             dev: torch.device, M: int, K: Optional[int], N: Optional[int]):
+    """(adapters, rank, K, N) of the pool and the addresses of down [L, r, K], up [L, r, N], scale [L] and the
+    rows' adapters [M]; K or N is given by the call's first operand."""
+    if not isinstance(down, torch.Tensor) or not isinstance(up, torch.Tensor):
+        raise TypeError("down and up must be tensors")
+    if down.dim() != 3 or up.dim() != 3:
+        raise ValueError("down and up must be 3-D [adapters, rank, columns]")
+    L, r, k = down.shape
+    n = up.shape[2]
+    if K is None:
+        K = k
+    if N is None:
+        N = n
+    return (L, r, K, N, _exact(down, "down", torch.bfloat16, dev, (L, r, K)), _exact(up, "up", torch.bfloat16, dev, (L, r, N)),
+            _exact(scale, "scale", torch.float32, dev, (L,)),
+            None if adapter is None else _exact(adapter, "adapter", torch.int32, dev, (M,)))
 
 
 def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
@@ -774,11 +782,7 @@ def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale
     ``save_v`` returns (Y, V), V bf16 [M, r] = X down[a]^T for the backward pass.
     """
     M, K, ldx, dev = _input(X, "X")
-    L, r, _, N = _pool(down, up)
-    p_down = _exact(down, "down", torch.bfloat16, dev, (L, r, K))
-    p_up = _exact(up, "up", torch.bfloat16, dev, (L, r, N))
-    p_scale = _exact(scale, "scale", torch.float32, dev, (L,))
-    p_adapter = None if adapter is None else _exact(adapter, "adapter", torch.int32, dev, (M,))
+    L, r, _, N, p_down, p_up, p_scale, p_adapter = _factors(down, up, scale, adapter, dev, M, K, None)
     ldb = 0 if base is None else _matrix(base, "base", dev, M, N)
     Y, ldy = _out_matrix(out, X, M, N)
     V = X.new_empty((M, r)) if save_v else None
@@ -799,11 +803,7 @@ def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch
     projection's own input gradient; zero without it); ``out`` takes dX and may be ``base`` itself.
     """
     M, N, lddy, dev = _input(dY, "dY")
-    L, r, K, _ = _pool(down, up)
-    p_down = _exact(down, "down", torch.bfloat16, dev, (L, r, K))
-    p_up = _exact(up, "up", torch.bfloat16, dev, (L, r, N))
-    p_scale = _exact(scale, "scale", torch.float32, dev, (L,))
-    p_adapter = None if adapter is None else _exact(adapter, "adapter", torch.int32, dev, (M,))
+    L, r, K, _, p_down, p_up, p_scale, p_adapter = _factors(down, up, scale, adapter, dev, M, None, N)
     if need_down and X is None:
         raise ValueError("X (or its checkpoint) is needed for d_down")
     if need_up and V is None:

@@ -62,7 +62,7 @@ extern "C" {
 
 size_t cr_lora_forward_workspace_size(int M, int N, int K, int rank, int num_adapters) {
   if (!sizes_ok(M, N, K, rank, num_adapters)) return kWsHead;
-  if (M <= cr::kLoraRowsMaxM) return 0;
+  if (cr::use_lora_rows(M, N, K, rank, num_adapters)) return 0;
   return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank);
 }
 
@@ -80,7 +80,7 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if (st != CR_OK) return st;
   if (!aligned(down, 16) || !aligned(up, 16) || !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(V, 8))
     return CR_ERR_MISALIGNED;
-  const size_t need = cr_lora_forward_workspace_size(M, N, K, rank, num_adapters);
+  const size_t need = M > 0 ? cr_lora_forward_workspace_size(M, N, K, rank, num_adapters) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return CR_ERR_WORKSPACE;
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
@@ -95,9 +95,10 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   const uint16_t* b = static_cast<const uint16_t*>(base);
   uint16_t* y = static_cast<uint16_t*>(Y);
   const int L = num_adapters;
-  if (M <= cr::kLoraRowsMaxM)
+  if (cr::use_lora_rows(M, N, K, rank, L))
     return static_cast<cr_status>(
-        cr::launch_lora_rows(x, ldx, adapter, dn, u, scale, b, ldb, y, ldy, vout, M, N, K, rank, L, s));
+        cr::launch_lora_rows(x, ldx, adapter, dn, u, scale, b, ldb, y, ldy, vout, M, N, K, rank, L,
+                             workspace && workspace_bytes >= 16 ? status : nullptr, s));
   int r = cr::launch_lora_v_mma(x, ldx, adapter, dn, v, vout, M, K, rank, L, status, nsm, s);
   if (r == CR_OK) r = cr::launch_lora_y_mma(v, adapter, u, scale, b, ldb, y, ldy, M, N, rank, L, status, nsm, s);
   return static_cast<cr_status>(r);

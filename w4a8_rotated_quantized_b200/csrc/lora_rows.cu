@@ -6,11 +6,12 @@
 //
 // with a = adapter[m]; rows whose adapter lies outside the pool have V = 0 and Y = base.
 //
-// A row has a cluster of 16 CTAs (fewer when there are more rows).  Each multiplies its part of the row by the rank rows of A and sends the
-// partial sums to all the others, which add them in order; then each makes its part of the columns.  What
-// costs time here is latency: a token's factors are a few hundred KB.  So the first ranks' U and the base are on
-// their way before the first product, and the only other wait is one barrier of the cluster.  (As two launches
-// with the partial sums in memory: 6.9 us for one token at rank 16, 2560 -> 9728, against 4.4.)
+// A row has a cluster of 16 CTAs (fewer when there are more rows).  Each multiplies its part of the row by the
+// rank rows of A and sends the partial sums to all the others, which add them in order; then each makes its part
+// of the columns.  What costs time here is latency: a token's factors are a few hundred KB.  So each warp has
+// eight loads on their way whatever the rank (its tasks are pairs of a rank and 256 columns, not ranks), the
+// ranks of a column are shared out between the threads that columns leave idle, their first U and the base are
+// on their way before the first product, and the only other wait is one barrier of the cluster.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,115 +27,152 @@ namespace cr {
 namespace {
 
 constexpr int kMostCluster = 16;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 8;   // ranks of U on their way from the start
+constexpr int kAhead = 4;     // ranks of U that a thread has on their way from the start
+constexpr int kTasks = 8;     // loads of A that a warp has on their way
+constexpr int kMostPasses = CR_MAX_K / 256 / 4;  // 256 columns at a time: of a CTA in a cluster of 4 (2: half the K)
 
 __device__ __forceinline__ void st_shared_cluster_f1(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
     lora_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ adapter,
                      const uint16_t* __restrict__ down, const uint16_t* __restrict__ up,
                      const float* __restrict__ scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy,
-                     uint16_t* __restrict__ Vout, int N, int K, int rank, int L, int ctas) {
+                     uint16_t* __restrict__ Vout, int N, int K, int rank, int L, int ctas, int* __restrict__ status) {
   __shared__ float part[kMostCluster][kMaxRank];
+  // sums of the tasks [pass][rank]; later partial results [rank group][column piece][8]
+  __shared__ __align__(16) float scratch[kMostPasses * kMaxRank];
   __shared__ float v[kMaxRank];
+  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = CR_OK;
   const int c = static_cast<int>(cluster_ctarank());
   const int64_t m = blockIdx.x / ctas;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int a = row_adapter(adapter, m, L);  // the same in the whole cluster
-  // this CTA's columns of Y, eight a thread and pass
+  // this CTA's columns of Y in pieces of eight, and their ranks in groups where there are threads to spare
   const int per_n = (N / 8 + ctas - 1) / ctas;
-  const int n_end = 8 * min((c + 1) * per_n, N / 8);
-  int n = 8 * (c * per_n + threadIdx.x);
+  const int p0 = c * per_n;
+  const int pieces = min(per_n, N / 8 - p0);  // (none, or fewer than none, for the last CTAs of a short row)
+  const int groups = per_n > kThreads / 2 ? 1 : min(kThreads / per_n, 16);
+  const int group = groups > 1 ? tid / per_n : 0, piece = groups > 1 ? tid - group * per_n : tid;
+  const bool mine = piece < pieces && group < groups;
   const uint16_t* brow = base ? base + m * ldb : nullptr;
   if (a < 0) {
-    for (; n < n_end; n += 8 * kThreads)
-      *reinterpret_cast<uint4*>(Y + m * ldy + n) =
-          brow ? *reinterpret_cast<const uint4*>(brow + n) : make_uint4(0, 0, 0, 0);
-    if (Vout && c == 0 && threadIdx.x < rank) Vout[m * rank + threadIdx.x] = 0;
+    for (int p = tid; p < pieces; p += kThreads)
+      *reinterpret_cast<uint4*>(Y + m * ldy + 8 * (p0 + p)) =
+          brow ? *reinterpret_cast<const uint4*>(brow + 8 * (p0 + p)) : make_uint4(0, 0, 0, 0);
+    if (Vout && c == 0 && tid < rank) Vout[m * rank + tid] = 0;
     return;
   }
   cluster_arrive();
-  const uint16_t* u = up + static_cast<int64_t>(a) * rank * N;
+  const uint16_t* u = up + static_cast<int64_t>(a) * rank * N + 8 * p0;
   uint4 ahead[kAhead], b = make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) {
-    ahead[j] = make_uint4(0, 0, 0, 0);
-    if (n < n_end && j < rank) ahead[j] = ldg_here_u4(u + static_cast<int64_t>(j) * N + n);
+  for (int i = 0; i < kAhead; ++i) {
+    const int j = group + groups * i;
+    ahead[i] = make_uint4(0, 0, 0, 0);
+    if (mine && j < rank) ahead[i] = ldg_here_u4(u + static_cast<int64_t>(j) * N + 8 * piece);
   }
-  if (n < n_end && brow) b = ld_here_u4(brow + n);
+  if (mine && group == 0 && brow) b = ld_here_u4(brow + 8 * (p0 + piece));
 
-  // partial sums over this CTA's columns of X: ranks warp, warp + 8, ... for each warp
+  // partial sums over this CTA's columns of X: task t is rank t % rank over 256 columns
   const int per_k = (K / 8 + ctas - 1) / ctas;
-  const int k_end = 8 * min((c + 1) * per_k, K / 8);
+  const int q0 = c * per_k, q_end = min(q0 + per_k, K / 8);
+  const int passes = (per_k + 31) / 32;
   const uint16_t* x = X + m * ldx;
   const uint16_t* w = down + static_cast<int64_t>(a) * rank * K;
-  float acc[kMaxRank / kWarps] = {};
-  for (int k = 8 * (c * per_k + lane); k < k_end; k += 256) {
-    float xv[8];
-    widen8(ldg16(x + k), xv);
+  for (int t0 = kTasks * warp; t0 < rank * passes; t0 += kTasks * kWarps) {
+    uint4 xq[kTasks / 4], wq[kTasks];  // four tasks in a row are of one pass: ranks come in fours
 #pragma unroll
-    for (int i = 0; i < kMaxRank / kWarps; ++i) {
-      const int j = warp + kWarps * i;
-      if (j < rank) {
-        float wv[8];
-        widen8(ldg16(w + static_cast<int64_t>(j) * K + k), wv);
+    for (int i = 0; i < kTasks; i += 4) {
+      const int t = t0 + i, pass = t / rank, j = t - pass * rank;
+      const int q = q0 + 32 * pass + lane;
+      const bool in = q < q_end && t < rank * passes;
+      const uint16_t* src = w + static_cast<int64_t>(j) * K + 8 * q;
+      xq[i / 4] = in ? ldg16(x + 8 * q) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], wv[e], acc[i]);
-      }
+      for (int e = 0; e < 4; ++e) wq[i + e] = in ? ldg16(src + static_cast<int64_t>(e) * K) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kTasks; ++i) {
+      float xv[8], wv[8], s = 0.f;
+      widen8(xq[i / 4], xv);
+      widen8(wq[i], wv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf(xv[e], wv[e], s);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0 && t0 + i < rank * passes) scratch[t0 + i] = s;
     }
   }
+  __syncthreads();
   cluster_wait();  // every CTA of the cluster has started: its shared memory may be written to
-#pragma unroll
-  for (int i = 0; i < kMaxRank / kWarps; ++i) {
-    const int j = warp + kWarps * i;
-    if (j < rank) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (lane < ctas) st_shared_cluster_f1(mapa_shared(smem_u32(&part[c][j]), lane), acc[i]);
-    }
+  for (int i = tid; i < rank * ctas; i += kThreads) {
+    const int to = i / rank, j = i - to * rank;
+    float s = 0.f;
+    for (int p = 0; p < passes; ++p) s += scratch[p * rank + j];
+    st_shared_cluster_f1(mapa_shared(smem_u32(&part[c][j]), to), s);
   }
   __syncwarp();
   cluster_sync();
-  if (threadIdx.x < rank) {
+  if (tid < rank) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < kMostCluster; ++i)
-      if (i < ctas) t += part[i][threadIdx.x];
-    if (Vout && c == 0) Vout[m * rank + threadIdx.x] = bf16_bits(t);
-    v[threadIdx.x] = t * __ldg(scale + a);
+      if (i < ctas) t += part[i][tid];
+    if (Vout && c == 0) Vout[m * rank + tid] = bf16_bits(t);
+    v[tid] = t * __ldg(scale + a);
   }
   __syncthreads();
-  for (bool first = true; n < n_end; n += 8 * kThreads, first = false) {
+  for (int p = piece, first = 1; p < pieces && group < groups; p += kThreads, first = 0) {
     float y[8] = {};
     if (first) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = group + groups * i;
         if (j < rank) {
           float uv[8];
-          widen8(ahead[j], uv);
+          widen8(ahead[i], uv);
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = fmaf(v[j], uv[e], y[e]);
         }
       }
     } else if (brow) {
-      b = *reinterpret_cast<const uint4*>(brow + n);
+      b = *reinterpret_cast<const uint4*>(brow + 8 * (p0 + p));
     }
 #pragma unroll 8
-    for (int j = first ? kAhead : 0; j < rank; ++j) {
+    for (int j = group + (first ? groups * kAhead : 0); j < rank; j += groups) {
       float uv[8];
-      widen8(ldg16(u + static_cast<int64_t>(j) * N + n), uv);
+      widen8(ldg16(u + static_cast<int64_t>(j) * N + 8 * p), uv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = fmaf(v[j], uv[e], y[e]);
     }
-    float bv[8];
-    widen8(b, bv);
+    if (groups == 1) {
+      float bv[8];
+      widen8(b, bv);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += bv[e];
-    *reinterpret_cast<uint4*>(Y + m * ldy + n) = narrow8(y);
+      for (int e = 0; e < 8; ++e) y[e] += bv[e];
+      *reinterpret_cast<uint4*>(Y + m * ldy + 8 * (p0 + p)) = narrow8(y);
+    } else {  // (one pass: a thread for each piece and group)
+      float4* d = reinterpret_cast<float4*>(scratch) + 2 * (group * per_n + p);
+      d[0] = make_float4(y[0], y[1], y[2], y[3]);
+      d[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  if (mine && group == 0) {
+    float y[8];
+    widen8(b, y);
+    for (int g = 0; g < groups; ++g) {
+      const float4* d = reinterpret_cast<const float4*>(scratch) + 2 * (g * per_n + piece);
+      const float4 f0 = d[0], f1 = d[1];
+      y[0] += f0.x; y[1] += f0.y; y[2] += f0.z; y[3] += f0.w;
+      y[4] += f1.x; y[5] += f1.y; y[6] += f1.z; y[7] += f1.w;
+    }
+    *reinterpret_cast<uint4*>(Y + m * ldy + 8 * (p0 + piece)) = narrow8(y);
   }
 }
 
@@ -142,9 +180,23 @@ std::atomic<bool> g_attr_done[64];
 
 }  // namespace
 
+// By microseconds as measured at ranks 16 to 128 and 3072 to 9728 columns: the row form costs 5 and its rows'
+// factors at 6 TB/s (each row reads its own: L2).  The batch form costs 11 and its first adapter's factors at
+// 0.3 TB/s, and about a tenth more for every further adapter that occurs among a tile's rows; the pool's size
+// only bounds those, so half of them are counted.
+//   64 rows, rank 16, 2560 -> 9728:   one adapter 9 against 12, each row its own of 48: 9 against 48
+//   64 rows, rank 128, 12288 -> 3072: one adapter 47 against 24
+bool use_lora_rows(int M, int N, int K, int rank, int L) {
+  if (M > 1024) return false;
+  const double factors = 2.0 * rank * (static_cast<double>(K) + N);
+  const int most = L < M ? (L < 128 ? L : 128) : (M < 128 ? M : 128);
+  const double rows = 5 + M * factors / 6e6, batch = (11 + factors / 3e5) * (1 + 0.06 * (most - 1));
+  return rows < batch;
+}
+
 int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, const uint16_t* up,
                      const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, uint16_t* Vout,
-                     int M, int N, int K, int rank, int L, cudaStream_t stream) {
+                     int M, int N, int K, int rank, int L, int* status, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CR_ERR_CUDA;
   if (!g_attr_done[dev].load()) {
@@ -155,8 +207,8 @@ int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, con
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  // fewer CTAs a row where more rows share the machine
-  const int ctas = M <= 8 ? 16 : M <= 24 ? 8 : 4;
+  // fewer CTAs a row where more rows share the machine; two only where their passes fit
+  const int ctas = M <= 4 ? 16 : M <= 8 ? 8 : M <= 64 || K > CR_MAX_K / 2 ? 4 : 2;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
@@ -166,7 +218,7 @@ int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, lora_rows_kernel, X, ldx, adapter, down, up, scale, base, ldb, Y, ldy, Vout, N, K,
-                            rank, L, ctas) == cudaSuccess
+                            rank, L, ctas, status) == cudaSuccess
              ? CR_OK
              : CR_ERR_CUDA;
 }
