@@ -330,7 +330,7 @@ inline __host__ __device__ YPlan y_plan(int rank) {
   YPlan p;
   p.rp = round16(rank);
   p.u = p.rp * 256;  // two boxes of 64 columns x rank rows
-  p.nu = 4;
+  p.nu = p.rp <= 64 ? 4 : 3;
   p.off_y = p.nu * p.u;
   p.nb = (kSmemMax - p.off_y - kListBytes - kBarBytes) / kYTile;
   if (p.nb > 5) p.nb = 5;
@@ -604,7 +604,7 @@ constexpr int kMaxGradTiles = 512;  // token tiles of one CTA (64-bit row masks 
 struct GPlan {
   int rp, vcols, stage, stages, off_raw, off_mask, off_bar, smem, cols;
 };
-constexpr int kRaws = 3;  // tiles of codes on their way
+constexpr int kRaws = 4;  // tiles of codes on their way; even, so that each set meets its slots round by round
 inline __host__ __device__ GPlan g_plan(int rank, bool codes, bool v16) {
   GPlan p;
   p.rp = round16(rank);
@@ -624,15 +624,18 @@ constexpr int kGSet = 8;                  // warps of a set
 constexpr int kGWarps = 2 * kGSet;        // make the operands and, at the end, write the sums
 constexpr int kGThreads = 32 * (kGWarps + 2);  // then the MMA's and TMA's warps
 
-// Four signed bytes -> bf16 pairs, exactly: the low 7 bits put into the mantissa of 128, less 128, or less
-// 256 where the sign bit is set.
+// Four signed bytes -> bf16 pairs of 2^-6 times them, exactly: a byte's bits alone are a bf16 value of 2^-133
+// times the byte (subnormal up to 127, the first binade from 128 on), so with the sign bit turned one fma by
+// 2^127 and less 2 gives (byte + 128 - 128) 2^-6.  Half the integer operations of putting it into a mantissa.
 __device__ __forceinline__ uint2 bytes_to_bf16(uint32_t w) {
+  const uint32_t u = w ^ 0x80808080u, big = 0x7F007F00u, two = 0xC000C000u;  // bf16 pairs of 2^127 and -2
   uint2 o;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t x = __byte_perm(w, 0u, h ? 0x4342 : 0x4140);
-    const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, t = (x & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&t));
+    const uint32_t x = __byte_perm(u, 0u, h ? 0x4342 : 0x4140);
+    const __nv_bfloat162 d =
+        __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&big),
+                *reinterpret_cast<const __nv_bfloat162*>(&two));
     (h ? o.y : o.x) = *reinterpret_cast<const uint32_t*>(&d);
   }
   return o;
@@ -694,8 +697,10 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   tc_fence_after();
   const uint32_t tmem = *slot;
   // first tile at or after i with such a row, nt if none
+  const bool plain = !adapter && a == 0;  // every row of every tile
   auto next_tile = [&](int i) {
-    while (i < nt && mask[i] == 0) ++i;
+    if (!plain)
+      while (i < nt && mask[i] == 0) ++i;
     return i;
   };
 
@@ -782,6 +787,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     auto fetch = [&](int i, Ahead& x) {
       if (i >= nt) return;
       const int64_t m0 = static_cast<int64_t>(t0 + i) * GM;
+      const int rows = M - m0 < GM ? static_cast<int>(M - m0) : GM;
       const uint8_t* v = static_cast<const uint8_t*>(V) + m0 * rank * (kV16 ? 2 : 4);
       const float* cs = kCodes ? code_scale + m0 * (C >> 8) + (c0 >> 8) : nullptr;
 #pragma unroll
@@ -789,7 +795,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         x.v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if constexpr (kCodes) x.cs[k] = 0.f;
         const int r = at[k] >> 16;
-        if (from[k] >= 0 && (mask32[2 * i + (r >> 5)] >> (r & 31) & 1)) {
+        if (from[k] >= 0 && (plain ? r < rows : (mask32[2 * i + (r >> 5)] >> (r & 31) & 1) != 0)) {
           if constexpr (kV16) {
             const uint2 w = ldg_here_u2(v + from[k] * 2);
             x.v[k].x = __uint_as_float(w.x);
@@ -807,9 +813,11 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     uint32_t ph = 0, rph = 0;
     auto make = [&](int i, Ahead& x) {
       uint8_t* z = base + s * p.stage;
+      // The MMA has read the stage's last tile.  With an odd number of stages that tile was the other set's, so
+      // this also says that it had landed: a wait on z_full goes by parity and must not be two rounds behind.
+      if (f >= p.stages && !mbar_sleep_warp(empty(s), ph ^ 1u, abort)) return false;
       if constexpr (kCodes) {
         // codes are finite: those of other adapters' rows meet zeros of V
-        if (f >= p.stages && !mbar_sleep_warp(empty(s), ph ^ 1u, abort)) return false;
         if (!mbar_sleep_warp(z_full(rs), rph, abort)) return false;
         const uint8_t* raw = base + p.off_raw + rs * kRawTile;
 #pragma unroll
@@ -822,7 +830,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         }
       } else {
         if (!mbar_sleep_warp(z_full(s), ph, abort)) return false;
-        const unsigned long long rows = mask[i];
+        const unsigned long long rows = plain ? ~0ull : mask[i];  // (rows past M are zeros already)
         if (~rows) {
 #pragma unroll 1
           for (int k = 0; k < GM / kGSet; ++k) {
@@ -876,7 +884,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
     const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 ranks
     const int c = c0 + 128 * half + 32 * q + lane;
-    const float sc = __ldg(scale + a);
+    const float sc = __ldg(scale + a) * (kCodes ? 64.f : 1.f);  // codes come as 2^-6 of themselves
     float* out = G + (static_cast<int64_t>(split) * L + a) * rank * C + c;
     if (ok && first < nt) {
       if (mbar_sleep_warp(acc_full, 0, abort)) {
