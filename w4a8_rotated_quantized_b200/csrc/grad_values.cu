@@ -125,14 +125,28 @@ __global__ void __launch_bounds__(32)
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 2);
     const int k0 = (threadIdx.x & 31) >> 2, l = threadIdx.x & 3;
     const bool in = u < n_down >> 8;
+    float4 v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < (in ? parts_down : 0); ++p) {  // (a part's 16 loads are on their way together)
+      const float* src = Gdown + p * n_down + u * 256 + 8 * l;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
+        v[k].x += f.x;
+        v[k].y += f.y;
+        v[k].z += f.z;
+        v[k].w += f.w;
+      }
+    }
     Pairs P;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float v[8];
-      add_parts(Gdown + u * 256 + 32 * (k ^ k0) + 8 * l, in ? parts_down : 0, n_down, v);
+    for (int k = 0; k < 16; ++k) {
+      const float e[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (k < 4) P.w[8 * (k & 3) + e].x = v[e]; else P.w[8 * (k & 3) + e].y = v[e];
+      for (int c = 0; c < 4; ++c) {
+        float2& pair = P.w[8 * ((k >> 1) & 3) + 4 * (k & 1) + c];
+        if (k < 8) pair.x = e[c]; else pair.y = e[c];
       }
     }
     fwht256_mapped<4>(P);

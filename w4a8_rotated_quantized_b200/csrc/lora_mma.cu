@@ -293,13 +293,13 @@ __global__ void __launch_bounds__(kVThreads, 1)
   }
   // this CTA's rows: the splits' sums added in order
   const int groups = rank >> 2;
-  for (int i = threadIdx.x; i < rows * groups; i += kVThreads) {
+  const int mine = M - m0 - split * rows < rows ? static_cast<int>(M - m0 - split * rows) : rows;  // up to the last row
+#pragma unroll 4
+  for (int i = threadIdx.x; i < mine * groups; i += kVThreads) {
     const int r = i / groups, j = 4 * (i - r * groups);
     const int64_t m = m0 + split * rows + r;
-    if (m >= M) break;
     const float* src = part + r * p.part_ld + j;
     float4 t = *reinterpret_cast<const float4*>(src);
-#pragma unroll 4
     for (int c = 1; c < splits; ++c) {
       const float4 u = *reinterpret_cast<const float4*>(src + c * rows * p.part_ld);
       t.x += u.x;
