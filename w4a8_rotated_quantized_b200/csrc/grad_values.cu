@@ -16,6 +16,7 @@
 
 #include "cr_device.cuh"
 #include "cr_internal.h"
+#include "grid_sync.cuh"
 #include "lora_device.cuh"
 
 namespace cr {
@@ -108,8 +109,8 @@ __device__ __forceinline__ void add_parts(const float* __restrict__ src, int par
   for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    const float4 f0 = __ldg(reinterpret_cast<const float4*>(src + p * stride));
-    const float4 f1 = __ldg(reinterpret_cast<const float4*>(src + p * stride + 4));
+    const float4 f0 = __ldcg(reinterpret_cast<const float4*>(src + p * stride));
+    const float4 f1 = __ldcg(reinterpret_cast<const float4*>(src + p * stride + 4));
     v[0] += f0.x; v[1] += f0.y; v[2] += f0.z; v[3] += f0.w;
     v[4] += f1.x; v[5] += f1.y; v[6] += f1.z; v[7] += f1.w;
   }
@@ -121,6 +122,7 @@ __device__ __forceinline__ void add_parts(const float* __restrict__ src, int par
 __global__ void __launch_bounds__(32)
     lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts_down, int parts_up, int64_t n_down,
                             int64_t n_up, uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up, int rot_blocks) {
+  griddep_wait();  // launched as a dependent of the products' kernel
   if (static_cast<int>(blockIdx.x) < rot_blocks) {
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 2);
     const int k0 = (threadIdx.x & 31) >> 2, l = threadIdx.x & 3;
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(32)
       const float* src = Gdown + p * n_down + u * 256 + 8 * l;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
         v[k].x += f.x;
         v[k].y += f.y;
         v[k].z += f.z;
@@ -190,9 +192,17 @@ cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int pa
   const unsigned rot = rotate && d_down ? static_cast<unsigned>((n_down / 256 + 7) / 8) : 0;
   const int64_t plain = (rot ? 0 : n_down) + n_up;
   const unsigned blocks = rot + static_cast<unsigned>((plain + 255) / 256);
-  lora_grad_finish_kernel<<<blocks, 32, 0, stream>>>(Gdown, Gup, parts_down, parts_up, n_down, n_up, d_down, d_up,
-                                                              static_cast<int>(rot));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(32, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_grad_finish_kernel, Gdown, Gup, parts_down, parts_up, n_down, n_up, d_down, d_up,
+                            static_cast<int>(rot));
 }
 
 }  // namespace cr

@@ -36,9 +36,10 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
 
 // Loads that stay where they are written: the compiler sinks plain read-only loads to their first use, which
 // undoes a prefetch into registers.
-__device__ __forceinline__ float4 ldg_here_f4(const float* p) {
+// (past L1: of what a kernel wrote that this one started beside)
+__device__ __forceinline__ float4 ldcg_here_f4(const float* p) {
   float4 v;
-  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint2 ldg_here_u2(const void* p) {

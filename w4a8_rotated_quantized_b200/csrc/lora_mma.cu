@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) griddep_launch_dependents();  // what follows may set itself up beside this kernel
   if (warp == 1 && lane == 0) {
     prefetch_tmap(&tmap_u);
     if (has_base) prefetch_tmap(&tmap_base);
@@ -680,6 +681,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     *abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == kGWarps + 1 && lane == 0) prefetch_tmap(&tmap_z);
   if (warp == kGWarps) {
     tmem_alloc(smem_u32(slot), p.cols);
@@ -801,7 +803,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
             x.v[k].x = __uint_as_float(w.x);
             x.v[k].y = __uint_as_float(w.y);
           } else {
-            x.v[k] = ldg_here_f4(reinterpret_cast<const float*>(v) + from[k]);
+            x.v[k] = ldcg_here_f4(reinterpret_cast<const float*>(v) + from[k]);
             if constexpr (kCodes) x.cs[k] = ldg_here_f1(cs + r * (C >> 8));
           }
         }
@@ -872,6 +874,8 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       if (kCodes && (rs += 2) >= kRaws) { rs -= kRaws; rph ^= 1u; }
       return true;
     };
+    // dV comes from the kernel before (Z and a bf16 V do not, and may be read beside it)
+    if constexpr (!kV16) griddep_wait();
     Ahead x;
     const int first = next_tile(0);
     int i = set ? next_tile(first + 1) : first;
@@ -882,6 +886,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       fetch(i, x);
     }
     // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
+    if constexpr (kV16) griddep_wait();  // this kernel's end is to mean the ones before have ended, too
     const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 ranks
     const int c = c0 + 128 * half + 32 * q + lane;
     const float sc = __ldg(scale + a) * (kCodes ? 64.f : 1.f);  // codes come as 2^-6 of themselves
@@ -1093,10 +1098,21 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
               : rank <= 32 ? (codes ? lora_grad_mma_kernel<true, 2> : lora_grad_mma_kernel<false, 2>)
               : rank <= 64 ? (codes ? lora_grad_mma_kernel<true, 4> : lora_grad_mma_kernel<false, 4>)
                            : (codes ? lora_grad_mma_kernel<true, 8> : lora_grad_mma_kernel<false, 8>);
-  kern<<<static_cast<unsigned>(down + up), kGThreads, smem, stream>>>(tx, ty, code_scale, dV, V, adapter, scale, Gdown,
-                                                                      Gup, M, K, N, rank, L, splits_down, splits_up,
-                                                                      static_cast<int>(down), status);
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  // a programmatic dependent of the kernel before it on the stream
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(down + up), 1, 1);
+  cfg.blockDim = dim3(kGThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tx, ty, code_scale, dV, V, adapter, scale, Gdown, Gup, M, K, N, rank, L,
+                            splits_down, splits_up, static_cast<int>(down), status) == cudaSuccess
+             ? CR_OK
+             : CR_ERR_CUDA;
 }
 
 }  // namespace cr
