@@ -495,13 +495,13 @@ cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, voi
  * cr_w4a4_grad_input -- input gradient of the W4A4 layer with its weights
  * frozen (the quantisation of X taken as the identity):
  *   dX = dY W^,   W^[n, :] = w_scale[n] * (q[n, :] H_group)
- * with float32 sums, rounded once to bf16.  For more than 256 tokens W^ is
- * rounded to bf16 before the product.  The same Wq and w_scale as the forward
- * calls (either scale mode).
+ * with float32 sums, rounded once to bf16.  For many tokens (more than 256, or
+ * 512 if N > K) W^ is rounded to bf16 before the product.  The same Wq and
+ * w_scale as the forward calls (either scale mode).
  *   dY  bf16 [M, N], row stride lddy >= N;  dX  out: bf16 [M, K], row stride lddx >= K
  * Shape and alignment rules as cr_w4a4_linear, lddy and lddx % 8 == 0,
  * N <= CR_MAX_K; N == 0 writes zeros.  The workspace holds the bf16 weights
- * (2 N K bytes; for at most 256 tokens partial sums instead) during the call;
+ * (2 N K bytes; for fewer tokens partial sums instead) during the call;
  * none of it needs to be zero before.
  */
 size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group);

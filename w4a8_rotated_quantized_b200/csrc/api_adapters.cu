@@ -208,7 +208,7 @@ cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, voi
 size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group) {
   (void)group;
   if (M < 0 || N <= 0 || K < 256 || K % 256 != 0) return kWsHead;
-  if (M > 0 && M <= cr::kGradInputFewMaxM)
+  if (M > 0 && cr::use_grad_input_few(M, N, K))
     return kWsHead + cr::round_up(cr::grad_input_few_operand_rows(M) * N * 2, 256) +
            bytes_f32(static_cast<int64_t>(M) * K * cr::grad_input_few_splits(M, N, K, kSizingSms));
   return kWsHead + cr::round_up(static_cast<size_t>(N) * static_cast<size_t>(K) * 2, 256);
@@ -235,7 +235,7 @@ cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const
     return cuda_status(cudaMemset2DAsync(dX, static_cast<size_t>(lddx) * 2, 0, static_cast<size_t>(K) * 2,
                                          static_cast<size_t>(M), s));
   uint16_t* w = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWsHead);
-  if (M <= cr::kGradInputFewMaxM) {
+  if (cr::use_grad_input_few(M, N, K)) {
     float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead +
                                            cr::round_up(cr::grad_input_few_operand_rows(M) * N * 2, 256));
     return static_cast<cr_status>(cr::launch_grad_input_few(

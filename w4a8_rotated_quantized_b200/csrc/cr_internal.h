@@ -199,7 +199,7 @@ int launch_gemm_bf16(const void* A, int64_t lda, const void* W, void* Y, int64_t
 
 // The same gradient for few tokens, straight from the packed weights (grad_input_few.cu): V holds the product's
 // bf16 [operand_rows, N] operand, P `splits` partial sums float32 [M, K].
-constexpr int kGradInputFewMaxM = 256;
+bool use_grad_input_few(int M, int N, int K);
 int grad_input_few_splits(int M, int N, int K, int num_sms);
 size_t grad_input_few_operand_rows(int M);
 int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, const float* w_scale, uint16_t* V,

@@ -6,10 +6,10 @@
 // few tokens that leaves the packed weights, half a byte each, as all that has to be read.  (Unpacking them to
 // bf16 first writes and reads four times their bytes: 36 us of GPU time for 130 tokens, 9728 x 2560.)
 //
-// * A CTA takes 256 columns of the weights, a block of up to 128 tokens and a part of the sum over n, 64 rows of
-//   the weights at a time: the packed codes arrive by TMA, become bf16 (exact) and are the product's M side as
-//   they lie (MN-major); s_w dY, split into rounded values and rests (16 bits of mantissa), is its N side.  Two
-//   sets of eight warps prepare alternate tiles of codes.
+// * A CTA takes 256 columns of the weights, up to 256 tokens and a part of the sum over n, 64 rows of the weights
+//   at a time: the packed codes arrive by TMA, become bf16 (exact) and are the product's M side as they lie
+//   (MN-major); s_w dY, split into rounded values and rests (16 bits of mantissa) that go into the same sums, is
+//   its N side.  Two sets of eight warps prepare alternate tiles of codes.
 // * s_w dY is split once, by a small kernel before: split in each CTA it cost as much as the codes (128 tokens,
 //   9728 x 2560: 23 us against 15).  This one starts beside it and waits for it before the first N side's load.
 // * float32 sums in TMEM; the parts of the sum go to the workspace and a third kernel adds them in order,
@@ -39,27 +39,28 @@ constexpr int GC = 256;            // columns of a CTA
 constexpr int kBox = GN * 128;     // 64 rows x 64 bf16 columns
 constexpr int kZTile = 4 * kBox;
 constexpr int kRawTile = GN * GC / 2;
-constexpr int kRaws = 4;
 constexpr int kSet = 8;            // warps of a set
 constexpr int kWarps = 2 * kSet;
 constexpr int kThreads = 32 * (kWarps + 3);  // then the MMA's warp and those that load the codes and the N side
-constexpr int kMostTokens = 128;   // of a block
+constexpr int kMostTokens = 256;   // of a block
 constexpr int kSmemMax = 232448 - 1024;
 
 struct Plan {
-  int blocks, rp, stage, stages, off_raw, off_bar, smem, cols;  // rp: rows of a token block
+  int blocks, rp, raws, stage, stages, off_raw, off_bar, smem, cols;  // rp: rows of a token block
 };
 inline __host__ __device__ Plan plan(int M) {
   Plan p;
   p.blocks = (M + kMostTokens - 1) / kMostTokens;
-  p.rp = ((M + p.blocks - 1) / p.blocks + 7) & ~7;
-  p.stage = kZTile + ((2 * p.rp * 128 + 1023) & ~1023);
-  p.stages = (kSmemMax - 256 - kRaws * kRawTile) / p.stage;
+  p.rp = ((M + p.blocks - 1) / p.blocks + 15) & ~15;
+  p.stage = kZTile + 2 * p.rp * 128;
+  // an even number of raw tiles, so that each set of warps meets its slots round by round
+  p.raws = p.stage <= 48 * 1024 ? 4 : 2;
+  p.stages = (kSmemMax - 256 - p.raws * kRawTile) / p.stage;
   if (p.stages > 4) p.stages = 4;
   p.off_raw = p.stages * p.stage;
-  p.off_bar = p.off_raw + kRaws * kRawTile;
+  p.off_bar = p.off_raw + p.raws * kRawTile;
   p.smem = p.off_bar + 256;
-  const int c = 4 * p.rp;  // two halves of the columns, values and rests
+  const int c = 2 * p.rp;  // two halves of the columns
   p.cols = c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : c <= 256 ? 256 : 512;
   return p;
 }
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == kWarps + 1 && lane == 0) {
     prefetch_tmap(&tmap_w);
     prefetch_tmap(&tmap_v);
@@ -164,19 +166,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t ph = 0, last_bar = 0, last_ph = 0;
       int s = 0, i = 0;
-      const uint32_t idesc = idesc_bf16(128, 2 * p.rp, true, false);
+      const uint32_t idesc = idesc_bf16(128, p.rp, true, false);
       for (; i < nt; ++i) {
         if (!mbar_sleep(v_full(s), ph, abort) || !mbar_sleep(ready(s), ph, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t z = smem_u32(base + s * p.stage);
-        const uint64_t dv = sw128_kmajor_desc(z + kZTile);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kBox, kBox);
 #pragma unroll
-          for (int kk = 0; kk < GN / 16; ++kk)
-            umma_f16_ss(tmem + static_cast<uint32_t>(half * 2 * p.rp), dz + 128u * kk, dv + 2u * kk, idesc,
-                        (i || kk) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {  // rounded values, rests
+            const uint64_t dv = sw128_kmajor_desc(z + kZTile + h * p.rp * 128);
+#pragma unroll
+            for (int kk = 0; kk < GN / 16; ++kk)
+              umma_f16_ss(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 2u * kk, idesc,
+                          (i || h || kk) ? 1u : 0u);
+          }
         }
         umma_commit(empty(s));
         last_bar = empty(s);
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_sleep(raw_empty(s), ph, abort)) { ok = false; break; }
         mbar_arrive_expect_tx(raw_full(s), kRawTile);
         tma_load_2d(smem_u32(base + p.off_raw + s * kRawTile), &tmap_w, c0 / 2, (t0 + i) * GN, raw_full(s));
-        if (++s == kRaws) { s = 0; ph ^= 1u; }
+        if (++s == p.raws) { s = 0; ph ^= 1u; }
       }
       if (!ok) give_up(abort, status);
     }
@@ -215,7 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < nt; ++i) {
         if (!mbar_sleep(empty(s), ph, abort)) { ok = false; break; }
         mbar_arrive_expect_tx(v_full(s), 2 * p.rp * 128);
-        tma_load_2d(smem_u32(base + s * p.stage + kZTile), &tmap_v, (t0 + i) * GN, block * 2 * p.rp, v_full(s));
+        const uint32_t v = smem_u32(base + s * p.stage + kZTile);
+        tma_load_2d(v, &tmap_v, (t0 + i) * GN, block * 2 * p.rp, v_full(s));
+        tma_load_2d(v + p.rp * 128, &tmap_v, (t0 + i) * GN, block * 2 * p.rp + p.rp, v_full(s));
         if (++s == p.stages) { s = 0; ph ^= 1u; }
       }
       if (!ok) give_up(abort, status);
@@ -244,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(raw_empty(rs));
       }
       if ((s += 2) >= p.stages) { s -= p.stages; ph ^= 1u; }
-      if ((rs += 2) >= kRaws) { rs -= kRaws; rph ^= 1u; }
+      if ((rs += 2) >= p.raws) { rs -= p.raws; rph ^= 1u; }
     }
     // ---------------------------------------------------------------- epilogue: column 128 half + 32 q + lane
     const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 tokens
@@ -255,19 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
 #pragma unroll 1
       for (int j = 16 * part; j < p.rp; j += 32) {
-        uint32_t r[16], l[16];  // (past the block's tokens: columns that nobody keeps)
-        const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * 2 * p.rp + j);
-        tmem_ld8(src, r);
-        tmem_ld8(src + static_cast<uint32_t>(p.rp), l);
-        if (j + 8 < p.rp) {
-          tmem_ld8(src + 8u, r + 8);
-          tmem_ld8(src + static_cast<uint32_t>(p.rp) + 8u, l + 8);
-        }
+        uint32_t r[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * p.rp + j), r);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (j + e < p.rp && m0 + j + e < M)
-            out[static_cast<int64_t>(j + e) * K] = __uint_as_float(r[e]) + __uint_as_float(l[e]);
+          if (m0 + j + e < M) out[static_cast<int64_t>(j + e) * K] = __uint_as_float(r[e]);
       }
     } else {
       record_status(status, CR_ERR_TIMEOUT);
@@ -291,6 +291,7 @@ template <int kDig>
 __global__ void __launch_bounds__(128)
     grad_input_finish_kernel(const float* __restrict__ P, int parts, int64_t stride, uint16_t* __restrict__ dX,
                              int64_t lddx, int64_t units, int upr) {
+  griddep_wait();  // launched as a dependent of the product's kernel
   __shared__ float4 sums[3][16][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (lane >> 2);
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(128)
     const float* src = P + p * stride + u * 256 + 8 * l;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
       v[k].x += f.x;
       v[k].y += f.y;
       v[k].z += f.z;
@@ -362,6 +363,12 @@ bool set_attrs() {
 
 }  // namespace
 
+// Against unpacking the weights for the bf16 GEMM (us of GPU time, this form first): 9728 x 2560 (K x N) 1 token
+// 17 | 36, 256 tokens 41 | 52, 512 tokens 71 | 51; 3072 x 12288 256 tokens 47 | 95,
+// 512 tokens 78 | 97; 2560 x 9728 512 tokens 62 | 74.  A long sum favours this form: the GEMM's few tiles leave
+// most SMs idle.
+bool use_grad_input_few(int M, int N, int K) { return M <= 256 || (M <= 512 && N > K); }
+
 int grad_input_few_splits(int M, int N, int K, int num_sms) {
   const int tiles = (N + GN - 1) / GN;
   const int ctas = K / GC * plan(M).blocks;
@@ -392,7 +399,7 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, N, K / 2, K / 2, GC / 2, GN, CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
       !make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, V, grad_input_few_operand_rows(M), N,
-                    static_cast<uint64_t>(N) * 2, 64, 2 * p.rp, CU_TENSOR_MAP_SWIZZLE_128B,
+                    static_cast<uint64_t>(N) * 2, 64, p.rp, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return CR_ERR_CUDA;
   const dim3 ogrid((N / 8 + 255) / 256, p.blocks * p.rp);
@@ -415,8 +422,12 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
              : group == 64 ? grad_input_finish_kernel<3>
              : group == 256 ? grad_input_finish_kernel<4>
                             : grad_input_finish_kernel<5>;
-  fin<<<blocks, 128, 0, stream>>>(P, splits, stride, dX, lddx, units, K / 256);
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  const float* sums = P;
+  return cudaLaunchKernelEx(&cfg, fin, sums, splits, stride, dX, lddx, units, K / 256) == cudaSuccess ? CR_OK
+                                                                                                      : CR_ERR_CUDA;
 }
 
 }  // namespace cr
