@@ -4,7 +4,9 @@ Every function here only marshals arguments: it allocates outputs with
 torch, passes raw device pointers, sizes and the current CUDA stream to the
 library, and raises ``ConvRotError`` on a non-zero status.  All arithmetic of
 the layer runs in the library's CUDA kernels; there is no CPU fallback and
-importing this module fails loudly when the library has not been built.
+importing this module fails loudly when the library has not been built.  The
+calls whose GPU time is a few microseconds are marshalled by the extension
+module ``_calls`` instead of ctypes.
 """
 
 from __future__ import annotations
@@ -667,108 +669,20 @@ def cr_selftest_wait_timeout(ws: torch.Tensor) -> None:
 
 # ---------------------------------------------------------------------------
 # Low-rank adapters beside a projection, 8-bit activation checkpoints, and the packed layer's input
-# gradient.  Their scratch is a buffer of its own for each call, taken from torch's allocator on the
-# current stream (inside a graph capture: from the graph's pool), so calls on several streams and
-# captured graphs share nothing.  A caller's ``workspace`` takes its place; its status word can then be
-# read with ``cr_read_device_status(ws=...)``.
+# gradient.  A single token's call runs a few microseconds on the GPU, so the checks and the call itself are
+# in the extension module (csrc/py_calls.cpp).  Scratch is a buffer of its own for each call, taken from
+# torch's allocator on the current stream (inside a graph capture: from the graph's pool), so calls on several
+# streams and captured graphs share nothing.  A caller's ``workspace`` takes its place; its status word can
+# then be read with ``cr_read_device_status(ws=...)``.
 # ---------------------------------------------------------------------------
 
-def _run(name: str, dev: torch.device, *args) -> None:
-    """The library call on the current stream of ``dev``, with that device current."""
-    i = dev.index
-    if torch._C._cuda_getDevice() == i:
-        st = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(i))
-    else:
-        with torch.cuda.device(i):
-            st = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(i))
-    if st != CR_OK:
-        raise ConvRotError(name, st)
+try:
+    from . import _calls
+except ImportError as e:
+    raise ImportError("the extension module _calls is not built; build it with "
+                      "`python -m w4a8_rotated_quantized_b200.build`") from e
 
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-_sizes: dict = {}
-
-
-def _ws_size(name: str, *dims: int) -> int:
-    """The library's workspace size for these dimensions, kept for the next call with the same ones."""
-    key = (name, dims)
-    n = _sizes.get(key)
-    if n is None:
-        if len(_sizes) > 4096:
-            _sizes.clear()
-        n = _sizes[key] = getattr(_lib, name)(*dims)
-    return n
-
-
-def _scratch(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor):
-    """(address, bytes, tensor) of the workspace; a bf16 buffer like ``like`` if none is given and one is needed."""
-    if given is None:
-        if nbytes == 0:
-            return None, 0, None
-        given = like.new_empty((nbytes + 1) // 2)
-        return given.data_ptr(), nbytes, given
-    _dev(given, "workspace", torch.uint8, like.device)
-    if given.dim() != 1 or not given.is_contiguous():
-        raise ValueError("workspace must be a contiguous 1-D uint8 tensor")
-    return given.data_ptr(), given.numel(), given
-
-
-def _input(t: torch.Tensor, name: str) -> Tuple[int, int, int, torch.device]:
-    """The call's first operand, bf16 [M, C] on a CUDA device with dense columns: M, C, row stride, device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    M, C = t.shape
-    return M, C, _matrix(t, name, t.device, M, C), t.device
-
-
-def _matrix(t: torch.Tensor, name: str, device: torch.device, M: int, C: int) -> int:
-    """A bf16 [M, C] matrix with dense columns; returns its row stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device:
-        raise TypeError(f"{name} must be a bfloat16 tensor on {device}")
-    if t.shape != (M, C):
-        raise ValueError(f"{name} must have shape {(M, C)}, got {tuple(t.shape)}")
-    ld, unit = t.stride()
-    if C > 1 and M > 0 and unit != 1:
-        raise ValueError(f"{name} must have unit stride along the last dimension")
-    return C if M <= 1 or C == 0 else ld  # the stride of a single row or of an empty tensor says nothing
-
-
-def _out_matrix(out: Optional[torch.Tensor], like: torch.Tensor, M: int, C: int) -> Tuple[torch.Tensor, int]:
-    if out is None:
-        return like.new_empty((M, C)), C
-    return out, _matrix(out, "out", like.device, M, C)
-
-
-def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: Tuple[int, ...]) -> int:
-    """The address of a contiguous tensor of exactly this shape, dtype and device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.shape != shape \
-            or not t.is_contiguous():
-        _dense(t, name, dtype, device, shape)  # says what is wrong
-    return t.data_ptr()
-
-
-def _factors(down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor, adapter: Optional[torch.Tensor],
-             dev: torch.device, M: int, K: Optional[int], N: Optional[int]):
-    """(adapters, rank, K, N) of the pool and the addresses of down [L, r, K], up [L, r, N], scale [L] and the
-    rows' adapters [M]; K or N is given by the call's first operand."""
-    if not isinstance(down, torch.Tensor) or not isinstance(up, torch.Tensor):
-        raise TypeError("down and up must be tensors")
-    if down.dim() != 3 or up.dim() != 3:
-        raise ValueError("down and up must be 3-D [adapters, rank, columns]")
-    L, r, k = down.shape
-    n = up.shape[2]
-    if K is None:
-        K = k
-    if N is None:
-        N = n
-    return (L, r, K, N, _exact(down, "down", torch.bfloat16, dev, (L, r, K)), _exact(up, "up", torch.bfloat16, dev, (L, r, N)),
-            _exact(scale, "scale", torch.float32, dev, (L,)),
-            None if adapter is None else _exact(adapter, "adapter", torch.int32, dev, (M,)))
+_calls.set_error(ConvRotError)
 
 
 def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
@@ -781,15 +695,7 @@ def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale
     row uses adapter 0; without ``base`` the sum starts at zero.  ``out`` may be ``base`` itself.  With
     ``save_v`` returns (Y, V), V bf16 [M, r] = X down[a]^T for the backward pass.
     """
-    M, K, ldx, dev = _input(X, "X")
-    L, r, _, N, p_down, p_up, p_scale, p_adapter = _factors(down, up, scale, adapter, dev, M, K, None)
-    ldb = 0 if base is None else _matrix(base, "base", dev, M, N)
-    Y, ldy = _out_matrix(out, X, M, N)
-    V = X.new_empty((M, r)) if save_v else None
-    ws, nws, keep = _scratch(workspace, _ws_size("cr_lora_forward_workspace_size", M, N, K, r, L), X)
-    _run("cr_lora_forward", dev, X.data_ptr(), ldx, p_adapter, p_down, p_up, p_scale, _addr(base), ldb, Y.data_ptr(), ldy,
-         _addr(V), M, N, K, r, L, ws, nws)
-    return (Y, V) if save_v else Y
+    return _calls.lora_forward(X, down, up, scale, adapter, base, out, save_v, workspace)
 
 
 def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch.Tensor, up: torch.Tensor,
@@ -802,69 +708,21 @@ def cr_lora_backward(dY: torch.Tensor, X, V: Optional[torch.Tensor], down: torch
     needed); ``V`` is what the forward kept (None if d_up is not needed).  dX starts at ``base`` (the
     projection's own input gradient; zero without it); ``out`` takes dX and may be ``base`` itself.
     """
-    M, N, lddy, dev = _input(dY, "dY")
-    L, r, K, _, p_down, p_up, p_scale, p_adapter = _factors(down, up, scale, adapter, dev, M, None, N)
-    if need_down and X is None:
-        raise ValueError("X (or its checkpoint) is needed for d_down")
-    if need_up and V is None:
-        raise ValueError("V is needed for d_up")
-    p_x = p_codes = p_scales = None
-    ldx = 0
-    if isinstance(X, (tuple, list)):
-        if len(X) != 2:
-            raise ValueError("a checkpoint is (codes, scales)")
-        p_codes = _exact(X[0], "codes", torch.int8, dev, (M, K))
-        p_scales = _exact(X[1], "scales", torch.float32, dev, (M, K // 256))
-    elif X is not None:
-        ldx = _matrix(X, "X", dev, M, K)
-        p_x = X.data_ptr()
-    p_v = None if V is None else _exact(V, "V", torch.bfloat16, dev, (M, r))
-    ldb = 0 if base is None else _matrix(base, "base", dev, M, K)
-    if out is not None and not need_dx:
-        raise ValueError("out takes dX, which is not needed")
-    dX, lddx = _out_matrix(out, dY, M, K) if need_dx else (None, 0)
-    dd = dY.new_empty((L, r, K)) if need_down else None
-    du = dY.new_empty((L, r, N)) if need_up else None
-    ws, nws, keep = _scratch(workspace, _ws_size("cr_lora_backward_workspace_size", M, N, K, r, L), dY)
-    _run("cr_lora_backward", dev, dY.data_ptr(), lddy, p_x, ldx, p_codes, p_scales, p_v, p_adapter, p_down, p_up, p_scale,
-         _addr(base), ldb, _addr(dX), lddx, _addr(dd), _addr(du), M, N, K, r, L, ws, nws)
-    return dX, dd, du
+    return _calls.lora_backward(dY, X, V, down, up, scale, adapter, base, out, need_dx, need_down, need_up, workspace)
 
 
 def cr_ckpt_save(X: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """X bf16 [M, K] in 8 bits: (codes int8 [M, K] of the rotated rows, scales float32 [M, K/256])."""
-    M, K, ldx, dev = _input(X, "X")
-    codes = X.new_empty((M, K), dtype=torch.int8)
-    scales = X.new_empty((M, K // 256), dtype=torch.float32)
-    _run("cr_ckpt_save", dev, X.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    return _calls.ckpt_save(X)
 
 
 def cr_ckpt_load(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The bf16 [M, K] values that a checkpoint of :func:`cr_ckpt_save` stands for."""
-    M, K = _codes(codes, "codes", torch.int8)
-    _cuda(codes, "codes")
-    dev = codes.device
-    p_scales = _exact(scales, "scales", torch.float32, dev, (M, K // 256))
-    if out is None:
-        X, ldx = codes.new_empty((M, K), dtype=torch.bfloat16), K
-    else:
-        X, ldx = out, _matrix(out, "out", dev, M, K)
-    _run("cr_ckpt_load", dev, codes.data_ptr(), p_scales, M, K, X.data_ptr(), ldx)
-    return X
+    return _calls.ckpt_load(codes, scales, out)
 
 
 def cr_w4a4_grad_input(dY: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, group: int = GROUP,
                        out: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Input gradient of the W4A4 layer with frozen weights: dX bf16 [M, K] = dY [M, N] . (w_scale * Wq H_group)."""
-    M, N, lddy, dev = _input(dY, "dY")
-    if not isinstance(Wq, torch.Tensor) or Wq.dim() != 2:
-        raise TypeError("Wq must be a 2-D tensor [N, K/2]")
-    K = 2 * Wq.shape[1]
-    p_w = _exact(Wq, "Wq", torch.uint8, dev, (N, K // 2))
-    p_s = _exact(w_scale, "w_scale", torch.float32, dev, (N,))
-    dX, lddx = _out_matrix(out, dY, M, K)
-    ws, nws, keep = _scratch(workspace, _ws_size("cr_w4a4_grad_input_workspace_size", M, N, K, group), dY)
-    _run("cr_w4a4_grad_input", dev, dY.data_ptr(), lddy, p_w, p_s, dX.data_ptr(), lddx, M, N, K, group, ws, nws)
-    return dX
+    return _calls.grad_input(dY, Wq, w_scale, group, out, workspace)

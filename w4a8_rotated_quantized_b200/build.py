@@ -1,8 +1,10 @@
-"""Build the in-tree CUDA library (sm_100a only) with nvcc.
+"""Build the in-tree CUDA library (sm_100a only) with nvcc, and the extension module ``_calls`` with g++.
 
 The shared library is written next to this file as ``libconvrot_b200.so``
 and object files go to ``_build/``.  nvcc cross-compiles for sm_100a on a
-machine without a GPU.
+machine without a GPU.  ``_calls.so`` marshals the calls whose GPU time is a
+few microseconds; it is compiled against the installed torch and links to the
+library beside it.
 """
 
 from __future__ import annotations
@@ -11,12 +13,15 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconvrot_b200.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
 SOURCES = ["api.cu", "act_kernels.cu", "gemm_w4a4.cu", "gemm_w4a4_pair.cu", "gemm_w4a4_small.cu", "gemm_i8.cu",
            "gemm_w4a8.cu", "gemm_a8w4.cu", "tmap.cu", "noalloc.cu",
            "selftest.cu", "api_adapters.cu", "lora_rows.cu", "lora_mma.cu", "grad_values.cu", "ckpt_mma.cu", "gemm_bf16.cu",
@@ -40,6 +45,19 @@ def _mtime(p: str) -> float:
     return os.path.getmtime(p) if os.path.exists(p) else -1.0
 
 
+def _calls_cmd() -> list:
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(t, "include"),
+            "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"), "-isystem", cuda, CALLS_SRC,
+            "-o", CALLS, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every .cu source and link the shared library; return its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -59,7 +77,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
@@ -68,6 +86,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 sys.stderr.write(err)
     if jobs or force or _mtime(LIB) < max(_mtime(o) for o in objs):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs])
+    if force or _mtime(CALLS) < max(_mtime(CALLS_SRC), _mtime(HEADERS[0])):
+        run(_calls_cmd())
     return LIB
 
 
