@@ -76,22 +76,24 @@ struct Bars {
   __device__ uint32_t acc_empty(int i) const { return b + 144u + 8u * i; }
 };
 
-// Barriers, TMEM and what both kernels share of their start; returns the TMEM base.
-__device__ __forceinline__ uint32_t start(const Bars& bars, uint8_t* misc, int stages) {
-  uint32_t* slot = reinterpret_cast<uint32_t*>(misc);
-  volatile int* abort = reinterpret_cast<volatile int*>(misc + 4);
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(bars.full(s), 1);
-      mbar_init(bars.empty(s), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars.acc_full(i), 1);
-      mbar_init(bars.acc_empty(i), 8);
-    }
-    *abort = 0;
-    fence_mbar_init();
+// Barriers, by the TMA's thread: it asks for its first boxes at once, before the rest of the block is set up.
+__device__ __forceinline__ void init_bars(const Bars& bars, volatile int* abort, int stages) {
+  for (int s = 0; s < stages; ++s) {
+    mbar_init(bars.full(s), 1);
+    mbar_init(bars.empty(s), 1);
   }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(bars.acc_full(i), 1);
+    mbar_init(bars.acc_empty(i), 8);
+  }
+  *abort = 0;
+  fence_mbar_init();
+  fence_proxy_async_smem();
+}
+
+// TMEM and the block's meeting; returns the TMEM base.
+__device__ __forceinline__ uint32_t start(uint8_t* misc) {
+  uint32_t* slot = reinterpret_cast<uint32_t*>(misc);
   if (threadIdx.x < 32) {
     tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
@@ -132,9 +134,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 4);
   const int64_t tiles = (static_cast<int64_t>(M) + TM - 1) / TM * slices;
 
+  auto load = [&](int64_t t, int i, int s) {
+    mbar_arrive_expect_tx(bars.full(s), kBox);
+    tma_load_2d(smem_u32(base + kSaveOffRing + s * kBox), &tmap_x, static_cast<int>(t % slices) * TC + 64 * i,
+                static_cast<int>(t / slices) * TM, bars.full(s));
+  };
   if (warp == 1 && lane == 0) {
-    prefetch_tmap(&tmap_x);
-    prefetch_tmap(&tmap_c);
+    init_bars(bars, abort, kSaveStages);
+    for (int i = 0; i < 4; ++i) load(blockIdx.x, i, i);  // (there is no block without a tile)
   }
   // [H64, H64], [-H64, H64], [H64, -H64]: 128 rows of 64 values, 16-byte pieces in the 128-byte swizzle's places
   for (int e = threadIdx.x; e < 3 * TM * 8; e += kThreads) {
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) w[i] = 0x3F803F80u | (m >> (2 * i) & 1) << 15 | (m >> (2 * i + 1) & 1) << 31;
     *reinterpret_cast<uint4*>(base + v * kBox + n * 128 + ((piece ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  const uint32_t tmem = start(bars, misc, kSaveStages);
+  const uint32_t tmem = start(misc);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -185,16 +192,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      int s = 0;
+      int s = 4;  // the first tile is on its way
       uint32_t ph = 1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const int x = static_cast<int>(t % slices) * TC, y = static_cast<int>(t / slices) * TM;
+      for (int64_t t = static_cast<int64_t>(blockIdx.x) + gridDim.x; ok && t < tiles; t += gridDim.x) {
         for (int i = 0; i < 4; ++i) {
+          if (s == kSaveStages) { s = 0; ph ^= 1u; }
           if (!mbar_sleep(bars.empty(s), ph, abort)) { ok = false; break; }
-          mbar_arrive_expect_tx(bars.full(s), kBox);
-          tma_load_2d(smem_u32(base + kSaveOffRing + s * kBox), &tmap_x, x + 64 * i, y, bars.full(s));
-          if (++s == kSaveStages) { s = 0; ph ^= 1u; }
+          load(t, i, s++);
         }
       }
       if (!ok) gave_up(abort);
@@ -283,9 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 4);
   const int64_t tiles = (static_cast<int64_t>(M) + TM - 1) / TM * slices;
 
+  auto load = [&](int64_t t, int kb, int s) {
+    mbar_arrive_expect_tx(bars.full(s), kBox);
+    tma_load_2d(smem_u32(base + kLoadOffRing + s * kBox), &tmap_c, static_cast<int>(t % slices) * TC + 128 * kb,
+                static_cast<int>(t / slices) * TM, bars.full(s));
+  };
   if (warp == 1 && lane == 0) {
-    prefetch_tmap(&tmap_c);
-    prefetch_tmap(&tmap_x);
+    init_bars(bars, abort, kLoadStages);
+    for (int i = 0; i < 2; ++i) load(blockIdx.x, i, i);  // (there is no block without a tile)
   }
   // H256 as bytes: for each 128 of the sum, 256 rows of 128 bytes
   for (int e = threadIdx.x; e < 2 * TC * 8; e += kThreads) {
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w[i] = ((m >> (4 * i) & 15u) * 0x00204081u & 0x01010101u) * 0xFEu + 0x01010101u;
     *reinterpret_cast<uint4*>(base + kb * 2 * kBox + n * 128 + ((piece ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  const uint32_t tmem = start(bars, misc, kLoadStages);
+  const uint32_t tmem = start(misc);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -331,16 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      int s = 0;
+      int s = 2;  // the first tile is on its way
       uint32_t ph = 1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const int x = static_cast<int>(t % slices) * TC, y = static_cast<int>(t / slices) * TM;
+      for (int64_t t = static_cast<int64_t>(blockIdx.x) + gridDim.x; ok && t < tiles; t += gridDim.x) {
         for (int kb = 0; kb < 2; ++kb) {
+          if (s == kLoadStages) { s = 0; ph ^= 1u; }
           if (!mbar_sleep(bars.empty(s), ph, abort)) { ok = false; break; }
-          mbar_arrive_expect_tx(bars.full(s), kBox);
-          tma_load_2d(smem_u32(base + kLoadOffRing + s * kBox), &tmap_c, x + 128 * kb, y, bars.full(s));
-          if (++s == kLoadStages) { s = 0; ph ^= 1u; }
+          load(t, kb, s++);
         }
       }
       if (!ok) gave_up(abort);
