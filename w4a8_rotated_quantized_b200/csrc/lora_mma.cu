@@ -401,8 +401,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  // (base tiles need no adapters: their warp goes on)
-  const int nd = warp == 1 ? 0 : tile_adapters(adapter, m0, M, L, ids, list, counts, kYMmaThreads - 32);
+  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts, kYMmaThreads);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -450,6 +449,9 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       int y = 0;
       uint32_t yph = 0;
       for (int t = t0; t < t1; ++t) {
+        // two tiles, then V's turn: behind the whole ring's loads it would take microseconds to arrive (4096 x
+        // 3072 -> 3072 at rank 64: 28.7 us a call with the ring first, 26.6 so)
+        if (t - t0 == 2 && nd > 0 && !mbar_sleep(v_ready, 0, abort)) { ok = false; break; }
         if (t - t0 >= p.nb && !mbar_sleep(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
         const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
         if (has_base) {
