@@ -425,7 +425,8 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  *   X        bf16 [M, K], row stride ldx >= K
  *   base     bf16 [M, N], row stride ldb >= N (the projection's output), or
  *            NULL for zero.  base may be Y itself (same pointer and stride);
- *            any other overlap is an error of the caller.
+ *            any other overlap is an error of the caller (refused where the
+ *            pointers are equal).
  *   Y        out: bf16 [M, N], row stride ldy >= N.  Rows without adapter: base.
  *   V        out: bf16 [M, rank], dense: V rounded once, for the backward pass;
  *            NULL if not wanted.  (Y is computed from the float32 V.)

@@ -66,17 +66,18 @@ def test_oracle_bound_catches_a_planted_mistake():
 @pytest.mark.skipif(torch.cuda.is_available(), reason="fake device pointers are only safe where no GPU can be reached")
 def test_refusals_by_code():
     lib, P = b._lib, ctypes.c_void_p
-    A, odd, n0 = P(1 << 20), P((1 << 20) + 8), P(None)
+    A, B, C, odd, n0 = P(1 << 20), P(1 << 22), P(1 << 23), P((1 << 20) + 8), P(None)
     ws, wsn = P(1 << 21), 1 << 26
     DEV = (4, 6)
 
-    def fwd(X=A, ldx=512, ad=A, dn=A, up=A, sc=A, base=A, ldb=264, Y=A, ldy=264, V=n0, M=40, N=264, K=512, r=8, L=2,
+    def fwd(X=A, ldx=512, ad=A, dn=A, up=A, sc=A, base=C, ldb=264, Y=B, ldy=264, V=n0, M=40, N=264, K=512, r=8, L=2,
             w=ws, n=wsn):
         return lib.cr_lora_forward(X, ldx, ad, dn, up, sc, base, ldb, Y, ldy, V, M, N, K, r, L, w, n, None)
 
     assert fwd() in DEV and fwd(ad=n0, base=n0, ldb=0) in DEV and fwd(V=A) in DEV
     assert fwd(X=n0, dn=n0, up=n0, sc=n0, Y=n0, base=n0, M=0) in DEV
     assert fwd(X=n0) == 1 and fwd(dn=n0) == 1 and fwd(up=n0) == 1 and fwd(sc=n0) == 1 and fwd(Y=n0) == 1
+    assert fwd(base=B) in DEV and fwd(base=B, ldb=272) == 1 and fwd(Y=A) == 1  # in place: the base, with its stride
     assert fwd(M=-1) == 1 and fwd(L=-1) == 1 and fwd(r=-4) == 1 and fwd(ldx=-8) == 1
     assert fwd(r=6) == 2 and fwd(r=0) == 2 and fwd(r=132) == 2 and fwd(L=0) == 2 and fwd(L=4097) == 2
     assert fwd(K=516) == 2 and fwd(N=260) == 2 and fwd(N=0) == 2 and fwd(K=65544, ldx=65544) == 2
@@ -88,13 +89,14 @@ def test_refusals_by_code():
     assert fwd(M=4000, n=need) in DEV and fwd(M=4000, n=need - 1) == 5 and fwd(M=4000, w=n0) == 5
     assert fwd(M=4000, w=P((1 << 21) + 128)) == 5
 
-    def bwd(dY=A, X=A, ldx=512, c=n0, cs=n0, V=A, ad=A, dn=A, up=A, sc=A, base=A, ldb=512, dX=A, lddx=512, dd=A, du=A,
+    def bwd(dY=A, X=A, ldx=512, c=n0, cs=n0, V=A, ad=A, dn=A, up=A, sc=A, base=C, ldb=512, dX=B, lddx=512, dd=A, du=A,
             M=40, N=264, K=512, r=8, L=2, w=ws, n=wsn):
         return lib.cr_lora_backward(dY, 264, X, ldx, c, cs, V, ad, dn, up, sc, base, ldb, dX, lddx, dd, du, M, N, K, r, L,
                                     w, n, None)
 
     assert bwd() in DEV and bwd(X=n0, ldx=0, c=A, cs=A) in DEV and bwd(X=n0, dd=n0) in DEV and bwd(V=n0, du=n0) in DEV
     assert bwd(dX=n0, dd=n0, du=n0) in DEV
+    assert bwd(base=B) in DEV and bwd(base=B, ldb=520) == 1 and bwd(dX=A) == 1 and bwd(dY=B, dX=B) == 1
     assert bwd(c=A, cs=A) == 1  # both X and its checkpoint
     assert bwd(X=n0, c=A) == 1 and bwd(X=n0, cs=A) == 1 and bwd(X=n0) == 1 and bwd(V=n0) == 1 and bwd(sc=n0) == 1
     assert bwd(X=n0, c=A, cs=A, K=520, ldb=520, lddx=520) == 2  # a checkpoint has whole slices
@@ -109,11 +111,11 @@ def test_refusals_by_code():
     assert lib.cr_ckpt_load(A, A, 4, 512, A, 512, None) in DEV and lib.cr_ckpt_load(A, None, 4, 512, A, 512, None) == 1
     assert lib.cr_ckpt_load(A, A, 4, 128, A, 512, None) == 2 and lib.cr_ckpt_load(A, A, 4, 512, A, 516, None) == 3
 
-    def gi(dY=A, lddy=264, Wq=A, s=A, dX=A, lddx=512, M=40, N=264, K=512, group=256, w=ws, n=wsn):
+    def gi(dY=A, lddy=264, Wq=A, s=A, dX=B, lddx=512, M=40, N=264, K=512, group=256, w=ws, n=wsn):
         return lib.cr_w4a4_grad_input(dY, lddy, Wq, s, dX, lddx, M, N, K, group, w, n, None)
 
     assert gi() in DEV and gi(M=0, dY=n0, dX=n0) in DEV and gi(N=0, dY=n0, Wq=n0, s=n0) in DEV
-    assert gi(dY=n0) == 1 and gi(Wq=n0) == 1 and gi(s=n0) == 1 and gi(dX=n0) == 1 and gi(lddx=504) == 1
+    assert gi(dX=A) == 1 and gi(dY=n0) == 1 and gi(Wq=n0) == 1 and gi(s=n0) == 1 and gi(dX=n0) == 1 and gi(lddx=504) == 1
     assert gi(group=32) == 2 and gi(group=1024) == 2 and gi(N=260) == 2 and gi(K=384) == 2
     assert gi(lddy=268) == 3 and gi(dX=odd) == 3
     need = lib.cr_w4a4_grad_input_workspace_size(40, 264, 512, 256)

@@ -469,3 +469,116 @@ def test_refusals():
     with pytest.raises(m.ConvRotError):
         m.cr_w4a4_grad_input(d["base"], torch.zeros(264, 256, dtype=torch.uint8, device="cuda"),
                              torch.ones(264, device="cuda"), group=32)
+
+
+# ---------------------------------------------------------------------------------------------- many times, large, side by side
+
+@pytest.mark.parametrize("M,K,N,r,L,mix,kept", [(8192, 2048, 512, 32, 1, "all", "int8"), (1500, 512, 1024, 128, 1, "all", "bf16"),
+                                                (1500, 512, 1024, 128, 3, "runs", "bf16"), (3000, 256, 256, 80, 2, "rows", "int8"),
+                                                (700, 1024, 256, 12, 6, "rows", "bf16")])
+def test_the_same_bits_a_hundred_times(M, K, N, r, L, mix, kept):
+    """Waits that are answered too early show as rare differences."""
+    d = make(M, K, N, r, L, mix, seed=51)
+    Wq, s_w = cr().cr_pack_weight(randn(gen(52), N, K, std=0.02))
+
+    def once():
+        Y, V = cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=d["base"], save_v=True)
+        keep = cr().cr_ckpt_save(d["X"])
+        g = cr().cr_lora_backward(d["dY"], keep if kept == "int8" else d["X"], V, d["down"], d["up"], d["scale"],
+                                  adapter=d["adapter"], base=d["dbase"])
+        return (Y, V, *keep, *g, cr().cr_w4a4_grad_input(d["dY"], Wq, s_w), cr().cr_w4a4_grad_input(d["dY"][:200], Wq, s_w))
+
+    want = once()
+    wrong = torch.zeros(len(want), device="cuda")
+    for _ in range(100):
+        wrong += torch.stack([(a.view(torch.uint8) != b.view(torch.uint8)).any() for a, b in zip(once(), want)])
+    assert not wrong.any(), wrong.tolist()
+
+
+def test_two_streams_at_once():
+    sets = [make(900, 512, 768, 16, 3, "runs", seed=61), make(50, 1024, 512, 64, 4, "rows", seed=62)]
+    want = [cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=d["base"]) for d in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, d in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=d["base"]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_adapters_past_32_bit_offsets():
+    """270000 x 8192 values: only the last rows name an adapter, and all others pass through."""
+    M, K, N, r = 270000, 8192, 64, 8
+    g = gen(71)
+    X = torch.zeros(M, K, dtype=BF, device="cuda")
+    X[-3:] = randn(g, 3, K)
+    a = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    a[-3:] = torch.tensor([1, 0, 1], dtype=torch.int32)
+    down, up = randn(g, 2, r, K, std=K ** -0.5), randn(g, 2, r, N)
+    scale = torch.tensor([0.5, 2.0], device="cuda")
+    Y, V = cr().cr_lora_forward(X, down, up, scale, adapter=a, save_v=True)
+    Y3, V3 = cr().cr_lora_forward(X[-3:], down, up, scale, adapter=a[-3:], save_v=True)
+    want, v, ey, ev = ao.lora_forward(f64(X[-3:]), f64(down), f64(up), f64(scale), ids(a[-3:]))
+    for got, w, e in ((Y[-3:], want, ey), (Y3, want, ey), (V[-3:], v, ev), (V3, v, ev)):
+        within(got, w, e, "last rows")
+    assert not Y[:-3].any() and not V[:-3].any()
+    # and the other way round: wide outputs, gradients of the wide side
+    dY = torch.zeros(M, N, dtype=BF, device="cuda")
+    dY[-3:] = randn(g, 3, N)
+    dX, dd, du = cr().cr_lora_backward(dY, X, V, down, up, scale, adapter=a)
+    (wx, wd, wu), (ex, ed, eu) = ao.lora_backward(f64(dY[-3:]), f64(X[-3:]), f64(V[-3:]), f64(down), f64(up), f64(scale), ids(a[-3:]))
+    within(dX[-3:], wx, ex, "dX")
+    within(dd, wd, ed, "d_down")
+    within(du, wu, eu, "d_up")
+    assert not dX[:-3].any()
+    del dX
+    kept = cr().cr_ckpt_save(X)
+    x, mags = ao.ckpt_values(kept[0][-3:].cpu().numpy(), kept[1][-3:].cpu().numpy())
+    (_, wd, _), (_, ed, _) = ao.lora_backward(f64(dY[-3:]), x, f64(V[-3:]), f64(down), f64(up), f64(scale), ids(a[-3:]), None, mags)
+    within(cr().cr_lora_backward(dY, kept, V, down, up, scale, adapter=a, need_dx=False, need_up=False)[1], wd, ed, "d_down from codes")
+
+
+def test_grad_input_past_32_bit_offsets():
+    M, K, N = 140000, 256, 16384
+    g = gen(72)
+    dY = torch.zeros(M, N, dtype=BF, device="cuda")
+    dY[-2:] = randn(g, 2, N)
+    Wq, s = cr().cr_pack_weight(randn(g, N, K, std=0.02), scale_mode="row")
+    want, bound = ao.grad_input(f64(dY[-2:]), Wq.cpu().numpy(), s.cpu().numpy())
+    got = cr().cr_w4a4_grad_input(dY, Wq, s)
+    within(got[-2:], want, bound, "dX")
+    assert not got[:-2].any()
+
+
+def test_views_at_odd_places():
+    """Row indices, scales and V that start anywhere their elements may."""
+    d = make(260, 512, 264, 4, 3, "rows", seed=81)
+    a = torch.zeros(261, dtype=torch.int32, device="cuda")
+    a[1:] = d["adapter"]
+    sc = torch.zeros(4, device="cuda")
+    sc[1:] = d["scale"]
+    args = (d["X"], d["down"], d["up"])
+    Y, V = cr().cr_lora_forward(*args, d["scale"], adapter=d["adapter"], base=d["base"], save_v=True)
+    Y2, V2 = cr().cr_lora_forward(*args, sc[1:], adapter=a[1:], base=d["base"], save_v=True)
+    assert torch.equal(Y, Y2) and torch.equal(V, V2)
+    rows = slice(1, 260)  # every operand one row further: V's rows are 8 bytes long
+    g = cr().cr_lora_backward(d["dY"][rows], d["X"][rows], V[rows], d["down"], d["up"], sc[1:], adapter=a[1:][rows])
+    want, bound = ao.lora_backward(f64(d["dY"][rows]), f64(d["X"][rows]), f64(V[rows]), f64(d["down"]), f64(d["up"]),
+                                   f64(d["scale"]), ids(d["adapter"][rows]))
+    for x, w, b, name in zip(g, want, bound, ("dX", "d_down", "d_up")):
+        within(x, w, b, name)
+
+
+def test_output_on_another_operand_is_refused():
+    d = make(40, 256, 256, 8, 2, "rows", seed=91)
+    with pytest.raises(cr().ConvRotError):
+        cr().cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], out=d["X"])
+    with pytest.raises(cr().ConvRotError):
+        cr().cr_lora_backward(d["dY"], d["X"], None, d["down"], d["up"], d["scale"], out=d["X"], need_up=False)
+    Wq, s = cr().cr_pack_weight(randn(gen(92), 256, 256))
+    with pytest.raises(cr().ConvRotError):
+        cr().cr_w4a4_grad_input(d["dY"], Wq, s, out=d["dY"])

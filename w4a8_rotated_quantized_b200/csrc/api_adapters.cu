@@ -51,6 +51,12 @@ size_t backward_bytes(int M, int N, int K, int rank, int L, bool codes) {
   return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + bytes_f32(g.down * per * K) + bytes_f32(g.up * per * N);
 }
 
+// An output may start at the very rows of the base that is added to it, and at no other operand's.
+bool in_place_ok(const void* out, int64_t ldo, const void* base, int64_t ldb, int M, const void* a, const void* b) {
+  if (out && (out == a || out == b)) return false;
+  return !out || out != base || ldo == ldb || M <= 1;
+}
+
 cr_status check_rows(const void* p, int64_t ld, int cols) {
   if (ld < cols) return CR_ERR_INVALID_ARG;
   return (!aligned(p, 16) || ld % 8 != 0) ? CR_ERR_MISALIGNED : CR_OK;
@@ -73,6 +79,7 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if (M < 0 || N < 0 || K < 0 || rank < 0 || num_adapters < 0 || ldx < 0 || ldb < 0 || ldy < 0)
     return CR_ERR_INVALID_ARG;
   if (M > 0 && (!X || !down || !up || !scale || !Y)) return CR_ERR_INVALID_ARG;
+  if (M > 0 && !in_place_ok(Y, ldy, base, ldb, M, X, V)) return CR_ERR_INVALID_ARG;
   if (!sizes_ok(M, N, K, rank, num_adapters)) return CR_ERR_UNSUPPORTED_SHAPE;
   cr_status st = check_rows(X, ldx, K);
   if (st == CR_OK) st = check_rows(Y, ldy, N);
@@ -122,6 +129,7 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   if (M > 0 && (!dY || !down || !up)) return CR_ERR_INVALID_ARG;
   if (!scale || (X && codes) || ((codes != nullptr) != (code_scales != nullptr))) return CR_ERR_INVALID_ARG;
   if (M > 0 && ((d_down && !X && !codes) || (d_up && !V))) return CR_ERR_INVALID_ARG;
+  if (M > 0 && !in_place_ok(dX, lddx, dX_base, ldb, M, dY, X)) return CR_ERR_INVALID_ARG;
   if (!sizes_ok(M, N, K, rank, num_adapters) || (codes && K % 256 != 0)) return CR_ERR_UNSUPPORTED_SHAPE;
   cr_status st = check_rows(dY, lddy, N);
   if (st == CR_OK && X) st = check_rows(X, ldx, K);
@@ -217,7 +225,7 @@ size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group) {
 cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const float* w_scale, void* dX, int64_t lddx,
                              int M, int N, int K, int group, void* workspace, size_t workspace_bytes, void* stream) {
   if (M < 0 || N < 0 || K < 0 || lddy < 0 || lddx < 0) return CR_ERR_INVALID_ARG;
-  if (M > 0 && (!dX || (N > 0 && (!dY || !Wq || !w_scale)))) return CR_ERR_INVALID_ARG;
+  if (M > 0 && (!dX || (N > 0 && (!dY || !Wq || !w_scale || dX == dY)))) return CR_ERR_INVALID_ARG;
   if ((group != CR_GROUP_16 && group != CR_GROUP_64 && group != CR_GROUP_256 && group != CR_GROUP_1024) || K < 256 ||
       K % 256 != 0 || K % group != 0 || K > CR_MAX_K || N % 8 != 0 || N > CR_MAX_K)
     return CR_ERR_UNSUPPORTED_SHAPE;
