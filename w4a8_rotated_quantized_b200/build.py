@@ -27,7 +27,8 @@ SOURCES = ["api.cu", "act_kernels.cu", "gemm_w4a4.cu", "gemm_w4a4_pair.cu", "gem
            "selftest.cu", "api_adapters.cu", "lora_rows.cu", "lora_mma.cu", "grad_values.cu", "ckpt_mma.cu", "gemm_bf16.cu",
            "grad_input_few.cu"]
 HEADERS = [os.path.join(ROOT, "include", "convrot.h")] + [
-    os.path.join(CSRC, f) for f in ("cr_device.cuh", "cr_internal.h", "act_device.cuh", "grid_sync.cuh", "lora_device.cuh")
+    os.path.join(CSRC, f) for f in ("cr_device.cuh", "cr_internal.h", "act_device.cuh", "grid_sync.cuh", "lora_device.cuh",
+                                    "unit_device.cuh")
 ]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=default",

@@ -48,7 +48,9 @@ GradSplits grad_splits(int M, int N, int K, int rank, int L, bool codes) {
 size_t backward_bytes(int M, int N, int K, int rank, int L, bool codes) {
   const GradSplits g = grad_splits(M, N, K, rank, L, codes);
   const int64_t per = static_cast<int64_t>(L) * rank;
-  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + bytes_f32(g.down * per * K) + bytes_f32(g.up * per * N);
+  // (a gradient that is not split is written as it is)
+  return kWsHead + bytes_f32(static_cast<int64_t>(M) * rank) + (g.down > 1 ? bytes_f32(g.down * per * K) : 0) +
+         (g.up > 1 ? bytes_f32(g.up * per * N) : 0);
 }
 
 // An output may start at the very rows of the base that is added to it, and at no other operand's.
@@ -157,7 +159,7 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   float* dv = reinterpret_cast<float*>(w);
   const GradSplits parts = grad_splits(M, N, K, rank, L, codes != nullptr);
   float* gd = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank));
-  float* gu = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(gd) + bytes_f32(parts.down * nd));
+  float* gu = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(gd) + (parts.down > 1 ? bytes_f32(parts.down * nd) : 0));
   int* status = ws_status(workspace);
   if (dX || d_down) {
     st = static_cast<cr_status>(cr::launch_lora_v_mma(static_cast<const uint16_t*>(dY), lddy, adapter,
@@ -176,10 +178,14 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   if (d_down || d_up) {
     st = static_cast<cr_status>(cr::launch_lora_grad_mma(
         codes ? codes : X, ldx, code_scales, dY, lddy, dv, static_cast<const uint16_t*>(V), adapter, scale,
-        d_down ? gd : nullptr, d_up ? gu : nullptr, M, K, N, rank, L, parts.down, parts.up, status, s));
+        gd, gu, static_cast<uint16_t*>(d_down), static_cast<uint16_t*>(d_up), M, K, N, rank, L, parts.down, parts.up,
+        status, s));
     if (st != CR_OK) return st;
-    if (cr::launch_lora_grad_finish(gd, gu, parts.down, parts.up, static_cast<int64_t>(L) * rank, K, N, static_cast<uint16_t*>(d_down),
-                                    static_cast<uint16_t*>(d_up), codes != nullptr, s) != cudaSuccess)
+    uint16_t* split_down = parts.down > 1 ? static_cast<uint16_t*>(d_down) : nullptr;
+    uint16_t* split_up = parts.up > 1 ? static_cast<uint16_t*>(d_up) : nullptr;
+    if ((split_down || split_up) &&
+        cr::launch_lora_grad_finish(gd, gu, parts.down, parts.up, static_cast<int64_t>(L) * rank, K, N, split_down,
+                                    split_up, codes != nullptr, s) != cudaSuccess)
       return CR_ERR_CUDA;
   }
   return CR_OK;

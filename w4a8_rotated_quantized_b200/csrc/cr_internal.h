@@ -172,14 +172,15 @@ int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, co
 int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up, const float* scale,
                       const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, int M, int N, int rank, int L,
                       int* status, int num_sms, cudaStream_t stream);
-// Both gradients' products in one launch: partial sums Gdown float32 [splits_down, L, rank, K] of scale[a] * sum
-// over the adapter's rows of dV^T X (X bf16 rows, or codes with code_scale: then in the checkpoint's rotated
-// basis) and Gup [splits_up, L, rank, N] of V^T dY; either may be null.  dV float32, V bf16, [M, rank].
+// Both gradients' products in one launch: d_down [L, rank, K] = scale[a] * sum over the adapter's rows of dV^T X
+// (X bf16 rows, or codes with code_scale) and d_up [L, rank, N] of V^T dY, bf16; either may be null.  dV float32,
+// V bf16, [M, rank].  One that is split over more CTAs is left as partial sums instead, Gdown float32 [splits_down,
+// L, rank, K] (of codes: in the checkpoint's rotated basis) or Gup [splits_up, L, rank, N], for the finish kernel.
 void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_sms, int* down, int* up);
 int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, const void* dY, int64_t lddy,
                          const float* dV, const uint16_t* V, const int32_t* adapter, const float* scale, float* Gdown,
-                         float* Gup, int M, int K, int N, int rank, int L, int splits_down, int splits_up, int* status,
-                         cudaStream_t stream);
+                         float* Gup, uint16_t* d_down, uint16_t* d_up, int M, int K, int N, int rank, int L,
+                         int splits_down, int splits_up, int* status, cudaStream_t stream);
 // The partial sums added in order and rounded: d_down [rows, K] (rotated by H256 if `rotate`) and d_up
 // [rows, N], rows = L * rank; either may be null.
 cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts_down, int parts_up, int64_t rows, int K, int N,

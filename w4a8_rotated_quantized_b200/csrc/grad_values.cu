@@ -23,6 +23,7 @@ namespace cr {
 namespace {
 
 #include "act_device.cuh"
+#include "unit_device.cuh"
 
 constexpr int kWarps = 4;
 
@@ -56,24 +57,6 @@ __device__ __forceinline__ void put8(Pairs& P, int k, const float2 (&v)[4]) {
       a.y = v[e].x;
       b.y = v[e].y;
     }
-  }
-}
-
-// Pairs of the lane's 64 values of a slice to bf16, times `f`: piece p = k ^ k0 at elements 32p + 8l.
-__device__ __forceinline__ void store_unit_bf16(const Pairs& P, int k0, float f, uint16_t* __restrict__ unit) {
-  const int l = threadIdx.x & 3;
-  const float2 f2 = make_float2(f, f);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float lo[8], hi[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 t = __fmul2_rn(P.w[8 * k + e], f2);
-      lo[e] = t.x;
-      hi[e] = t.y;
-    }
-    *reinterpret_cast<uint4*>(unit + 32 * (k ^ k0) + 8 * l) = narrow8(lo);
-    *reinterpret_cast<uint4*>(unit + 32 * ((k + 4) ^ k0) + 8 * l) = narrow8(hi);
   }
 }
 
@@ -143,14 +126,7 @@ __global__ void __launch_bounds__(32)
     }
     Pairs P;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float e[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float2& pair = P.w[8 * ((k >> 1) & 3) + 4 * (k & 1) + c];
-        if (k < 8) pair.x = e[c]; else pair.y = e[c];
-      }
-    }
+    for (int k = 0; k < 16; ++k) put4(P, k, v[k]);
     fwht256_mapped<4>(P);
     if (in) store_unit_bf16(P, k0, 0.0625f, d_down + u * 256);
     return;

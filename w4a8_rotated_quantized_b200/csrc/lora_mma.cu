@@ -36,6 +36,9 @@
 namespace cr {
 namespace {
 
+#include "act_device.cuh"
+#include "unit_device.cuh"
+
 constexpr int TM = 128;             // tokens of a v or y tile
 constexpr int KB = 64;              // bf16 values of a 128-byte swizzle row
 constexpr int kSmemMax = 232448 - 1024;  // the base is aligned up to 1024
@@ -607,6 +610,7 @@ constexpr int kMaxGradTiles = 512;  // token tiles of one CTA (64-bit row masks 
 struct GPlan {
   int rp, vcols, stage, stages, off_raw, off_mask, off_bar, smem, cols;
 };
+constexpr int kSumsLd = GC + 4;  // floats between the ranks' sums: eight ranks' fours, 32 columns apart, side by side
 constexpr int kRaws = 4;  // tiles of codes on their way; even, so that each set meets its slots round by round
 inline __host__ __device__ GPlan g_plan(int rank, bool codes, bool v16) {
   GPlan p;
@@ -649,8 +653,9 @@ __device__ __forceinline__ uint2 bytes_to_bf16(uint32_t w) {
 template <bool kCodes, bool kV16, int kN>
 __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float* __restrict__ code_scale,
                                           const void* __restrict__ V, const int32_t* __restrict__ adapter,
-                                          const float* __restrict__ scale, float* __restrict__ G, int M, int C,
-                                          int rank, int L, int splits, int block, int* __restrict__ status) {
+                                          const float* __restrict__ scale, float* __restrict__ G,
+                                          uint16_t* __restrict__ grad, int M, int C, int rank,
+                                          int L, int splits, int block, int* __restrict__ status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align_smem(smem_raw);
   const GPlan p = g_plan(rank, kCodes, kV16);
@@ -892,9 +897,12 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 ranks
     const int c = c0 + 128 * half + 32 * q + lane;
     const float sc = __ldg(scale + a) * (kCodes ? 64.f : 1.f);  // codes come as 2^-6 of themselves
+    const bool whole = splits == 1;  // no other part: rounded here
     float* out = G + (static_cast<int64_t>(split) * L + a) * rank * C + c;
-    if (ok && first < nt) {
-      if (mbar_sleep_warp(acc_full, 0, abort)) {
+    uint16_t* rows16 = grad + static_cast<int64_t>(a) * rank * C + c0;
+    float* sums = reinterpret_cast<float*>(base);  // [rank, kSumsLd], where the operands were
+    if (first < nt) {
+      if (ok && mbar_sleep_warp(acc_full, 0, abort)) {
         tc_fence_after();
 #pragma unroll 1
         for (int j = 16 * part; j < p.rp; j += 32) {
@@ -903,18 +911,48 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
           tmem_ld16(src, r);
           if constexpr (!kV16) tmem_ld16(src + static_cast<uint32_t>(p.rp), l);
           tmem_ld_wait();
-          if (c < C) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float t = __uint_as_float(r[e]);
-              if constexpr (!kV16) t += __uint_as_float(l[e]);
-              if (j + e < rank) out[static_cast<int64_t>(j + e) * C] = sc * t;
+          for (int e = 0; e < 16; ++e) {
+            float t = __uint_as_float(r[e]);
+            if constexpr (!kV16) t += __uint_as_float(l[e]);
+            if (j + e < rank) {
+              if (whole) sums[(j + e) * kSumsLd + c - c0] = sc * t;
+              else if (c < C) out[static_cast<int64_t>(j + e) * C] = sc * t;
             }
           }
         }
       } else {
         ok = false;
       }
+      if (whole) {
+        named_bar_sync(1, 32 * kGWarps);
+        if constexpr (kCodes) {  // taken against codes: rotated back, a rank's 256 columns by four lanes
+          const int u = 8 * warp + (lane >> 2), k0 = lane >> 2, l = lane & 3;
+          Pairs P;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (u < rank)
+              f = *reinterpret_cast<const float4*>(sums + u * kSumsLd + 32 * ((k >> 1) ^ k0) + 8 * l + 4 * (k & 1));
+            put4(P, k, f);
+          }
+          fwht256_mapped<4>(P);
+          if (u < rank) store_unit_bf16(P, k0, 0.0625f, rows16 + static_cast<int64_t>(u) * C);
+        } else if (c0 + 8 * lane < C) {
+          for (int j = warp; j < rank; j += kGWarps) {
+            float v[8];
+            const float4 f0 = *reinterpret_cast<const float4*>(sums + j * kSumsLd + 8 * lane);
+            const float4 f1 = *reinterpret_cast<const float4*>(sums + j * kSumsLd + 8 * lane + 4);
+            v[0] = f0.x; v[1] = f0.y; v[2] = f0.z; v[3] = f0.w;
+            v[4] = f1.x; v[5] = f1.y; v[6] = f1.z; v[7] = f1.w;
+            *reinterpret_cast<uint4*>(rows16 + static_cast<int64_t>(j) * C + 8 * lane) = narrow8(v);
+          }
+        }
+      }
+    } else if (whole) {
+      if (c0 + 8 * lane < C)
+        for (int j = warp; j < rank; j += kGWarps)
+          *reinterpret_cast<uint4*>(rows16 + static_cast<int64_t>(j) * C + 8 * lane) = make_uint4(0, 0, 0, 0);
     } else if (c < C) {
       for (int j = part; j < rank; j += 2) out[static_cast<int64_t>(j) * C] = 0.f;
     }
@@ -935,15 +973,15 @@ __global__ void __launch_bounds__(kGThreads, 1)
     lora_grad_mma_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_dy,
                          const float* __restrict__ code_scale, const float* __restrict__ dV,
                          const uint16_t* __restrict__ V, const int32_t* __restrict__ adapter,
-                         const float* __restrict__ scale, float* __restrict__ Gdown, float* __restrict__ Gup, int M,
-                         int K, int N, int rank, int L, int splits_down, int splits_up, int down_blocks,
+                         const float* __restrict__ scale, float* __restrict__ Gdown, float* __restrict__ Gup,
+                         uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up, int M, int K, int N, int rank, int L, int splits_down, int splits_up, int down_blocks,
                          int* __restrict__ status) {
   if (static_cast<int>(blockIdx.x) < down_blocks)
-    grad_body<kCodes, false, kN>(tmap_x, code_scale, dV, adapter, scale, Gdown, M, K, rank, L, splits_down, blockIdx.x,
-                                status);
+    grad_body<kCodes, false, kN>(tmap_x, code_scale, dV, adapter, scale, Gdown, d_down, M, K, rank, L, splits_down,
+                                blockIdx.x, status);
   else
-    grad_body<false, true, kN>(tmap_dy, nullptr, V, adapter, scale, Gup, M, N, rank, L, splits_up, blockIdx.x - down_blocks,
-                           status);
+    grad_body<false, true, kN>(tmap_dy, nullptr, V, adapter, scale, Gup, d_up, M, N, rank, L, splits_up,
+                               blockIdx.x - down_blocks, status);
 }
 
 std::atomic<bool> g_attr_done[64];
@@ -1068,7 +1106,8 @@ void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_
     const int64_t most = td > tu ? td : tu, ctas = cd * sd + cu * su;
     // one round: the longest CTA; more: the work spread over the SMs and half of a CTA left over
     const int64_t time = ctas <= num_sms ? most : (cd * sd * td + cu * su * tu) / num_sms + most / 2;
-    const int64_t cost = time + (sd * K + su * N) * static_cast<int64_t>(L) * rank / 50000;
+    const int64_t parts = sd > 1 || su > 1 ? 40 + (sd * K + su * N) * static_cast<int64_t>(L) * rank / 50000 : 0;
+    const int64_t cost = time + parts;
     if (cost < best) {
       best = cost;
       *down = sd;
@@ -1079,19 +1118,19 @@ void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_
 
 int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, const void* dY, int64_t lddy,
                          const float* dV, const uint16_t* V, const int32_t* adapter, const float* scale, float* Gdown,
-                         float* Gup, int M, int K, int N, int rank, int L, int splits_down, int splits_up, int* status,
-                         cudaStream_t stream) {
+                         float* Gup, uint16_t* d_down, uint16_t* d_up, int M, int K, int N, int rank, int L,
+                         int splits_down, int splits_up, int* status, cudaStream_t stream) {
   if (!set_attrs()) return CR_ERR_CUDA;
   const bool codes = code_scale != nullptr;
   CUtensorMap tx, ty;
   memset(&tx, 0, sizeof(tx));
   memset(&ty, 0, sizeof(ty));
-  if (Gdown && !(codes ? make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, X, M, K, K, GC, GM, CU_TENSOR_MAP_SWIZZLE_NONE, kL2)
+  if (d_down && !(codes ? make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, X, M, K, K, GC, GM, CU_TENSOR_MAP_SWIZZLE_NONE, kL2)
                        : make_tmap_2d(&tx, kBf, X, M, K, static_cast<uint64_t>(ldx) * 2, 64, GM, kSw128, kL2)))
     return CR_ERR_CUDA;
-  if (Gup && !make_tmap_2d(&ty, kBf, dY, M, N, static_cast<uint64_t>(lddy) * 2, 64, GM, kSw128, kL2)) return CR_ERR_CUDA;
-  const int64_t down = Gdown ? static_cast<int64_t>((K + GC - 1) / GC) * L * splits_down : 0;
-  const int64_t up = Gup ? static_cast<int64_t>((N + GC - 1) / GC) * L * splits_up : 0;
+  if (d_up && !make_tmap_2d(&ty, kBf, dY, M, N, static_cast<uint64_t>(lddy) * 2, 64, GM, kSw128, kL2)) return CR_ERR_CUDA;
+  const int64_t down = d_down ? static_cast<int64_t>((K + GC - 1) / GC) * L * splits_down : 0;
+  const int64_t up = d_up ? static_cast<int64_t>((N + GC - 1) / GC) * L * splits_up : 0;
   if (down + up > INT32_MAX) return CR_ERR_UNSUPPORTED_SHAPE;
   const int s0 = g_plan(rank, codes, false).smem, s1 = g_plan(rank, false, true).smem;
   const int smem = (s0 > s1 ? s0 : s1) + 1024;
@@ -1111,8 +1150,8 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tx, ty, code_scale, dV, V, adapter, scale, Gdown, Gup, M, K, N, rank, L,
-                            splits_down, splits_up, static_cast<int>(down), status) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, kern, tx, ty, code_scale, dV, V, adapter, scale, Gdown, Gup, d_down, d_up, M, K, N,
+                            rank, L, splits_down, splits_up, static_cast<int>(down), status) == cudaSuccess
              ? CR_OK
              : CR_ERR_CUDA;
 }

@@ -180,17 +180,20 @@ std::atomic<bool> g_attr_done[64];
 
 }  // namespace
 
-// By microseconds as measured at ranks 16 to 128 and 3072 to 9728 columns: the row form costs 5 and its rows'
-// factors at 6 TB/s (each row reads its own: L2).  The batch form costs 11 and its first adapter's factors at
-// 0.3 TB/s, and about a tenth more for every further adapter that occurs among a tile's rows; the pool's size
-// only bounds those, so half of them are counted.
-//   64 rows, rank 16, 2560 -> 9728:   one adapter 9 against 12, each row its own of 48: 9 against 48
-//   64 rows, rank 128, 12288 -> 3072: one adapter 47 against 24
+// By microseconds, fitted to both forms' times for 260 calls of 1 to 1400 rows, 256 to 10240 columns, ranks 4 to
+// 128 and pools of 1 to 48 adapters: the choice costs 0.4 % over the better form on average and 27 % at worst.
+// The row form costs 4.6, a row's CTAs a fortieth, and each row's own factors come at 8.6 TB/s (L2).  The batch
+// form costs 8.3, its first adapter's factors at 0.4 TB/s, the rows' values, and for every further adapter that
+// may occur among a tile's rows 0.44 and its factors at 1.4 TB/s.
+//   693 rows, rank 8, 1672 -> 616, one adapter:     rows 31, batch 9
+//   130 rows, rank 4, 328 -> 4200, 24 adapters:     rows 6, batch 26
+//   154 rows, rank 32, 1712 -> 6464, 11 adapters:   rows 14, batch 17 (the worst choice)
 bool use_lora_rows(int M, int N, int K, int rank, int L) {
   if (M > 1024) return false;
-  const double factors = 2.0 * rank * (static_cast<double>(K) + N);
+  const double columns = static_cast<double>(K) + N, factors = 2.0 * rank * columns;
   const int most = L < M ? (L < 128 ? L : 128) : (M < 128 ? M : 128);
-  const double rows = 5 + M * factors / 6e6, batch = (11 + factors / 3e5) * (1 + 0.06 * (most - 1));
+  const double rows = 4.6 + M / 40.0 + M * factors / 8.6e6;
+  const double batch = 8.3 + factors / 4e5 + M * columns / 1.7e6 + (most - 1) * (0.44 + factors / 1.4e6);
   return rows < batch;
 }
 
