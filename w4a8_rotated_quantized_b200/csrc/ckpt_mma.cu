@@ -28,6 +28,7 @@
 
 #include "cr_device.cuh"
 #include "cr_internal.h"
+#include "grid_sync.cuh"
 #include "lora_device.cuh"
 
 namespace cr {
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp == 1 && lane == 0) {
     init_bars(bars, abort, kSaveStages);
+    griddep_wait();  // for what the stream ran before
     for (int i = 0; i < 4; ++i) load(blockIdx.x, i, i);  // (there is no block without a tile)
   }
   // [H64, H64], [-H64, H64], [H64, -H64]: 128 rows of 64 values, 16-byte pieces in the 128-byte swizzle's places
@@ -154,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *reinterpret_cast<uint4*>(base + v * kBox + n * 128 + ((piece ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   const uint32_t tmem = start(misc);
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -295,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp == 1 && lane == 0) {
     init_bars(bars, abort, kLoadStages);
+    griddep_wait();  // for what the stream ran before
     for (int i = 0; i < 2; ++i) load(blockIdx.x, i, i);  // (there is no block without a tile)
   }
   // H256 as bytes: for each 128 of the sum, 256 rows of 128 bytes
@@ -308,6 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *reinterpret_cast<uint4*>(base + kb * 2 * kBox + n * 128 + ((piece ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   const uint32_t tmem = start(misc);
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -363,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
       const int64_t m0 = t / slices * TM;
       const int slice = static_cast<int>(t % slices);
-      float s = m0 + row < M ? __ldg(scales + (m0 + row) * slices + slice) * 0.0625f : 0.f;
+      float s = m0 + row < M ? __ldcg(scales + (m0 + row) * slices + slice) * 0.0625f : 0.f;
       if (ok) ok = mbar_sleep_warp(bars.acc_full(b), ph, abort);
       if (!ok) s = __uint_as_float(0x7FC00000u);
       tc_fence_after();
@@ -428,6 +435,22 @@ unsigned blocks(int M, int K, int num_sms) {
   return static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
 }
 
+// A launch as a programmatic dependent of what the stream ran before: the block sets itself up beside its end.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  Launch(unsigned grid, int smem, cudaStream_t stream) {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem + 1024;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+};
+
 bool codes_map(CUtensorMap* map, const void* codes, int M, int K) {
   return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, M, K, K, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
@@ -443,16 +466,16 @@ int launch_ckpt_save(const uint16_t* X, int M, int K, int64_t ldx, int8_t* codes
                      cudaStream_t stream) {
   CUtensorMap tx, tc;
   if (!set_attrs() || !values_map(&tx, X, M, K, ldx) || !codes_map(&tc, codes, M, K)) return CR_ERR_CUDA;
-  ckpt_save_kernel<<<blocks(M, K, num_sms), kThreads, kSaveSmem + 1024, stream>>>(tx, tc, scales, M, K / TC);
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  Launch l(blocks(M, K, num_sms), kSaveSmem, stream);
+  return cudaLaunchKernelEx(&l.cfg, ckpt_save_kernel, tx, tc, scales, M, K / TC) == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 int launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uint16_t* X, int64_t ldx, int num_sms,
                      cudaStream_t stream) {
   CUtensorMap tx, tc;
   if (!set_attrs() || !values_map(&tx, X, M, K, ldx) || !codes_map(&tc, codes, M, K)) return CR_ERR_CUDA;
-  ckpt_load_kernel<<<blocks(M, K, num_sms), kThreads, kLoadSmem + 1024, stream>>>(tc, tx, scales, M, K / TC);
-  return cudaGetLastError() == cudaSuccess ? CR_OK : CR_ERR_CUDA;
+  Launch l(blocks(M, K, num_sms), kLoadSmem, stream);
+  return cudaLaunchKernelEx(&l.cfg, ckpt_load_kernel, tc, tx, scales, M, K / TC) == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
 
 }  // namespace cr

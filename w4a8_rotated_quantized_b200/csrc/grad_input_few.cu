@@ -91,13 +91,14 @@ __device__ __forceinline__ void give_up(volatile int* abort, int* status) {
 __global__ void __launch_bounds__(256)
     grad_input_operand_kernel(const uint16_t* __restrict__ dY, int64_t lddy, const float* __restrict__ w_scale,
                               uint16_t* __restrict__ V, int M, int N, int rp, int* __restrict__ status) {
+  griddep_wait();  // for what the stream ran before
   griddep_launch_dependents();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = CR_OK;
   const int n = (blockIdx.x * 256 + threadIdx.x) * 8, m = blockIdx.y;
   if (n >= N) return;
   float v[8] = {};
   if (m < M) {
-    widen8(ldg16(dY + m * lddy + n), v);
+    widen8(ldcg16(dY + m * lddy + n), v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= __ldg(w_scale + n + e);
   }
@@ -146,7 +147,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == kWarps + 1 && lane == 0) {
     prefetch_tmap(&tmap_w);
     prefetch_tmap(&tmap_v);
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarps) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
+    if (lane == 0) griddep_launch_dependents();
   }
   tc_fence_before();
   __syncthreads();
@@ -403,11 +404,17 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return CR_ERR_CUDA;
   const dim3 ogrid((N / 8 + 255) / 256, p.blocks * p.rp);
-  grad_input_operand_kernel<<<ogrid, 256, 0, stream>>>(dY, lddy, w_scale, V, M, N, p.rp, status);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = ogrid;
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, grad_input_operand_kernel, dY, lddy, w_scale, V, M, N, p.rp, status) != cudaSuccess)
+    return CR_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(K / GC * p.blocks * splits), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = p.smem + 1024;

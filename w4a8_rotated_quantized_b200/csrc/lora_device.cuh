@@ -13,7 +13,8 @@ __device__ __forceinline__ float bf16_float(uint16_t b) { return __uint_as_float
 
 __device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-__device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// Past L1: of what a kernel may have written that this one started beside.
+__device__ __forceinline__ uint4 ldcg16(const uint16_t* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
 
 __device__ __forceinline__ void widen8(uint4 q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -35,32 +36,25 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
 }
 
 // Loads that stay where they are written: the compiler sinks plain read-only loads to their first use, which
-// undoes a prefetch into registers.
-// (past L1: of what a kernel wrote that this one started beside)
+// undoes a prefetch into registers.  Past L1, as above.
 __device__ __forceinline__ float4 ldcg_here_f4(const float* p) {
   float4 v;
   asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ldg_here_u2(const void* p) {
+__device__ __forceinline__ uint2 ldcg_here_u2(const void* p) {
   uint2 v;
-  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint4 ldg_here_u4(const void* p) {
+__device__ __forceinline__ uint4 ldcg_here_u4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-// (of memory that the kernel may write to)
-__device__ __forceinline__ uint4 ld_here_u4(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ float ldg_here_f1(const float* p) {
+__device__ __forceinline__ float ldcg_here_f1(const float* p) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
 

@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(kVThreads, 1)
   int* counts = reinterpret_cast<int*>(base + p.off_bar + 160);
 
   cluster_arrive();  // this CTA has started: its shared memory may be written to
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = CR_OK;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(full(s), 1);
@@ -168,7 +167,6 @@ __global__ void __launch_bounds__(kVThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) griddep_launch_dependents();  // the y kernel may set itself up beside this one
   if (warp == 1 && lane == 0) {
     prefetch_tmap(&tmap_x);
     prefetch_tmap(&tmap_a);
@@ -176,6 +174,11 @@ __global__ void __launch_bounds__(kVThreads, 1)
   if (warp == 0) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
+  }
+  griddep_wait();  // for what the stream ran before
+  if (threadIdx.x == 0) {
+    griddep_launch_dependents();  // the y kernel may set itself up beside this one
+    if (blockIdx.x == 0) *status = CR_OK;
   }
   const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts, kVThreads);
   tc_fence_before();
@@ -390,7 +393,6 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) griddep_launch_dependents();  // what follows may set itself up beside this kernel
   if (warp == 1 && lane == 0) {
     prefetch_tmap(&tmap_u);
     if (has_base) prefetch_tmap(&tmap_base);
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   if (warp == 0) {
     tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
+    if (lane == 0) griddep_launch_dependents();  // what follows may set itself up beside this kernel
   }
   tc_fence_before();
   __syncthreads();
@@ -688,11 +691,11 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     *abort = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) griddep_launch_dependents();
   if (warp == kGWarps + 1 && lane == 0) prefetch_tmap(&tmap_z);
   if (warp == kGWarps) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
+    if (lane == 0) griddep_launch_dependents();
   }
   // the rows of this CTA's token tiles that name its adapter
   for (int t = warp; t < nt; t += kGThreads / 32) {
@@ -806,12 +809,12 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         const int r = at[k] >> 16;
         if (from[k] >= 0 && (plain ? r < rows : (mask32[2 * i + (r >> 5)] >> (r & 31) & 1) != 0)) {
           if constexpr (kV16) {
-            const uint2 w = ldg_here_u2(v + from[k] * 2);
+            const uint2 w = ldcg_here_u2(v + from[k] * 2);
             x.v[k].x = __uint_as_float(w.x);
             x.v[k].y = __uint_as_float(w.y);
           } else {
             x.v[k] = ldcg_here_f4(reinterpret_cast<const float*>(v) + from[k]);
-            if constexpr (kCodes) x.cs[k] = ldg_here_f1(cs + r * (C >> 8));
+            if constexpr (kCodes) x.cs[k] = ldcg_here_f1(cs + r * (C >> 8));
           }
         }
       }
@@ -1027,17 +1030,19 @@ int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, co
   int splits = 1;
   while (splits < kVMostSplits && tiles * splits * 2 <= num_sms && nkb >= 4 * splits) splits *= 2;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), 1, 1);
   cfg.blockDim = dim3(kVThreads, 1, 1);
   cfg.dynamicSmemBytes = p.smem + 1024;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, lora_v_mma_kernel, tx, ta, adapter, V, Vout, M, K, rank, L, splits, status) ==
                  cudaSuccess
              ? CR_OK

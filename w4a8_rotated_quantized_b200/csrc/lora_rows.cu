@@ -21,6 +21,7 @@
 
 #include "cr_device.cuh"
 #include "cr_internal.h"
+#include "grid_sync.cuh"
 #include "lora_device.cuh"
 
 namespace cr {
@@ -46,7 +47,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   // sums of the tasks [pass][rank]; later partial results [rank group][column piece][8]
   __shared__ __align__(16) float scratch[kMostPasses * kMaxRank];
   __shared__ float v[kMaxRank];
-  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = CR_OK;
+  griddep_wait();  // for what the stream ran before; past L1 from here on: that may have left older values there
+  if (threadIdx.x == 0) {
+    griddep_launch_dependents();
+    if (status && blockIdx.x == 0) *status = CR_OK;
+  }
   const int c = static_cast<int>(cluster_ctarank());
   const int64_t m = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -62,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (a < 0) {
     for (int p = tid; p < pieces; p += kThreads)
       *reinterpret_cast<uint4*>(Y + m * ldy + 8 * (p0 + p)) =
-          brow ? *reinterpret_cast<const uint4*>(brow + 8 * (p0 + p)) : make_uint4(0, 0, 0, 0);
+          brow ? ldcg16(brow + 8 * (p0 + p)) : make_uint4(0, 0, 0, 0);
     if (Vout && c == 0 && tid < rank) Vout[m * rank + tid] = 0;
     return;
   }
@@ -73,9 +78,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = 0; i < kAhead; ++i) {
     const int j = group + groups * i;
     ahead[i] = make_uint4(0, 0, 0, 0);
-    if (mine && j < rank) ahead[i] = ldg_here_u4(u + static_cast<int64_t>(j) * N + 8 * piece);
+    if (mine && j < rank) ahead[i] = ldcg_here_u4(u + static_cast<int64_t>(j) * N + 8 * piece);
   }
-  if (mine && group == 0 && brow) b = ld_here_u4(brow + 8 * (p0 + piece));
+  if (mine && group == 0 && brow) b = ldcg_here_u4(brow + 8 * (p0 + piece));
 
   // partial sums over this CTA's columns of X: task t is rank t % rank over 256 columns
   const int per_k = (K / 8 + ctas - 1) / ctas;
@@ -91,9 +96,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int q = q0 + 32 * pass + lane;
       const bool in = q < q_end && t < rank * passes;
       const uint16_t* src = w + static_cast<int64_t>(j) * K + 8 * q;
-      xq[i / 4] = in ? ldg16(x + 8 * q) : make_uint4(0, 0, 0, 0);
+      xq[i / 4] = in ? ldcg16(x + 8 * q) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) wq[i + e] = in ? ldg16(src + static_cast<int64_t>(e) * K) : make_uint4(0, 0, 0, 0);
+      for (int e = 0; e < 4; ++e) wq[i + e] = in ? ldcg16(src + static_cast<int64_t>(e) * K) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
@@ -140,12 +145,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     } else if (brow) {
-      b = *reinterpret_cast<const uint4*>(brow + 8 * (p0 + p));
+      b = ldcg16(brow + 8 * (p0 + p));
     }
 #pragma unroll 8
     for (int j = group + (first ? groups * kAhead : 0); j < rank; j += groups) {
       float uv[8];
-      widen8(ldg16(u + static_cast<int64_t>(j) * N + 8 * p), uv);
+      widen8(ldcg16(u + static_cast<int64_t>(j) * N + 8 * p), uv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = fmaf(v[j], uv[e], y[e]);
     }
@@ -208,7 +213,7 @@ int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, con
     g_attr_done[dev].store(true);
   }
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   // fewer CTAs a row where more rows share the machine; two only where their passes fit
   const int ctas = M <= 4 ? 16 : M <= 8 ? 8 : M <= 64 || K > CR_MAX_K / 2 ? 4 : 2;
@@ -219,7 +224,9 @@ int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, con
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, lora_rows_kernel, X, ldx, adapter, down, up, scale, base, ldb, Y, ldy, Vout, N, K,
                             rank, L, ctas, status) == cudaSuccess
              ? CR_OK
