@@ -582,3 +582,40 @@ def test_output_on_another_operand_is_refused():
     Wq, s = cr().cr_pack_weight(randn(gen(92), 256, 256))
     with pytest.raises(cr().ConvRotError):
         cr().cr_w4a4_grad_input(d["dY"], Wq, s, out=d["dY"])
+
+
+@pytest.mark.parametrize("M,L,mix", [(1, 1, "all"), (3, 4, "rows"), (60, 3, "runs"), (300, 2, "runs"), (700, 9, "rows")])
+def test_calls_on_each_others_results(M, L, mix):
+    """Calls whose kernels start beside the end of the call before, each reading or overwriting what that one
+    wrote or read, with nothing else between them: the same bits as with a synchronisation after every call."""
+    m = cr()
+    d = make(M, 512, 512, 16, L, mix, seed=71)
+    Wq, s_w = m.cr_pack_weight(randn(gen(72), 512, 512, std=0.04))
+    scale, a = d["scale"] * 0.1, d["adapter"]
+
+    def run(between):
+        A, B, seen = d["X"].clone(), d["base"].clone(), []
+        torch.cuda.synchronize()
+        for _ in range(8):
+            _, V = m.cr_lora_forward(A, d["down"], d["up"], scale, adapter=a, base=B, out=B, save_v=True)
+            between()
+            codes, scales = m.cr_ckpt_save(A)
+            between()
+            m.cr_ckpt_load(codes, scales, out=A)
+            between()
+            _, dd, du = m.cr_lora_backward(B, (codes, scales), V, d["down"], d["up"], scale, adapter=a, base=A, out=A)
+            between()
+            Y = m.cr_lora_forward(B, dd, du, scale, adapter=a, base=A)
+            between()
+            m.cr_w4a4_grad_input(A, Wq, s_w, out=B)
+            between()
+            _, dd2, _ = m.cr_lora_backward(B, A, None, dd, du, scale, adapter=a, need_dx=False, need_up=False)
+            between()
+            seen += [Y, dd, du, dd2]
+        torch.cuda.synchronize()
+        return seen + [A, B]
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        got = run(lambda: None)
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(got, want))
