@@ -106,7 +106,7 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   const int L = num_adapters;
   if (cr::use_lora_rows(M, N, K, rank, L))
     return static_cast<cr_status>(
-        cr::launch_lora_rows(x, ldx, adapter, dn, u, scale, b, ldb, y, ldy, vout, M, N, K, rank, L,
+        cr::launch_lora_rows(x, ldx, adapter, dn, u, scale, b, ldb, y, ldy, nullptr, vout, M, N, K, rank, L,
                              workspace && workspace_bytes >= 16 ? status : nullptr, s));
   int r = cr::launch_lora_v_mma(x, ldx, adapter, dn, v, vout, M, K, rank, L, status, nsm, s);
   if (r == CR_OK) r = cr::launch_lora_y_mma(v, adapter, u, scale, b, ldb, y, ldy, M, N, rank, L, status, nsm, s);
@@ -161,20 +161,22 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   float* gd = reinterpret_cast<float*>(w + bytes_f32(static_cast<int64_t>(M) * rank));
   float* gu = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(gd) + (parts.down > 1 ? bytes_f32(parts.down * nd) : 0));
   int* status = ws_status(workspace);
-  if (dX || d_down) {
-    st = static_cast<cr_status>(cr::launch_lora_v_mma(static_cast<const uint16_t*>(dY), lddy, adapter,
-                                                      static_cast<const uint16_t*>(up), dv, nullptr, M, N, rank, L,
-                                                      status, nsm, s));
-    if (st != CR_OK) return st;
+  const uint16_t* dy = static_cast<const uint16_t*>(dY);
+  const uint16_t* dn = static_cast<const uint16_t*>(down);
+  const uint16_t* u = static_cast<const uint16_t*>(up);
+  const uint16_t* xb = static_cast<const uint16_t*>(dX_base);
+  uint16_t* dx = static_cast<uint16_t*>(dX);
+  int r = CR_OK;
+  if (dX && cr::use_lora_rows(M, K, N, rank, L)) {  // the forward's two products, up and down in each other's places
+    r = cr::launch_lora_rows(dy, lddy, adapter, u, dn, scale, xb, ldb, dx, lddx, dv, nullptr, M, K, N, rank, L, status, s);
+  } else if (dX || d_down) {
+    r = cr::launch_lora_v_mma(dy, lddy, adapter, u, dv, nullptr, M, N, rank, L, status, nsm, s);
+    if (r == CR_OK && dX)
+      r = cr::launch_lora_y_mma(dv, adapter, dn, scale, xb, ldb, dx, lddx, M, K, rank, L, status, nsm, s);
   } else if (cudaMemsetAsync(workspace, 0, 16, s) != cudaSuccess) {
     return CR_ERR_CUDA;
   }
-  if (dX) {
-    st = static_cast<cr_status>(cr::launch_lora_y_mma(dv, adapter, static_cast<const uint16_t*>(down), scale,
-                                                      static_cast<const uint16_t*>(dX_base), ldb,
-                                                      static_cast<uint16_t*>(dX), lddx, M, K, rank, L, status, nsm, s));
-    if (st != CR_OK) return st;
-  }
+  if (r != CR_OK) return static_cast<cr_status>(r);
   if (d_down || d_up) {
     st = static_cast<cr_status>(cr::launch_lora_grad_mma(
         codes ? codes : X, ldx, code_scales, dY, lddy, dv, static_cast<const uint16_t*>(V), adapter, scale,

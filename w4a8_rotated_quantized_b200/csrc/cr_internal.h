@@ -160,11 +160,12 @@ int launch_w4a4_gemm_multi_s32(const void* Xq, int num_proj, const void* const* 
 
 // ---- adapters beside a projection, their gradients, 8-bit checkpoints (lora_rows.cu, ckpt_kernels.cu) ----
 constexpr int kMaxRank = 128;
-// Forward for few rows in one launch (lora_rows.cu; it clears the status word if there is one), and whether it is the faster form.
+// Both products for few rows in one launch (lora_rows.cu; it clears the status word if there is one; V float32 and
+// Vout bf16 [M, rank], each null if not wanted), and whether it is the faster form.
 bool use_lora_rows(int M, int N, int K, int rank, int L);
 int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, const uint16_t* up,
-                     const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, uint16_t* Vout,
-                     int M, int N, int K, int rank, int L, int* status, cudaStream_t stream);
+                     const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, float* V,
+                     uint16_t* Vout, int M, int N, int K, int rank, int L, int* status, cudaStream_t stream);
 // The products on the tensor cores, for batches (lora_mma.cu).  V float32 [M, rank] of the rows' own adapters
 // (zeros for rows without one), Vout its bf16 copy or null; the v product clears the status word.
 int launch_lora_v_mma(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, float* V,

@@ -33,6 +33,7 @@ namespace cr {
 namespace {
 
 #include "act_device.cuh"
+#include "unit_device.cuh"
 
 constexpr int GN = 64;             // weight rows of a tile
 constexpr int GC = 256;            // columns of a CTA
@@ -285,69 +286,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The parts of the sum added up, rotated (values and lane mapping of act_device.cuh: 4 lanes for each 256
-// values, 8 slices a block) and rounded.  Warp w of four adds parts w, w + 4, ..., in order; the first adds the
-// four sums: as many loads on their way as four warps can have, since each is a round trip to L2.
+// The parts of the sum joined, rotated (values and lane mapping of act_device.cuh: 4 lanes for each 256 values, 8
+// slices a block) and rounded.
 template <int kDig>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     grad_input_finish_kernel(const float* __restrict__ P, int parts, int64_t stride, uint16_t* __restrict__ dX,
                              int64_t lddx, int64_t units, int upr) {
   griddep_wait();  // launched as a dependent of the product's kernel
-  __shared__ float4 sums[3][16][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (lane >> 2);
-  const int k0 = lane >> 2, l = lane & 3;
+  __shared__ JoinSums sums;
+  const int lane = threadIdx.x & 31, k0 = lane >> 2, l = lane & 3;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + k0;
   const bool in = u < units;
   float4 v[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = warp; p < (in ? parts : 0); p += 4) {
-    const float* src = P + p * stride + u * 256 + 8 * l;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
-      v[k].x += f.x;
-      v[k].y += f.y;
-      v[k].z += f.z;
-      v[k].w += f.w;
-    }
-  }
-  if (warp > 0) {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) sums[warp - 1][k][lane] = v[k];
-  }
-  __syncthreads();
-  if (warp > 0) return;
+  auto at = [&](int k) { return 32 * ((k >> 1) ^ k0) + 8 * l + 4 * (k & 1); };
+  if (!join_parts(P + u * 256, parts, stride, in, at, sums, v)) return;
   Pairs V;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-#pragma unroll
-    for (int w = 0; w < 3; ++w) {
-      const float4 f = sums[w][k][lane];
-      v[k].x += f.x;
-      v[k].y += f.y;
-      v[k].z += f.z;
-      v[k].w += f.w;
-    }
-    const float e[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float2& pair = V.w[8 * ((k >> 1) & 3) + 4 * (k & 1) + c];
-      if (k < 8) pair.x = e[c]; else pair.y = e[c];
-    }
-  }
+  for (int k = 0; k < 16; ++k) put4(V, k, v[k]);
   fwht256_mapped<kDig>(V);
-  if (!in) return;
-  const int64_t row = u / upr;
-  uint16_t* unit = dX + row * lddx + (u - row * upr) * 256;
-  constexpr float f = 1.f / static_cast<float>(1 << kDig);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = f * (k < 4 ? V.w[8 * (k & 3) + e].x : V.w[8 * (k & 3) + e].y);
-    *reinterpret_cast<uint4*>(unit + 32 * (k ^ k0) + 8 * l) = narrow8(v);
-  }
+  if (in)
+    store_unit_bf16(V, k0, 1.f / static_cast<float>(1 << kDig), dX + u / upr * lddx + (u % upr) * 256);
 }
 
 std::atomic<bool> g_attr_done[64];

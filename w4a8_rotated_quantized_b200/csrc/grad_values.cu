@@ -86,44 +86,23 @@ __global__ void __launch_bounds__(32 * kWarps)
   store_unit_bf16(P, k0, s, W + u * 256);
 }
 
-// Eight values of the partial sums, added in order.
-__device__ __forceinline__ void add_parts(const float* __restrict__ src, int parts, int64_t stride, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float4 f0 = __ldcg(reinterpret_cast<const float4*>(src + p * stride));
-    const float4 f1 = __ldcg(reinterpret_cast<const float4*>(src + p * stride + 4));
-    v[0] += f0.x; v[1] += f0.y; v[2] += f0.z; v[3] += f0.w;
-    v[4] += f1.x; v[5] += f1.y; v[6] += f1.z; v[7] += f1.w;
-  }
-}
-
-// The gradients' partial sums joined and rounded.  The first `rot_blocks` blocks take slices of 256 values
-// of the rotated d_down, the rest eight values a thread of what is left: d_down unrotated, then d_up.
-// One warp a block: few, small pieces of work, each a round trip to L2.
-__global__ void __launch_bounds__(32)
-    lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts_down, int parts_up, int64_t n_down,
-                            int64_t n_up, uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up, int rot_blocks) {
+// The gradients' partial sums joined and rounded, a block of four warps for what one can hold.  The first
+// `rot_blocks` blocks take eight slices of 256 values of the rotated d_down, the rest 256 values each of what is
+// left: d_down unrotated, then d_up.
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    lora_grad_finish_kernel(const float* __restrict__ Gdown, const float* __restrict__ Gup, int parts_down, int parts_up,
+                            int64_t n_down, int64_t n_up, uint16_t* __restrict__ d_down, uint16_t* __restrict__ d_up,
+                            int rot_blocks, int down_blocks) {
   griddep_wait();  // launched as a dependent of the products' kernel
-  if (static_cast<int>(blockIdx.x) < rot_blocks) {
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 2);
-    const int k0 = (threadIdx.x & 31) >> 2, l = threadIdx.x & 3;
+  __shared__ JoinSums sums;
+  const int lane = threadIdx.x & 31, block = static_cast<int>(blockIdx.x);
+  if (block < rot_blocks) {
+    const int64_t u = static_cast<int64_t>(block) * 8 + (lane >> 2);
+    const int k0 = lane >> 2, l = lane & 3;
     const bool in = u < n_down >> 8;
     float4 v[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = 0; p < (in ? parts_down : 0); ++p) {  // (a part's 16 loads are on their way together)
-      const float* src = Gdown + p * n_down + u * 256 + 8 * l;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(src + 32 * ((k >> 1) ^ k0) + 4 * (k & 1)));
-        v[k].x += f.x;
-        v[k].y += f.y;
-        v[k].z += f.z;
-        v[k].w += f.w;
-      }
-    }
+    auto at = [&](int k) { return 32 * ((k >> 1) ^ k0) + 8 * l + 4 * (k & 1); };
+    if (!join_parts(Gdown + u * 256, parts_down, n_down, in, at, sums, v)) return;
     Pairs P;
 #pragma unroll
     for (int k = 0; k < 16; ++k) put4(P, k, v[k]);
@@ -131,19 +110,15 @@ __global__ void __launch_bounds__(32)
     if (in) store_unit_bf16(P, k0, 0.0625f, d_down + u * 256);
     return;
   }
-  int64_t i = (static_cast<int64_t>(blockIdx.x - rot_blocks) * 32 + threadIdx.x) * 8;
-  float v[8];
-  if (!rot_blocks) {
-    if (i < n_down) {
-      add_parts(Gdown + i, parts_down, n_down, v);
-      *reinterpret_cast<uint4*>(d_down + i) = narrow8(v);
-      return;
-    }
-    i -= n_down;
-  }
-  if (i >= n_up) return;
-  add_parts(Gup + i, parts_up, n_up, v);
-  *reinterpret_cast<uint4*>(d_up + i) = narrow8(v);
+  const bool down = block - rot_blocks < down_blocks;
+  const int64_t i = static_cast<int64_t>(block - rot_blocks - (down ? 0 : down_blocks)) * 256 + 8 * lane;
+  const int64_t n = down ? n_down : n_up;
+  float4 f[2];
+  if (!join_parts((down ? Gdown : Gup) + i, down ? parts_down : parts_up, n, i < n, [](int k) { return 4 * k; }, sums, f))
+    return;
+  if (i >= n) return;
+  const float v[8] = {f[0].x, f[0].y, f[0].z, f[0].w, f[1].x, f[1].y, f[1].z, f[1].w};
+  *reinterpret_cast<uint4*>((down ? d_down : d_up) + i) = narrow8(v);
 }
 
 unsigned unit_blocks(int64_t units) { return static_cast<unsigned>((units + 8 * kWarps - 1) / (8 * kWarps)); }
@@ -165,20 +140,20 @@ cudaError_t launch_weight_values(const uint8_t* Wq, const float* w_scale, uint16
 cudaError_t launch_lora_grad_finish(const float* Gdown, const float* Gup, int parts_down, int parts_up, int64_t rows, int K, int N,
                                     uint16_t* d_down, uint16_t* d_up, bool rotate, cudaStream_t stream) {
   const int64_t n_down = d_down ? rows * K : 0, n_up = d_up ? rows * N : 0;
-  const unsigned rot = rotate && d_down ? static_cast<unsigned>((n_down / 256 + 7) / 8) : 0;
-  const int64_t plain = (rot ? 0 : n_down) + n_up;
-  const unsigned blocks = rot + static_cast<unsigned>((plain + 255) / 256);
+  const unsigned rot = rotate ? static_cast<unsigned>((n_down / 256 + 7) / 8) : 0;
+  const unsigned down = rotate ? 0 : static_cast<unsigned>((n_down + 255) / 256);
+  const unsigned blocks = rot + down + static_cast<unsigned>((n_up + 255) / 256);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(32, 1, 1);
+  cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, lora_grad_finish_kernel, Gdown, Gup, parts_down, parts_up, n_down, n_up, d_down, d_up,
-                            static_cast<int>(rot));
+                            static_cast<int>(rot), static_cast<int>(down));
 }
 
 }  // namespace cr

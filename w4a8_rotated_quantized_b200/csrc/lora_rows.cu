@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     lora_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, const int32_t* __restrict__ adapter,
                      const uint16_t* __restrict__ down, const uint16_t* __restrict__ up,
                      const float* __restrict__ scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy,
-                     uint16_t* __restrict__ Vout, int N, int K, int rank, int L, int ctas, int* __restrict__ status) {
+                     float* __restrict__ V32, uint16_t* __restrict__ Vout, int N, int K, int rank, int L, int ctas,
+                     int* __restrict__ status) {
   __shared__ float part[kMostCluster][kMaxRank];
   // sums of the tasks [pass][rank]; later partial results [rank group][column piece][8]
   __shared__ __align__(16) float scratch[kMostPasses * kMaxRank];
@@ -68,6 +69,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int p = tid; p < pieces; p += kThreads)
       *reinterpret_cast<uint4*>(Y + m * ldy + 8 * (p0 + p)) =
           brow ? ldcg16(brow + 8 * (p0 + p)) : make_uint4(0, 0, 0, 0);
+    if (V32 && c == 0 && tid < rank) V32[m * rank + tid] = 0.f;
     if (Vout && c == 0 && tid < rank) Vout[m * rank + tid] = 0;
     return;
   }
@@ -127,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int i = 0; i < kMostCluster; ++i)
       if (i < ctas) t += part[i][tid];
+    if (V32 && c == 0) V32[m * rank + tid] = t;
     if (Vout && c == 0) Vout[m * rank + tid] = bf16_bits(t);
     v[tid] = t * __ldg(scale + a);
   }
@@ -203,8 +206,8 @@ bool use_lora_rows(int M, int N, int K, int rank, int L) {
 }
 
 int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, const uint16_t* down, const uint16_t* up,
-                     const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, uint16_t* Vout,
-                     int M, int N, int K, int rank, int L, int* status, cudaStream_t stream) {
+                     const float* scale, const uint16_t* base, int64_t ldb, uint16_t* Y, int64_t ldy, float* V,
+                     uint16_t* Vout, int M, int N, int K, int rank, int L, int* status, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CR_ERR_CUDA;
   if (!g_attr_done[dev].load()) {
@@ -227,7 +230,7 @@ int launch_lora_rows(const uint16_t* X, int64_t ldx, const int32_t* adapter, con
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, lora_rows_kernel, X, ldx, adapter, down, up, scale, base, ldb, Y, ldy, Vout, N, K,
+  return cudaLaunchKernelEx(&cfg, lora_rows_kernel, X, ldx, adapter, down, up, scale, base, ldb, Y, ldy, V, Vout, N, K,
                             rank, L, ctas, status) == cudaSuccess
              ? CR_OK
              : CR_ERR_CUDA;
