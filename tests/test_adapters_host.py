@@ -120,6 +120,9 @@ def test_refusals_by_code():
     assert gi(lddy=268) == 3 and gi(dX=odd) == 3
     need = lib.cr_w4a4_grad_input_workspace_size(40, 264, 512, 256)
     assert need >= 40 * 512 * 4 and gi(n=need) in DEV and gi(n=need - 1) == 5
+    need = lib.cr_w4a4_grad_input_workspace_size(4, 2640, 512, 256)  # straight from the packed weights
+    assert 4 * 2640 * 2 <= need < 2640 * 512 * 2 and gi(M=4, N=2640, lddy=2640, n=need) in DEV
+    assert gi(M=4, N=2640, lddy=2640, n=need - 1) == 5
     need = lib.cr_w4a4_grad_input_workspace_size(4000, 264, 512, 256)
     assert need >= 264 * 512 * 2 and gi(M=4000, n=need) in DEV and gi(M=4000, n=need - 1) == 5
 

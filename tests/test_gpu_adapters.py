@@ -319,7 +319,10 @@ def test_checkpoint_past_32_bit_offsets():
     (1, 256, 8, 256, "tensor"), (1, 2560, 9728, 256, "row"), (21, 1024, 136, 1024, "row"), (130, 512, 256, 16, "tensor"),
     (129, 768, 264, 64, "row"), (257, 1280, 1000, 256, "tensor"), (300, 9728, 2560, 256, "row"), (1030, 3072, 1544, 256, "tensor"),
     (5, 4096, 72, 1024, "tensor"), (64, 512, 64, 64, "row"), (128, 1024, 520, 16, "row"), (512, 512, 320, 256, "tensor"),
-    (513, 512, 320, 256, "row"), (300, 256, 520, 64, "row"), (512, 256, 1024, 256, "tensor"), (600, 2048, 200, 1024, "tensor"), (77, 256, 2048, 256, "row")])
+    (513, 512, 320, 256, "row"), (300, 256, 520, 64, "row"), (512, 256, 1024, 256, "tensor"), (600, 2048, 200, 1024, "tensor"), (77, 256, 2048, 256, "row"),
+    # straight from the packed weights: enough of them for each token
+    (3, 512, 520, 16, "row"), (130, 2048, 2304, 64, "row"), (200, 2048, 4008, 1024, "row"), (257, 4096, 2312, 256, "tensor"),
+    (600, 4096, 5128, 256, "row"), (512, 5120, 3600, 16, "tensor")])
 def test_grad_input(M, K, N, group, mode):
     g = gen(M + N)
     W = randn(g, N, K, std=0.02)

@@ -8,12 +8,12 @@
 //
 // * A CTA takes 256 columns of the weights, up to 256 tokens and a part of the sum over n, 64 rows of the weights
 //   at a time: the packed codes arrive by TMA, become bf16 (exact) and are the product's M side as they lie
-//   (MN-major); s_w dY, split into rounded values and rests (16 bits of mantissa) that go into the same sums, is
-//   its N side.  Two sets of eight warps prepare alternate tiles of codes.
-// * s_w dY is split once, by a small kernel before: split in each CTA it cost as much as the codes (128 tokens,
+//   (MN-major); s_w dY, rounded to bf16, is its N side.  Two sets of eight warps prepare alternate tiles of codes.
+// * s_w dY is made once, by a small kernel before: made in each CTA it cost as much as the codes (128 tokens,
 //   9728 x 2560: 23 us against 15).  This one starts beside it and waits for it before the first N side's load.
 // * float32 sums in TMEM; the parts of the sum go to the workspace and a third kernel adds them in order,
-//   rotates and rounds once.
+//   rotates and rounds once.  (Joined by a cluster through distributed shared memory instead, without the third
+//   kernel, 130 tokens of 9728 x 2560 took 31 us instead of 24: few clusters fit, and the sums' way is no shorter.)
 //
 // What bounds it: the codes' way through the ALUs (13 instructions for 8) and, with few tiles a CTA, setting up.
 
@@ -53,7 +53,7 @@ inline __host__ __device__ Plan plan(int M) {
   Plan p;
   p.blocks = (M + kMostTokens - 1) / kMostTokens;
   p.rp = ((M + p.blocks - 1) / p.blocks + 15) & ~15;
-  p.stage = kZTile + 2 * p.rp * 128;
+  p.stage = kZTile + p.rp * 128;
   // an even number of raw tiles, so that each set of warps meets its slots round by round
   p.raws = p.stage <= 48 * 1024 ? 4 : 2;
   p.stages = (kSmemMax - 256 - p.raws * kRawTile) / p.stage;
@@ -88,10 +88,12 @@ __device__ __forceinline__ void give_up(volatile int* abort, int* status) {
   while (globaltimer_ns() - t < 1000000ull) __nanosleep(1000);
 }
 
-// The N side: for each token block rp rows of bf16(s_w dY) and rp rows of what those leave; zeros past M.
+// The N side: bf16(s_w dY), rows of zeros behind the last token.  Rounding it once is off by at most 2^-9 of each
+// term, what the GEMM's form pays for bf16 weights (here those are exact); with the rests as a second part of the
+// sum 130 tokens of 9728 x 2560 took 27 us instead of 24.
 __global__ void __launch_bounds__(256)
     grad_input_operand_kernel(const uint16_t* __restrict__ dY, int64_t lddy, const float* __restrict__ w_scale,
-                              uint16_t* __restrict__ V, int M, int N, int rp, int* __restrict__ status) {
+                              uint16_t* __restrict__ V, int M, int N, int* __restrict__ status) {
   griddep_wait();  // for what the stream ran before
   griddep_launch_dependents();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = CR_OK;
@@ -103,12 +105,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= __ldg(w_scale + n + e);
   }
-  uint32_t hi[4], lo[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) split_bf16(v[2 * e], v[2 * e + 1], hi[e], lo[e]);
-  uint16_t* out = V + (static_cast<int64_t>(m / rp) * 2 * rp + m % rp) * N + n;
-  *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(out + static_cast<int64_t>(rp) * N) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  *reinterpret_cast<uint4*>(V + static_cast<int64_t>(m) * N + n) = narrow8(v);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -176,14 +173,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kBox, kBox);
+          const uint64_t dv = sw128_kmajor_desc(z + kZTile);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // rounded values, rests
-            const uint64_t dv = sw128_kmajor_desc(z + kZTile + h * p.rp * 128);
-#pragma unroll
-            for (int kk = 0; kk < GN / 16; ++kk)
-              umma_f16_ss(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 2u * kk, idesc,
-                          (i || h || kk) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < GN / 16; ++kk)
+            umma_f16_ss(tmem + static_cast<uint32_t>(half * p.rp), dz + 128u * kk, dv + 2u * kk, idesc,
+                        (i || kk) ? 1u : 0u);
         }
         umma_commit(empty(s));
         last_bar = empty(s);
@@ -221,10 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 1;
       for (int i = 0; i < nt; ++i) {
         if (!mbar_sleep(empty(s), ph, abort)) { ok = false; break; }
-        mbar_arrive_expect_tx(v_full(s), 2 * p.rp * 128);
-        const uint32_t v = smem_u32(base + s * p.stage + kZTile);
-        tma_load_2d(v, &tmap_v, (t0 + i) * GN, block * 2 * p.rp, v_full(s));
-        tma_load_2d(v + p.rp * 128, &tmap_v, (t0 + i) * GN, block * 2 * p.rp + p.rp, v_full(s));
+        mbar_arrive_expect_tx(v_full(s), p.rp * 128);
+        tma_load_2d(smem_u32(base + s * p.stage + kZTile), &tmap_v, (t0 + i) * GN, m0, v_full(s));
         if (++s == p.stages) { s = 0; ph ^= 1u; }
       }
       if (!ok) give_up(abort, status);
@@ -322,11 +314,13 @@ bool set_attrs() {
 
 }  // namespace
 
-// Against unpacking the weights for the bf16 GEMM (us of GPU time, this form first): 9728 x 2560 (K x N) 1 token
-// 17 | 36, 256 tokens 41 | 52, 512 tokens 71 | 51; 3072 x 12288 256 tokens 47 | 95,
-// 512 tokens 78 | 97; 2560 x 9728 512 tokens 62 | 74.  A long sum favours this form: the GEMM's few tiles leave
-// most SMs idle.
-bool use_grad_input_few(int M, int N, int K) { return M <= 256 || (M <= 512 && N > K); }
+// Unpacking the weights for the bf16 GEMM costs by their number, this form by the tokens for each of them.  Fitted
+// to both forms' times for 310 calls of 1 to 1600 tokens and 128 to 12288 rows and columns: the choice costs 1.2 %
+// over the faster form on average and 59 % at worst (us, this form first):
+//   112 tokens, 7936 x 11200 (K x N): 40 | 118        238 tokens, 5376 x 520:  21 | 12
+//   308 tokens, 4608 x 6368:          41 | 58         435 tokens, 7680 x 4416: 52 | 52
+//   621 tokens, 768 x 7888:           33 | 52 (the worst choice)
+bool use_grad_input_few(int M, int N, int K) { return M <= 600 && static_cast<int64_t>(N) * K > 100000 + 34000LL * M; }
 
 int grad_input_few_splits(int M, int N, int K, int num_sms) {
   const int tiles = (N + GN - 1) / GN;
@@ -346,7 +340,7 @@ int grad_input_few_splits(int M, int N, int K, int num_sms) {
 
 size_t grad_input_few_operand_rows(int M) {
   const Plan p = plan(M);
-  return static_cast<size_t>(p.blocks) * 2 * p.rp;
+  return static_cast<size_t>(p.blocks) * p.rp;
 }
 
 int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, const float* w_scale, uint16_t* V,
@@ -371,7 +365,7 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, grad_input_operand_kernel, dY, lddy, w_scale, V, M, N, p.rp, status) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, grad_input_operand_kernel, dY, lddy, w_scale, V, M, N, status) != cudaSuccess)
     return CR_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(K / GC * p.blocks * splits), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
