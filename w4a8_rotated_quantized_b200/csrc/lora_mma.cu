@@ -107,6 +107,10 @@ __device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter
 // ---------------------------------------------------------------------------------------------------
 // v: 128 tokens x (up to 256 / rank adapters side by side); the sum over k split over a cluster's CTAs,
 // whose partial sums go to the CTA that adds up their row, in rank order, through distributed shared memory.
+// By itself it takes 13.5 us for 4096 x 3072 at rank 64 and 16 us for 8192 x 3072 at rank 32 (1.9 and 3.2 TB/s):
+// X comes in about 5 and 9 of them, the rest is starting and the exchange, which is why the kernels before and
+// after it run into it.  (As one kernel with y, V passed round a cluster, the two took 28.4 us instead of 26.6 for
+// 4096 tokens and 20.5 instead of 15.5 for 130.)
 // ---------------------------------------------------------------------------------------------------
 
 struct VPlan {
@@ -323,6 +327,9 @@ __global__ void __launch_bounds__(kVThreads, 1)
 // from.  V of the 128 rows, scaled and split into bf16 pairs, stays in TMEM as the product's A operand for
 // all column tiles: read from shared memory it would cost as many bytes there as U does, and at rank 128
 // those bytes, not memory's, set the pace (134 us against 110 us for 8192 x 12288).
+// By itself it takes 72 us for 8192 -> 12288 at rank 32 (402 MB of base and result: 5.6 TB/s) and 107 us at rank
+// 128 with four adapters (3.8 TB/s), where memory waits for the products of tiles that hold two adapters' rows and
+// for the 20 SMs that 64 token tiles in two column parts leave idle.
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int TN = 128;
@@ -602,6 +609,12 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
 // widened to bf16): a set's chain of loads, conversions, stores and signals is longer than a tile's time, and
 // each set's next V is on its way in registers meanwhile.  V's rounded values and rests lie side by side as
 // twice as many columns of one product, which costs the same up to 64 columns: the MMAs' issue bounds those.
+// A gradient that is not split is rounded here, one against codes after its rotation in shared memory: for few
+// tokens the partial sums' way through memory and a kernel more cost as much as the product (1 token, 14 adapters
+// of rank 64, 1024 -> 4296: 32 us a backward pass with them, 21 without).
+// By itself it takes 17.6 us for 4096 x (3072 + 3072) at rank 64 (52 MB: 3.0 TB/s; start, first tiles and sums are
+// half of it) and 54 us for 8192 x (12288 codes + 3072 bf16) at rank 32 (154 MB: 2.8 TB/s), bound by the codes'
+// way through the ALUs (56 % of the issue slots).
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int GM = 64;           // tokens of a tile
@@ -727,10 +740,10 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
         if (!mbar_sleep(ready(s), ph, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t z = smem_u32(base + s * p.stage);
-  #pragma unroll
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint64_t dz = sw128_mnmajor_desc(z + half * 2 * kZBox, kZBox);
-            const uint64_t dv = sw128_mnmajor_desc(z + kZTile, GM * 128);
+          const uint64_t dv = sw128_mnmajor_desc(z + kZTile, GM * 128);
 #pragma unroll
           for (int kk = 0; kk < GM / 16; ++kk)
             umma_f16_ss(tmem + static_cast<uint32_t>(half * p.vcols), dz + 128u * kk, dv + 128u * kk, idesc,
@@ -1092,8 +1105,8 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
 
 // Token splits of the two gradient products, down's and up's.  In units of one bf16 tile's time on an SM (about
 // a third of a microsecond; a tile of codes takes about 1.5): each CTA has its tiles and about eight tiles'
-// worth of setting up and writing out; the partial sums go to memory and back (about 1.6 MB a unit).  Up's
-// splits follow from down's so that both kinds of CTA take as long.
+// worth of setting up and writing out; if either is split a kernel more costs about ten, and the partial sums go to
+// memory and back (about 0.8 MB a unit).  Up's splits follow from down's so that both kinds of CTA take as long.
 void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_sms, int* down, int* up) {
   const int64_t cd = static_cast<int64_t>((K + GC - 1) / GC) * L, cu = static_cast<int64_t>((N + GC - 1) / GC) * L;
   const int tiles = (M + GM - 1) / GM;
