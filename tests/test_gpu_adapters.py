@@ -622,3 +622,64 @@ def test_calls_on_each_others_results(M, L, mix):
     for _ in range(5):
         got = run(lambda: None)
         assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(got, want))
+
+
+def test_after_other_work_on_the_stream():
+    """Calls behind a copy, a memset, another stream's event and each other, eagerly and captured: their kernels
+    start beside the end of what is before them and must not read too early."""
+    m = cr()
+    sets = [make(3, 512, 768, 16, 3, "rows", seed=81), make(300, 512, 768, 64, 2, "runs", seed=82)]
+    Wq, s_w = m.cr_pack_weight(randn(gen(83), 768, 512, std=0.02))
+    side = torch.cuda.Stream()
+    late = [{k: torch.zeros_like(v) if torch.is_tensor(v) else v for k, v in d.items()} for d in sets]
+    slow = torch.zeros(64 << 20, device="cuda")
+
+    def calls(i):
+        here, d, t = torch.cuda.current_stream(), sets[i], late[i]
+        for k in d:  # whatever the call before left there goes
+            if torch.is_tensor(d[k]):
+                t[k].zero_()
+        for k in ("down", "up", "scale", "adapter", "base"):  # copies right before the call
+            t[k].copy_(d[k])
+        side.wait_stream(here)
+        with torch.cuda.stream(side):  # and rows from another stream, after something long
+            slow.add_(1)
+            t["X"].copy_(d["X"])
+            t["dY"].copy_(d["dY"])
+        here.wait_stream(side)
+        Y, V = m.cr_lora_forward(t["X"], t["down"], t["up"], t["scale"], adapter=t["adapter"], base=t["base"], save_v=True)
+        t["X"].zero_()
+        t["X"].copy_(d["X"])
+        kept = m.cr_ckpt_save(t["X"])
+        back = m.cr_ckpt_load(*kept)
+        _, _, du = m.cr_lora_backward(t["dY"], None, V, t["down"], t["up"], t["scale"], adapter=t["adapter"],
+                                      need_dx=False, need_down=False)
+        g = m.cr_lora_backward(t["dY"], kept, V, t["down"], t["up"], t["scale"], adapter=t["adapter"])
+        t["dY"].zero_()
+        t["dY"].copy_(d["dY"])
+        return (Y, V, *kept, back, du, *g, m.cr_w4a4_grad_input(t["dY"], Wq, s_w))
+
+    def same(a, b):
+        return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)) for x, y in zip(a, b))
+
+    for i, d in enumerate(sets):
+        Y, V = m.cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=d["adapter"], base=d["base"], save_v=True)
+        torch.cuda.synchronize()
+        kept = m.cr_ckpt_save(d["X"])
+        torch.cuda.synchronize()
+        back = m.cr_ckpt_load(*kept)
+        g = m.cr_lora_backward(d["dY"], kept, V, d["down"], d["up"], d["scale"], adapter=d["adapter"])
+        torch.cuda.synchronize()
+        want = (Y, V, *kept, back, g[2], *g, m.cr_w4a4_grad_input(d["dY"], Wq, s_w))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            assert same(calls(i), want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = calls(i)
+        for _ in range(3):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert same(got, want)

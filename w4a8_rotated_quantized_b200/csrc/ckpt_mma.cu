@@ -94,9 +94,10 @@ __device__ __forceinline__ void init_bars(const Bars& bars, volatile int* abort,
   fence_proxy_async_smem();
 }
 
-// TMEM and the block's meeting; returns the TMEM base.
+// What the stream ran before, TMEM, and the block's meeting; returns the TMEM base.
 __device__ __forceinline__ uint32_t start(uint8_t* misc) {
   uint32_t* slot = reinterpret_cast<uint32_t*>(misc);
+  griddep_wait();
   if (threadIdx.x < 32) {
     tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
@@ -158,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     *reinterpret_cast<uint4*>(base + v * kBox + n * 128 + ((piece ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   const uint32_t tmem = start(misc);
-  griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
@@ -315,7 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     *reinterpret_cast<uint4*>(base + kb * 2 * kBox + n * 128 + ((piece ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   const uint32_t tmem = start(misc);
-  griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {

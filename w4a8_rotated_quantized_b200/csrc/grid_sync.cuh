@@ -56,8 +56,9 @@ __device__ __forceinline__ bool grid_arrive_wait(unsigned long long* count, unsi
 // with griddep_wait until this grid has completed and its memory is visible before it reads this grid's
 // results.  A chain's first kernel is a dependent of whatever the stream ran before: it waits before it touches
 // any memory of the caller's, and lets its own dependents start only then, so that what they read ahead of their
-// own wait is complete too.  A kernel that holds TMEM allocates it before it lets dependents start, which might
-// otherwise take what it still needs and wait for it.
+// own wait is complete too.  TMEM: a kernel allocates its own before it lets dependents start, which might otherwise
+// take what it still needs and wait for it; a chain's first kernel, after one that need not do so, allocates after
+// its wait.
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

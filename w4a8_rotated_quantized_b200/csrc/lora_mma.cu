@@ -175,11 +175,11 @@ __global__ void __launch_bounds__(kVThreads, 1)
     prefetch_tmap(&tmap_x);
     prefetch_tmap(&tmap_a);
   }
+  griddep_wait();  // for what the stream ran before
   if (warp == 0) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
   }
-  griddep_wait();  // for what the stream ran before
   if (threadIdx.x == 0) {
     griddep_launch_dependents();  // the y kernel may set itself up beside this one
     if (blockIdx.x == 0) *status = CR_OK;
