@@ -114,6 +114,21 @@ def test_forward(shape):
     assert torch.equal(Y.view(torch.int16), Y2.view(torch.int16))
 
 
+@pytest.mark.parametrize("has_base", [True, False])
+@pytest.mark.parametrize("r,L,mix", [(24, 5, "runs"), (128, 9, "runs"), (64, 6, "rows"), (16, 2, "last"), (100, 1, "all"), (4, 3, "none")])
+def test_column_tiles_dealt_out_over_token_tiles(r, L, mix, has_base):
+    """75 token tiles of 20 column tiles: most CTAs go on from one token tile to the next."""
+    d = make(9500, 136, 2504, r, L, mix, seed=9)
+    base = d["base"] if has_base else None
+    args = (d["down"], d["up"], d["scale"])
+    want, _, ey, _ = ao.lora_forward(f64(d["X"]), *(f64(t) for t in args), ids(d["adapter"]), f64(base) if has_base else None)
+    got = cr().cr_lora_forward(d["X"], *args, adapter=d["adapter"], base=base)
+    within(got, want, ey, "Y")
+    parts = [cr().cr_lora_forward(d["X"][i:j], *args, adapter=None if d["adapter"] is None else d["adapter"][i:j],
+                                  base=base[i:j] if has_base else None) for i, j in ((0, 2048), (2048, 9500))]
+    assert torch.equal(got, torch.cat(parts))
+
+
 @pytest.mark.parametrize("shape", [(5, 264, 136, 8, 2, "rows"), (150, 520, 264, 24, 3, "runs"), (1, 256, 64, 4, 1, "all")],
                          ids=str)
 def test_forward_strides_no_base_and_in_place(shape):

@@ -327,9 +327,11 @@ __global__ void __launch_bounds__(kVThreads, 1)
 // from.  V of the 128 rows, scaled and split into bf16 pairs, stays in TMEM as the product's A operand for
 // all column tiles: read from shared memory it would cost as many bytes there as U does, and at rank 128
 // those bytes, not memory's, set the pace (134 us against 110 us for 8192 x 12288).
-// By itself it takes 72 us for 8192 -> 12288 at rank 32 (402 MB of base and result: 5.6 TB/s) and 107 us at rank
-// 128 with four adapters (3.8 TB/s), where memory waits for the products of tiles that hold two adapters' rows and
-// for the 20 SMs that 64 token tiles in two column parts leave idle.
+// Column tiles are dealt out over the CTAs token tile by token tile; where that does not come out even a CTA goes on
+// to the next token tile, with that one's V.  8192 tokens, 3072 -> 12288 at rank 128 with four adapters take 117 us
+// a call that way and 123 in two equal parts of each token tile, which leave 20 SMs idle.
+// By itself the kernel takes 72 us for 8192 -> 12288 at rank 32 (402 MB of base and result: 5.6 TB/s); at rank 128
+// with four adapters memory waits for the products of the tiles that hold two adapters' rows (101 us: 4 TB/s).
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int TN = 128;
@@ -359,16 +361,15 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     lora_y_mma_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_base,
                       const __grid_constant__ CUtensorMap tmap_y, const float* __restrict__ V,
                       const int32_t* __restrict__ adapter, const float* __restrict__ scale, int has_base, int M, int N,
-                      int rank, int L, int nsplit, int* __restrict__ status) {
+                      int rank, int L, int* __restrict__ status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align_smem(smem_raw);
   const YPlan p = y_plan(rank);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / nsplit) * TM;
-  const int part = blockIdx.x % nsplit;
+  // this CTA's share of all tiles, token tile by token tile
   const int tiles = (N + TN - 1) / TN;
-  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * part / nsplit);
-  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / nsplit);
+  const int64_t all = (static_cast<int64_t>(M) + TM - 1) / TM * tiles;
+  const int64_t begin = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
   int* ids = reinterpret_cast<int*>(base + p.off_list);
   int* list = ids + TM;
   const uint32_t bars = smem_u32(base + p.off_bar);
@@ -414,187 +415,211 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts, kYMmaThreads);
+  // what the rings have gone through so far: tiles, products, times that V was made
+  int64_t tiles_done = 0, products = 0;
+  uint32_t vs = 0;
+  // the part in one token tile after the other; `next` is where the one after begins
+  for (int64_t pos = begin, next; pos < end; pos = next) {
+    const int64_t m0 = pos / tiles * TM;
+    const int t0 = static_cast<int>(pos % tiles);
+    const int t1 = end - pos < tiles - t0 ? t0 + static_cast<int>(end - pos) : tiles;
+    next = pos + t1 - t0;
+    const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts, kYMmaThreads);
+    const int y_first = static_cast<int>(tiles_done % p.nb), u_first = static_cast<int>(products % p.nu),
+              b_first = static_cast<int>(products % kAcc);
+    const uint32_t y_phase = tiles_done / p.nb & 1, u_phase = products / p.nu & 1, b_phase = products / kAcc & 1;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- MMA issuer (one thread)
-    if (elect_one()) {
-      bool ok = nd == 0 || mbar_sleep(v_ready, 0, abort);
-      tc_fence_after();
-      bool committed = false;
-      uint32_t last_bar = 0, last_ph = 0, ph = 0;
-      int s = 0, b = 0;  // the product's U stage and accumulator
-      uint32_t bph = 1;  // its accumulator is free: the phase before the first counts as completed
-      const uint32_t idesc = idesc_bf16(TM, TN, false, true);
-      for (int t = t0; ok && t < t1; ++t) {
-        for (int i = 0; i < nd; ++i) {
-          if (!mbar_sleep(acc_empty(b), bph, abort)) { ok = false; break; }
-          if (!mbar_sleep(u_full(s), ph, abort)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
+    if (warp == 0) {
+      // ---------------------------------------------------------------- MMA issuer (one thread)
+      if (elect_one()) {
+        bool ok = nd == 0 || mbar_sleep(v_ready, vs & 1, abort);
+        tc_fence_after();
+        bool committed = false;
+        uint32_t last_bar = 0, last_ph = 0, ph = u_phase;
+        int s = u_first, b = b_first;  // the product's U stage and accumulator
+        uint32_t bph = b_phase ^ 1u;   // its accumulator is free: the phase before the first counts as completed
+        const uint32_t idesc = idesc_bf16(TM, TN, false, true);
+        for (int t = t0; ok && t < t1; ++t) {
+          for (int i = 0; i < nd; ++i) {
+            if (!mbar_sleep(acc_empty(b), bph, abort)) { ok = false; break; }
+            if (!mbar_sleep(u_full(s), ph, abort)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t du = sw128_mnmajor_desc(smem_u32(base + s * p.u), p.rp * 128);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
+            for (int h = 0; h < 2; ++h)  // V's rounded values, then the rests
 #pragma unroll
-            for (int kk = 0; kk < kMaxRank / 16; ++kk)
-              if (kk < p.rp / 16)
-                umma_f16_ts(tmem + static_cast<uint32_t>(b * TN),
-                            tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
-                            (h | kk) ? 1u : 0u);
-          umma_commit(u_empty(s));
-          umma_commit(acc_full(b));
-          last_bar = u_empty(s);
-          last_ph = ph;
-          committed = true;
-          if (++s == p.nu) { s = 0; ph ^= 1u; }
-          if (++b == kAcc) { b = 0; bph ^= 1u; }
+              for (int kk = 0; kk < kMaxRank / 16; ++kk)
+                if (kk < p.rp / 16)
+                  umma_f16_ts(tmem + static_cast<uint32_t>(b * TN),
+                              tmem + static_cast<uint32_t>(kVCol + h * (p.rp / 2) + 8 * kk), du + 128u * kk, idesc,
+                              (h | kk) ? 1u : 0u);
+            umma_commit(u_empty(s));
+            umma_commit(acc_full(b));
+            last_bar = u_empty(s);
+            last_ph = ph;
+            committed = true;
+            if (++s == p.nu) { s = 0; ph ^= 1u; }
+            if (++b == kAcc) { b = 0; bph ^= 1u; }
+          }
+        }
+        if (!ok) {
+          fail(abort, status);
+          volatile int never = 0;
+          if (committed) mbar_sleep(last_bar, last_ph, &never);
         }
       }
-      if (!ok) {
-        fail(abort, status);
-        volatile int never = 0;
-        if (committed) mbar_sleep(last_bar, last_ph, &never);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- TMA: base tiles
+      if (lane == 0) {
+        bool ok = true;
+        int y = y_first;
+        uint32_t yph = y_phase;
+        for (int t = t0; t < t1; ++t) {
+          // two tiles, then V's turn: behind the whole ring's loads it would take microseconds to arrive (4096 x
+          // 3072 -> 3072 at rank 64: 28.7 us a call with the ring first, 26.6 so)
+          if (t - t0 == 2 && nd > 0 && !mbar_sleep(v_ready, vs & 1, abort)) { ok = false; break; }
+          if (tiles_done + t - t0 >= p.nb && !mbar_sleep(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
+          const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
+          if (has_base) {
+            mbar_arrive_expect_tx(y_full(y), kYTile);
+            tma_load_2d(dst, &tmap_base, t * TN, static_cast<int32_t>(m0), y_full(y));
+            tma_load_2d(dst + kYTile / 2, &tmap_base, t * TN + 64, static_cast<int32_t>(m0), y_full(y));
+          } else {
+            mbar_arrive(y_full(y));
+          }
+          if (++y == p.nb) { y = 0; yph ^= 1u; }
+        }
+        if (!ok) {
+          fail(abort, status);
+          grace();
+        }
       }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- TMA: base tiles
-    if (lane == 0) {
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- TMA: U tiles
+      if (lane == 0) {
+        bool ok = true;
+        int s = u_first;
+        int64_t f = products;
+        uint32_t ph = u_phase;
+        for (int t = t0; ok && t < t1; ++t) {
+          for (int i = 0; i < nd; ++i, ++f) {
+            if (f >= p.nu && !mbar_sleep(u_empty(s), ph ^ 1u, abort)) { ok = false; break; }
+            const uint32_t ud = smem_u32(base + s * p.u);
+            mbar_arrive_expect_tx(u_full(s), p.u);
+            tma_load_3d(ud, &tmap_u, t * TN, 0, list[i], u_full(s));
+            tma_load_3d(ud + p.u / 2, &tmap_u, t * TN + 64, 0, list[i], u_full(s));
+            if (++s == p.nu) { s = 0; ph ^= 1u; }
+          }
+        }
+        if (!ok) {
+          fail(abort, status);
+          grace();
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- V, then the epilogue
+      const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
+      griddep_wait();  // V comes from the kernel before this one
+      const int mine = ids[row];
+      if (nd > 0) {
+        // this warp's rows, every other 16 ranks
+        const float sc = mine >= 0 ? __ldg(scale + mine) : 0.f;
+        const float* src = V + (m0 + row) * rank;
+#pragma unroll 2
+        for (int g = half; g < p.rp / 16; g += 2) {
+          float4 f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine >= 0 && 16 * g + 4 * k < rank) f[k] = __ldcg(reinterpret_cast<const float4*>(src + 16 * g + 4 * k));
+          }
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            split_bf16(f[k].x * sc, f[k].y * sc, hi[2 * k], lo[2 * k]);
+            split_bf16(f[k].z * sc, f[k].w * sc, hi[2 * k + 1], lo[2 * k + 1]);
+          }
+          const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(kVCol + 8 * g);
+          tmem_st8(at, hi);
+          tmem_st8(at + static_cast<uint32_t>(p.rp / 2), lo);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(v_ready);
+      }
+      const bool storer = (warp == 2 || warp == 6) && lane == 0;  // of this half's 64 columns
       bool ok = true;
-      int y = 0;
-      uint32_t yph = 0;
-      for (int t = t0; t < t1; ++t) {
-        // two tiles, then V's turn: behind the whole ring's loads it would take microseconds to arrive (4096 x
-        // 3072 -> 3072 at rank 64: 28.7 us a call with the ring first, 26.6 so)
-        if (t - t0 == 2 && nd > 0 && !mbar_sleep(v_ready, 0, abort)) { ok = false; break; }
-        if (t - t0 >= p.nb && !mbar_sleep(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
-        const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
-        if (has_base) {
-          mbar_arrive_expect_tx(y_full(y), kYTile);
-          tma_load_2d(dst, &tmap_base, t * TN, static_cast<int32_t>(m0), y_full(y));
-          tma_load_2d(dst + kYTile / 2, &tmap_base, t * TN + 64, static_cast<int32_t>(m0), y_full(y));
-        } else {
-          mbar_arrive(y_full(y));
+      int y = y_first, b = b_first;
+      uint32_t yph = y_phase, bph = b_phase;
+      for (int t = t0; ok && t < t1; ++t) {
+        uint8_t* box = base + p.off_y + y * kYTile + half * (kYTile / 2);
+        uint8_t* tile = box + row * 128;
+        if (!mbar_sleep_warp(y_full(y), yph, abort)) { ok = false; break; }
+        if (!has_base && mine < 0) {  // no adapter, no base: zeros
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + (c << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        for (int i = 0; i < nd; ++i) {
+          if (!mbar_sleep_warp(acc_full(b), bph, abort)) { ok = false; break; }
+          tc_fence_after();
+          const bool hit = mine == list[i];
+          if (__any_sync(0xffffffffu, hit)) {
+            uint32_t r[2][32];
+            const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * TN + 64 * half);
+            tmem_ld32(src, r[0]);
+            tmem_ld32(src + 32, r[1]);
+            tmem_ld_wait();
+            if (hit) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(tile + ((c ^ (row & 7)) << 4));
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[c >> 2][8 * (c & 3) + e]);
+                if (has_base) {
+                  float bv[8];
+                  widen8(*at, bv);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) v[e] += bv[e];
+                }
+                *at = narrow8(v);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty(b));
+          if (++b == kAcc) { b = 0; bph ^= 1u; }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        named_bar_sync(1 + half, 128);
+        if (storer) {
+          if (t * TN + 64 * half < N) tma_store_2d(&tmap_y, t * TN + 64 * half, static_cast<int32_t>(m0), smem_u32(box));
+          bulk_commit_group();
+          // the box before this one has left its buffer
+          bulk_wait_group_read<1>();
+          if (t > t0) mbar_arrive(y_empty(y ? y - 1 : p.nb - 1));
         }
         if (++y == p.nb) { y = 0; yph ^= 1u; }
       }
-      if (!ok) {
-        fail(abort, status);
-        grace();
+      if (storer && next < end) {
+        bulk_wait_group_read<0>();
+        if (ok) mbar_arrive(y_empty(y ? y - 1 : p.nb - 1));
+      } else if (storer) {
+        bulk_wait_group<0>();
       }
+      if (!ok) fail(abort, status);
     }
-  } else if (warp == 10) {
-    // ---------------------------------------------------------------- TMA: U tiles
-    if (lane == 0) {
-      bool ok = true;
-      int s = 0, f = 0;
-      uint32_t ph = 0;
-      for (int t = t0; ok && t < t1; ++t) {
-        for (int i = 0; i < nd; ++i, ++f) {
-          if (f >= p.nu && !mbar_sleep(u_empty(s), ph ^ 1u, abort)) { ok = false; break; }
-          const uint32_t ud = smem_u32(base + s * p.u);
-          mbar_arrive_expect_tx(u_full(s), p.u);
-          tma_load_3d(ud, &tmap_u, t * TN, 0, list[i], u_full(s));
-          tma_load_3d(ud + p.u / 2, &tmap_u, t * TN + 64, 0, list[i], u_full(s));
-          if (++s == p.nu) { s = 0; ph ^= 1u; }
-        }
-      }
-      if (!ok) {
-        fail(abort, status);
-        grace();
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- V, then the epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
-    griddep_wait();  // V comes from the kernel before this one
-    const int mine = ids[row];
-    if (nd > 0) {
-      // this warp's rows, every other 16 ranks
-      const float sc = mine >= 0 ? __ldg(scale + mine) : 0.f;
-      const float* src = V + (m0 + row) * rank;
-#pragma unroll 2
-      for (int g = half; g < p.rp / 16; g += 2) {
-        float4 f[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (mine >= 0 && 16 * g + 4 * k < rank) f[k] = __ldcg(reinterpret_cast<const float4*>(src + 16 * g + 4 * k));
-        }
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          split_bf16(f[k].x * sc, f[k].y * sc, hi[2 * k], lo[2 * k]);
-          split_bf16(f[k].z * sc, f[k].w * sc, hi[2 * k + 1], lo[2 * k + 1]);
-        }
-        const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(kVCol + 8 * g);
-        tmem_st8(at, hi);
-        tmem_st8(at + static_cast<uint32_t>(p.rp / 2), lo);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(v_ready);
-    }
-    const bool storer = (warp == 2 || warp == 6) && lane == 0;  // of this half's 64 columns
-    bool ok = true;
-    int y = 0, b = 0;
-    uint32_t yph = 0, bph = 0;
-    for (int t = t0; ok && t < t1; ++t) {
-      uint8_t* box = base + p.off_y + y * kYTile + half * (kYTile / 2);
-      uint8_t* tile = box + row * 128;
-      if (!mbar_sleep_warp(y_full(y), yph, abort)) { ok = false; break; }
-      if (!has_base && mine < 0) {  // no adapter, no base: zeros
-        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + (c << 4)) = make_uint4(0, 0, 0, 0);
-      }
-      for (int i = 0; i < nd; ++i) {
-        if (!mbar_sleep_warp(acc_full(b), bph, abort)) { ok = false; break; }
-        tc_fence_after();
-        const bool hit = mine == list[i];
-        if (__any_sync(0xffffffffu, hit)) {
-          uint32_t r[2][32];
-          const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * TN + 64 * half);
-          tmem_ld32(src, r[0]);
-          tmem_ld32(src + 32, r[1]);
-          tmem_ld_wait();
-          if (hit) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(tile + ((c ^ (row & 7)) << 4));
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[c >> 2][8 * (c & 3) + e]);
-              if (has_base) {
-                float bv[8];
-                widen8(*at, bv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += bv[e];
-              }
-              *at = narrow8(v);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(b));
-        if (++b == kAcc) { b = 0; bph ^= 1u; }
-      }
-      if (!ok) break;
-      fence_proxy_async_smem();
-      named_bar_sync(1 + half, 128);
-      if (storer) {
-        if (t * TN + 64 * half < N) tma_store_2d(&tmap_y, t * TN + 64 * half, static_cast<int32_t>(m0), smem_u32(box));
-        bulk_commit_group();
-        // the box before this one has left its buffer
-        bulk_wait_group_read<1>();
-        if (t > t0) mbar_arrive(y_empty(y ? y - 1 : p.nb - 1));
-      }
-      if (++y == p.nb) { y = 0; yph ^= 1u; }
-    }
-    if (storer) bulk_wait_group<0>();
-    if (!ok) fail(abort, status);
+    tiles_done += t1 - t0;
+    products += static_cast<int64_t>(nd) * (t1 - t0);
+    vs += nd > 0;
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();  // the tile's list and V have been read
+    tc_fence_after();
+    if (*abort) break;
   }
 
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1075,30 +1100,32 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
     return CR_ERR_CUDA;
   const int64_t tiles_m = (static_cast<int64_t>(M) + TM - 1) / TM;
   const int tiles_n = (N + TN - 1) / TN;
-  // column parts of a token tile: the fewest rounds of (column tiles + about two tiles' worth of prologue)
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
+  // the same number of column parts of every token tile, or all tiles dealt out evenly: by rounds of (column tiles +
+  // about two tiles' worth of prologue for each token tile that a CTA meets)
+  int64_t ctas = 0, best_cost = INT64_MAX;
   for (int s = 1; s <= tiles_n && s <= 4 * num_sms; ++s) {
     const int64_t cost = (tiles_m * s + num_sms - 1) / num_sms * ((tiles_n + s - 1) / s + 2);
     if (cost < best_cost) {
       best_cost = cost;
-      best = s;
+      ctas = tiles_m * s;
     }
   }
+  const int64_t share = (tiles_m * tiles_n + num_sms - 1) / num_sms;
+  if (share + 2 * ((share + tiles_n - 1) / tiles_n + 1) < best_cost) ctas = num_sms;
   // a programmatic dependent of the v kernel: it starts, loads base and U while that one ends, and waits for
   // it on the device before it reads V
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles_m * best), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(kYMmaThreads, 1, 1);
   cfg.dynamicSmemBytes = p.smem + 1024;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, lora_y_mma_kernel, tu, tb, ty, V, adapter, scale, static_cast<int>(base != nullptr), M,
-                            N, rank, L, best, status) == cudaSuccess
+                            N, rank, L, status) == cudaSuccess
              ? CR_OK
              : CR_ERR_CUDA;
 }
