@@ -638,8 +638,8 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
 // tokens the partial sums' way through memory and a kernel more cost as much as the product (1 token, 14 adapters
 // of rank 64, 1024 -> 4296: 32 us a backward pass with them, 21 without).
 // By itself it takes 17.6 us for 4096 x (3072 + 3072) at rank 64 (52 MB: 3.0 TB/s; start, first tiles and sums are
-// half of it) and 54 us for 8192 x (12288 codes + 3072 bf16) at rank 32 (154 MB: 2.8 TB/s), bound by the codes'
-// way through the ALUs (56 % of the issue slots).
+// half of it) and 54 us for 8192 x (12288 codes + 3072 bf16) at rank 32 (154 MB: 2.8 TB/s), bound by shared memory:
+// of 1145 cycles for a tile of codes about 900 are its bytes' (16 KB in and out, 32 KB as bf16 in and out, V).
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int GM = 64;           // tokens of a tile
