@@ -459,7 +459,13 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  * aligned; none of it needs to be zero before: the call writes its status word
  * (the first 16 bytes, read with cr_read_device_status) itself.  The forward
  * call of few rows needs none (its size call returns 0) and may be given NULL;
- * it has no device-side waits to report on.
+ * it has no device-side waits to report on.  A workspace serves one call at a
+ * time: calls on different streams, and graphs that may run at the same time,
+ * need one each.
+ *
+ * These calls and the three below start on the device beside the end of the
+ * stream's work before them, and wait there for its results: the order of the
+ * stream holds as for any other call.
  */
 #define CR_MAX_RANK 128
 #define CR_MAX_ADAPTERS 4096
@@ -496,14 +502,15 @@ cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, voi
  * cr_w4a4_grad_input -- input gradient of the W4A4 layer with its weights
  * frozen (the quantisation of X taken as the identity):
  *   dX = dY W^,   W^[n, :] = w_scale[n] * (q[n, :] H_group)
- * with float32 sums, rounded once to bf16.  For many tokens (more than 256, or
- * 512 if N > K) W^ is rounded to bf16 before the product.  The same Wq and
- * w_scale as the forward calls (either scale mode).
+ * with float32 sums, rounded once to bf16.  One operand of the product is
+ * rounded to bf16 before it: W^, or, where there are few tokens for that many
+ * weights, w_scale[n] dY[:, n] (the codes are exact then; W^ is never made).
+ * The same Wq and w_scale as the forward calls (either scale mode).
  *   dY  bf16 [M, N], row stride lddy >= N;  dX  out: bf16 [M, K], row stride lddx >= K
  * Shape and alignment rules as cr_w4a4_linear, lddy and lddx % 8 == 0,
  * N <= CR_MAX_K; N == 0 writes zeros.  The workspace holds the bf16 weights
- * (2 N K bytes; for fewer tokens partial sums instead) during the call;
- * none of it needs to be zero before.
+ * (2 N K bytes; for few tokens the operand and partial sums instead) during the
+ * call; none of it needs to be zero before.
  */
 size_t cr_w4a4_grad_input_workspace_size(int M, int N, int K, int group);
 cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const float* w_scale,
