@@ -102,9 +102,20 @@ def ckpt_values(codes, scales):
 
 
 def grad_input(dy, wq_packed, w_scale, group: int = 256):
-    """(dX, bound): each weight rounded to bfloat16 once, float32 sums, one rounding."""
+    """(dX, bound): one operand of each product rounded to bfloat16 once, float32 sums, one rounding.
+
+    Either the weight is rounded, or w_scale[n] dY[m, n], whose relative error all columns k share, so that the
+    rotation of the sums carries it to |dY[m, n]| |W^[n, k]|, too.  The float32 sums are taken of the weights, or
+    of the codes and rotated then (at most 16 roundings one after the other): errors of theirs spread over the
+    group by the rotation's magnitudes, which are at least those of the weights.
+    """
     q = unpack_int4(wq_packed).astype(np.float64)
-    w = rotate64(q, group) * np.asarray(w_scale, np.float64)[:, None]
+    s = np.asarray(w_scale, np.float64)
+    w = rotate64(q, group) * s[:, None]
     dx = dy @ w
     mags = np.abs(dy) @ np.abs(w)
-    return dx, (BF16 + 2.0 ** -22 + steps(dy.shape[1])) * mags * (1 + BF16) + BF16 * np.abs(dx)
+    p = np.abs(dy) @ (np.abs(q) * s[:, None])
+    h = np.abs(np.asarray(regular_hadamard(group), np.float64))
+    spread = (p.reshape(p.shape[0], -1, group) @ h).reshape(p.shape)
+    e = (BF16 + 2.0 ** -22) * mags + (steps(dy.shape[1]) + 2.0 ** -20) * spread
+    return dx, e * (1 + BF16) + BF16 * np.abs(dx)

@@ -62,7 +62,7 @@ __device__ __forceinline__ void put8(Pairs& P, int k, const float2 (&v)[4]) {
 }
 
 // Packed INT4 weights to bf16 values in the unrotated basis.  Rounding the weights once to bf16 lets the
-// product run on bf16 operands; each is off by at most 2^-9 of itself, the same half step that rounding
+// product run on bf16 operands; each is off by at most 2^-8 of itself, the same half step that rounding
 // the result costs.
 template <int kDig>
 __global__ void __launch_bounds__(32 * kWarps)
