@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
 // all column tiles: read from shared memory it would cost as many bytes there as U does, and at rank 128
 // those bytes, not memory's, set the pace (134 us against 110 us for 8192 x 12288).
 // Column tiles are dealt out over the CTAs token tile by token tile; where that does not come out even a CTA goes on
-// to the next token tile, with that one's V.  8192 tokens, 3072 -> 12288 at rank 128 with four adapters take 117 us
+// to the next token tile, with that one's V.  8192 tokens, 3072 -> 12288 at rank 128 with four adapters took 117 us
 // a call that way and 123 in two equal parts of each token tile, which leave 20 SMs idle.
 // By itself the kernel takes 72 us for 8192 -> 12288 at rank 32 (402 MB of base and result: 5.6 TB/s); at rank 128
 // with four adapters memory waits for the products of the tiles that hold two adapters' rows (101 us: 4 TB/s).
@@ -359,17 +359,28 @@ constexpr int kYMmaThreads = 352;
 
 __global__ void __launch_bounds__(kYMmaThreads, 1)
     lora_y_mma_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_base,
-                      const __grid_constant__ CUtensorMap tmap_y, const float* __restrict__ V,
-                      const int32_t* __restrict__ adapter, const float* __restrict__ scale, int has_base, int M, int N,
-                      int rank, int L, int* __restrict__ status) {
+                      const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_v,
+                      const float* __restrict__ V, const int32_t* __restrict__ adapter, const float* __restrict__ scale, int has_base,
+                      int M, int N, int rank, int L, int parts, int* __restrict__ status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align_smem(smem_raw);
   const YPlan p = y_plan(rank);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this CTA's share of all tiles, token tile by token tile
+  // this CTA's share of the tiles: one of `parts` of a token tile, or (0) an even one of all, token tile by token tile
   const int tiles = (N + TN - 1) / TN;
-  const int64_t all = (static_cast<int64_t>(M) + TM - 1) / TM * tiles;
-  const int64_t begin = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
+  int mt, t0, left;  // `left` tiles from column tile t0 of token tile mt on
+  if (parts) {
+    const int part = blockIdx.x % parts, each = tiles / parts, more = tiles % parts;
+    mt = blockIdx.x / parts;
+    t0 = part * each + min(part, more);
+    left = each + (part < more);
+  } else {
+    const int64_t all = (static_cast<int64_t>(M) + TM - 1) / TM * tiles;
+    const int64_t begin = all * blockIdx.x / gridDim.x;
+    mt = static_cast<int>(begin / tiles);
+    t0 = static_cast<int>(begin % tiles);
+    left = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x - begin);
+  }
   int* ids = reinterpret_cast<int*>(base + p.off_list);
   int* list = ids + TM;
   const uint32_t bars = smem_u32(base + p.off_bar);
@@ -383,6 +394,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 200);
   volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 204);
   int* counts = reinterpret_cast<int*>(base + p.off_bar + 208);
+  const uint32_t v_in = bars + 224u;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nb; ++s) {
@@ -398,6 +410,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       mbar_init(acc_empty(b), 8);
     }
     mbar_init(v_ready, 256);
+    mbar_init(v_in, 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -405,6 +418,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
     prefetch_tmap(&tmap_u);
     if (has_base) prefetch_tmap(&tmap_base);
     prefetch_tmap(&tmap_y);
+    prefetch_tmap(&tmap_v);
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(slot), 512);
@@ -415,19 +429,19 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  // what the rings have gone through so far: tiles, products, times that V was made
-  int64_t tiles_done = 0, products = 0;
-  uint32_t vs = 0;
-  // the part in one token tile after the other; `next` is where the one after begins
-  for (int64_t pos = begin, next; pos < end; pos = next) {
-    const int64_t m0 = pos / tiles * TM;
-    const int t0 = static_cast<int>(pos % tiles);
-    const int t1 = end - pos < tiles - t0 ? t0 + static_cast<int>(end - pos) : tiles;
-    next = pos + t1 - t0;
+  // where the rings stand: next slots and their phases; tiles and products so far (the latter while it matters)
+  int tiles_done = 0, products = 0, y_first = 0, u_first = 0, b_first = 0;
+  uint32_t y_phase = 0, u_phase = 0, b_phase = 0, vs = 0;  // vs: times that V was made
+  for (; left > 0; ++mt, t0 = 0) {
+    const int64_t m0 = static_cast<int64_t>(mt) * TM;
+    const int t1 = left < tiles - t0 ? t0 + left : tiles;
+    left -= t1 - t0;
     const int nd = tile_adapters(adapter, m0, M, L, ids, list, counts, kYMmaThreads);
-    const int y_first = static_cast<int>(tiles_done % p.nb), u_first = static_cast<int>(products % p.nu),
-              b_first = static_cast<int>(products % kAcc);
-    const uint32_t y_phase = tiles_done / p.nb & 1, u_phase = products / p.nu & 1, b_phase = products / kAcc & 1;
+    // V of a tile comes by TMA at more than 32 ranks, by way of the buffers that the base reaches last, 32 ranks of
+    // the rows at a time: each thread loading its row is 32 half-used sectors a load (us a call by TMA | by threads:
+    // rank 128, 8192 x 12288 113 | 117, rank 64, 4096 x 3072 23.2 | 24.4, rank 8 backward, 777 x 512 15.5 | 14.4)
+    const bool v_tma = rank > 32;
+    auto v_box = [&](int i) { return base + p.off_y + (y_first + 2 + (i >> 1)) % p.nb * kYTile + (i & 1) * (kYTile / 2); };
 
     if (warp == 0) {
       // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -474,10 +488,20 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
         bool ok = true;
         int y = y_first;
         uint32_t yph = y_phase;
+        auto load_v = [&] {
+          griddep_wait();  // it comes from the kernel before this one
+          const int boxes = (rank + 31) / 32;
+          mbar_arrive_expect_tx(v_in, static_cast<uint32_t>(boxes) * (kYTile / 2));
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(smem_u32(v_box(i)), &tmap_v, 32 * i, static_cast<int32_t>(m0), v_in);
+        };
         for (int t = t0; t < t1; ++t) {
           // two tiles, then V's turn: behind the whole ring's loads it would take microseconds to arrive (4096 x
           // 3072 -> 3072 at rank 64: 28.7 us a call with the ring first, 26.6 so)
-          if (t - t0 == 2 && nd > 0 && !mbar_sleep(v_ready, vs & 1, abort)) { ok = false; break; }
+          if (t - t0 == 2 && nd > 0) {
+            if (v_tma) load_v();
+            if (!mbar_sleep(v_ready, vs & 1, abort)) { ok = false; break; }
+          }
           if (tiles_done + t - t0 >= p.nb && !mbar_sleep(y_empty(y), yph ^ 1u, abort)) { ok = false; break; }
           const uint32_t dst = smem_u32(base + p.off_y + y * kYTile);
           if (has_base) {
@@ -489,6 +513,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
           }
           if (++y == p.nb) { y = 0; yph ^= 1u; }
         }
+        if (ok && v_tma && t1 - t0 <= 2 && nd > 0) load_v();
         if (!ok) {
           fail(abort, status);
           grace();
@@ -498,8 +523,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       // ---------------------------------------------------------------- TMA: U tiles
       if (lane == 0) {
         bool ok = true;
-        int s = u_first;
-        int64_t f = products;
+        int s = u_first, f = products;
         uint32_t ph = u_phase;
         for (int t = t0; ok && t < t1; ++t) {
           for (int i = 0; i < nd; ++i, ++f) {
@@ -521,18 +545,11 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
       griddep_wait();  // V comes from the kernel before this one
       const int mine = ids[row];
-      if (nd > 0) {
+      bool ok = nd == 0 || !v_tma || mbar_sleep_warp(v_in, vs & 1, abort);
+      if (ok && nd > 0) {
         // this warp's rows, every other 16 ranks
         const float sc = mine >= 0 ? __ldg(scale + mine) : 0.f;
-        const float* src = V + (m0 + row) * rank;
-#pragma unroll 2
-        for (int g = half; g < p.rp / 16; g += 2) {
-          float4 f[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine >= 0 && 16 * g + 4 * k < rank) f[k] = __ldcg(reinterpret_cast<const float4*>(src + 16 * g + 4 * k));
-          }
+        auto put = [&](int g, const float4 (&f)[4]) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -542,13 +559,34 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
           const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(kVCol + 8 * g);
           tmem_st8(at, hi);
           tmem_st8(at + static_cast<uint32_t>(p.rp / 2), lo);
+        };
+        if (v_tma) {
+          for (int g = half; g < p.rp / 16; g += 2) {
+            const uint8_t* src = v_box(g >> 1) + row * 128;
+            float4 f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[k] = *reinterpret_cast<const float4*>(src + (((4 * (g & 1) + k) ^ (row & 7)) << 4));
+              if (mine < 0) f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            put(g, f);
+          }
+          fence_proxy_async_smem();  // the base's next tiles come where V was
+        } else if (half < p.rp / 16) {
+          const float* src = V + (m0 + row) * rank + 16 * half;
+          float4 f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine >= 0 && 16 * half + 4 * k < rank) f[k] = __ldcg(reinterpret_cast<const float4*>(src + 4 * k));
+          }
+          put(half, f);
         }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(v_ready);
       }
       const bool storer = (warp == 2 || warp == 6) && lane == 0;  // of this half's 64 columns
-      bool ok = true;
       int y = y_first, b = b_first;
       uint32_t yph = y_phase, bph = b_phase;
       for (int t = t0; ok && t < t1; ++t) {
@@ -602,7 +640,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
         }
         if (++y == p.nb) { y = 0; yph ^= 1u; }
       }
-      if (storer && next < end) {
+      if (storer && left > 0) {
         bulk_wait_group_read<0>();
         if (ok) mbar_arrive(y_empty(y ? y - 1 : p.nb - 1));
       } else if (storer) {
@@ -610,14 +648,23 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       }
       if (!ok) fail(abort, status);
     }
-    tiles_done += t1 - t0;
-    products += static_cast<int64_t>(nd) * (t1 - t0);
-    vs += nd > 0;
     __syncwarp();
     tc_fence_before();
     __syncthreads();  // the tile's list and V have been read
     tc_fence_after();
-    if (*abort) break;
+    if (left == 0 || *abort) break;
+    const int n = t1 - t0;
+    auto advance = [](int& slot, uint32_t& phase, int by, int slots) {
+      slot += by;
+      phase ^= slot / slots & 1;
+      slot %= slots;
+    };
+    advance(y_first, y_phase, n, p.nb);
+    advance(u_first, u_phase, nd * n, p.nu);
+    advance(b_first, b_phase, nd * n, kAcc);
+    tiles_done += n;
+    products = min(products + nd * n, p.nu);
+    vs += nd > 0;
   }
 
   if (warp == 0) {
@@ -1092,9 +1139,10 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
                       int* status, int num_sms, cudaStream_t stream) {
   if (!set_attrs()) return CR_ERR_CUDA;
   const YPlan p = y_plan(rank);
-  CUtensorMap tu, tb, ty;
+  CUtensorMap tu, tb, ty, tv;
   memset(&tb, 0, sizeof(tb));
-  if (!make_tmap_3d(&tu, kBf, up, L, rank, N, static_cast<uint64_t>(N) * 2, 64, p.rp, kSw128, kL2) ||
+  if (!make_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, V, M, rank, static_cast<uint64_t>(rank) * 4, 32, TM, kSw128, kL2) ||
+      !make_tmap_3d(&tu, kBf, up, L, rank, N, static_cast<uint64_t>(N) * 2, 64, p.rp, kSw128, kL2) ||
       !make_tmap_2d(&ty, kBf, Y, M, N, static_cast<uint64_t>(ldy) * 2, 64, TM, kSw128, CU_TENSOR_MAP_L2_PROMOTION_NONE) ||
       (base && !make_tmap_2d(&tb, kBf, base, M, N, static_cast<uint64_t>(ldb) * 2, 64, TM, kSw128, kL2)))
     return CR_ERR_CUDA;
@@ -1102,16 +1150,18 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
   const int tiles_n = (N + TN - 1) / TN;
   // the same number of column parts of every token tile, or all tiles dealt out evenly: by rounds of (column tiles +
   // about two tiles' worth of prologue for each token tile that a CTA meets)
-  int64_t ctas = 0, best_cost = INT64_MAX;
+  int parts = 1;
+  int64_t best_cost = INT64_MAX;
   for (int s = 1; s <= tiles_n && s <= 4 * num_sms; ++s) {
     const int64_t cost = (tiles_m * s + num_sms - 1) / num_sms * ((tiles_n + s - 1) / s + 2);
     if (cost < best_cost) {
       best_cost = cost;
-      ctas = tiles_m * s;
+      parts = s;
     }
   }
   const int64_t share = (tiles_m * tiles_n + num_sms - 1) / num_sms;
-  if (share + 2 * ((share + tiles_n - 1) / tiles_n + 1) < best_cost) ctas = num_sms;
+  if (share + 2 * ((share + tiles_n - 1) / tiles_n + 1) < best_cost) parts = 0;
+  const int64_t ctas = parts ? tiles_m * parts : num_sms;
   // a programmatic dependent of the v kernel: it starts, loads base and U while that one ends, and waits for
   // it on the device before it reads V
   cudaLaunchConfig_t cfg = {};
@@ -1124,8 +1174,8 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_y_mma_kernel, tu, tb, ty, V, adapter, scale, static_cast<int>(base != nullptr), M,
-                            N, rank, L, status) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, lora_y_mma_kernel, tu, tb, ty, tv, V, adapter, scale, static_cast<int>(base != nullptr), M,
+                            N, rank, L, parts, status) == cudaSuccess
              ? CR_OK
              : CR_ERR_CUDA;
 }
