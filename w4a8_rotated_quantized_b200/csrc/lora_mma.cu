@@ -160,8 +160,21 @@ __global__ void __launch_bounds__(kVThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 148);
   int* counts = reinterpret_cast<int*>(base + p.off_bar + 160);
 
+  const int nkb = (K + KB - 1) / KB;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * split / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
+  // `c` adapters' rows of A beside the block of X
+  auto load = [&](int stage, int s, int kb, const int* which, int c) {
+    const uint32_t dst = smem_u32(base + s * stage);
+    mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(TM + c * p.rp) * 128u);
+    tma_load_2d(dst, &tmap_x, kb * KB, static_cast<int32_t>(m0), full(s));
+    for (int i = 0; i < c; ++i)
+      tma_load_3d(dst + TM * 128 + i * p.rp * 128, &tmap_a, kb * KB, 0, which ? which[i] : 0, full(s));
+  };
+
   cluster_arrive();  // this CTA has started: its shared memory may be written to
-  if (threadIdx.x == 0) {
+  int asked = 0;     // loads on their way before the block is set up
+  if (warp == 1 && lane == 0) {
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -170,10 +183,16 @@ __global__ void __launch_bounds__(kVThreads, 1)
     mbar_init(acc_empty, 4);
     *abort = 0;
     fence_mbar_init();
-  }
-  if (warp == 1 && lane == 0) {
-    prefetch_tmap(&tmap_x);
-    prefetch_tmap(&tmap_a);
+    fence_proxy_async_smem();
+    griddep_wait();
+    if (!adapter) {  // nothing to look up first
+      const int stage = (TM + p.rp) * 128;
+      const int stages = p.ring / stage < kVStages ? p.ring / stage : kVStages;
+      for (; asked < stages && kb0 + asked < kb1; ++asked) load(stage, asked, kb0 + asked, nullptr, 1);
+    } else {
+      prefetch_tmap(&tmap_x);
+      prefetch_tmap(&tmap_a);
+    }
   }
   griddep_wait();  // for what the stream ran before
   if (warp == 0) {
@@ -194,9 +213,6 @@ __global__ void __launch_bounds__(kVThreads, 1)
   const int stage = (TM + (nd < p.cap ? nd : p.cap) * p.rp) * 128;
   const int stages = p.ring / stage < kVStages ? p.ring / stage : kVStages;
   const int rows = TM / splits;  // that this CTA adds up
-  const int nkb = (K + KB - 1) / KB;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * split / splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- MMA issuer (one thread)
@@ -214,7 +230,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
           tc_fence_after();
           const uint64_t da = sw128_kmajor_desc(smem_u32(base + s * stage));
           const uint64_t db = sw128_kmajor_desc(smem_u32(base + s * stage + TM * 128));
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < KB / 16; ++kk)
             umma_f16_ss(tmem, da + 2u * kk, db + 2u * kk, idesc, (kb != kb0 || kk) ? 1u : 0u);
           umma_commit(empty(s));
@@ -241,11 +257,7 @@ __global__ void __launch_bounds__(kVThreads, 1)
         const int c = nd - d0 < p.cap ? nd - d0 : p.cap;
         for (int kb = kb0; kb < kb1; ++kb, ++f) {
           if (f >= stages && !mbar_sleep(empty(s), ph ^ 1u, abort)) { ok = false; break; }
-          const uint32_t dst = smem_u32(base + s * stage);
-          mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(TM + c * p.rp) * 128u);
-          tma_load_2d(dst, &tmap_x, kb * KB, static_cast<int32_t>(m0), full(s));
-          for (int i = 0; i < c; ++i)
-            tma_load_3d(dst + TM * 128 + i * p.rp * 128, &tmap_a, kb * KB, 0, list[d0 + i], full(s));
+          if (f >= asked) load(stage, s, kb, list + d0, c);
           if (++s == stages) { s = 0; ph ^= 1u; }
         }
       }
