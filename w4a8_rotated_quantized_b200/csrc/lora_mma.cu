@@ -777,7 +777,22 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   uint32_t* slot = reinterpret_cast<uint32_t*>(base + p.off_bar + 136);
   volatile int* abort = reinterpret_cast<volatile int*>(base + p.off_bar + 140);
 
-  if (threadIdx.x == 0) {
+  const bool plain = !adapter && a == 0;  // every row of every tile
+  const int ring = kCodes ? kRaws : p.stages;
+  auto load = [&](int s, int i) {
+    const int y = (t0 + i) * GM;
+    if constexpr (kCodes) {
+      mbar_arrive_expect_tx(z_full(s), kRawTile);
+      tma_load_2d(smem_u32(base + p.off_raw + s * kRawTile), &tmap_z, c0, y, z_full(s));
+    } else {
+      const uint32_t z = smem_u32(base + s * p.stage);
+      mbar_arrive_expect_tx(z_full(s), kZTile);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tma_load_2d(z + b * kZBox, &tmap_z, c0 + 64 * b, y, z_full(s));
+    }
+  };
+  int asked = 0;  // tiles on their way before the block is set up: without indices none has to be looked up
+  if (warp == kGWarps + 1 && lane == 0) {
     for (int s = 0; s < 4; ++s) {
       mbar_init(z_full(s), 1);
       mbar_init(raw_empty(s), kGSet);
@@ -787,15 +802,19 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     mbar_init(acc_full, 1);
     *abort = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    if (plain)
+      for (; asked < ring && asked < nt; ++asked) load(asked, asked);
+    else
+      prefetch_tmap(&tmap_z);
   }
-  if (warp == kGWarps + 1 && lane == 0) prefetch_tmap(&tmap_z);
   if (warp == kGWarps) {
     tmem_alloc(smem_u32(slot), p.cols);
     tmem_relinquish();
     if (lane == 0) griddep_launch_dependents();
   }
   // the rows of this CTA's token tiles that name its adapter
-  for (int t = warp; t < nt; t += kGThreads / 32) {
+  for (int t = warp; !plain && t < nt; t += kGThreads / 32) {
     const int64_t m = static_cast<int64_t>(t0 + t) * GM + lane;
     const uint32_t lo = __ballot_sync(0xffffffffu, m < M && row_adapter(adapter, m, L) == a);
     const uint32_t hi = __ballot_sync(0xffffffffu, m + 32 < M && row_adapter(adapter, m + 32, L) == a);
@@ -806,7 +825,6 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   tc_fence_after();
   const uint32_t tmem = *slot;
   // first tile at or after i with such a row, nt if none
-  const bool plain = !adapter && a == 0;  // every row of every tile
   auto next_tile = [&](int i) {
     if (!plain)
       while (i < nt && mask[i] == 0) ++i;
@@ -852,19 +870,9 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
       bool ok = true;
       int s = 0, f = 0;
       uint32_t ph = 0;
-      const int ring = kCodes ? kRaws : p.stages;
       for (int i = next_tile(0); i < nt; i = next_tile(i + 1), ++f) {
         if (f >= ring && !mbar_sleep(kCodes ? raw_empty(s) : empty(s), ph ^ 1u, abort)) { ok = false; break; }
-        const int y = (t0 + i) * GM;
-        if constexpr (kCodes) {
-          mbar_arrive_expect_tx(z_full(s), kRawTile);
-          tma_load_2d(smem_u32(base + p.off_raw + s * kRawTile), &tmap_z, c0, y, z_full(s));
-        } else {
-          const uint32_t z = smem_u32(base + s * p.stage);
-          mbar_arrive_expect_tx(z_full(s), kZTile);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_2d(z + b * kZBox, &tmap_z, c0 + 64 * b, y, z_full(s));
-        }
+        if (f >= asked) load(s, i);
         if (++s == ring) { s = 0; ph ^= 1u; }
       }
       if (!ok) {
