@@ -383,7 +383,7 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
              : group == 256 ? grad_input_finish_kernel<4>
                             : grad_input_finish_kernel<5>;
   cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.dynamicSmemBytes = 0;
   const float* sums = P;
   return cudaLaunchKernelEx(&cfg, fin, sums, splits, stride, dX, lddx, units, K / 256) == cudaSuccess ? CR_OK
