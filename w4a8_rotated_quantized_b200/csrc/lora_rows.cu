@@ -9,12 +9,12 @@
 // A row has a cluster of 16 CTAs (fewer when there are more rows).  Each multiplies its part of the row by the
 // rank rows of A and sends the partial sums to all the others, which add them in order; then each makes its part
 // of the columns.  What costs time here is latency: a token's factors are a few hundred KB.  So each warp has
-// eight loads on their way whatever the rank (its tasks are pairs of a rank and 256 columns, not ranks), the
+// four loads on their way whatever the rank (its tasks are pairs of a rank and 256 columns, not ranks), the
 // ranks of a column are shared out between the threads that columns leave idle, their first U and the base are
 // on their way before the first product, and the only other wait is one barrier of the cluster.  One token of
-// rank 16, 2560 -> 9728, takes 5.1 us, 64 tokens of 48 adapters 9.3 (21.7 MB: 2.3 TB/s; two dependent rounds of
-// loads and the cluster's exchange, not bandwidth).  Asking L2 for the rest of U before the first product made the
-// latter 10.5.
+// rank 16, 2560 -> 9728, takes 4.1 us, 64 tokens of 48 adapters 7.1 (21.7 MB: 3.1 TB/s; two dependent rounds of
+// loads and the cluster's exchange, not bandwidth).  Asking L2 for the rest of U before the first product took
+// longer.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,8 +33,11 @@ namespace {
 constexpr int kMostCluster = 16;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;     // ranks of U that a thread has on their way from the start
-constexpr int kTasks = 8;     // loads of A that a warp has on their way
+constexpr int kAhead = 1;     // ranks of U that a thread has on their way from the start
+constexpr int kTasks = 4;     // loads of A that a warp has on their way
+// More of either, or of U in the second product, does not fit 64 registers a thread, two CTAs an SM, and costs more
+// in spills than it hides: 64 rows of 48 adapters take 7.1 us so, 8.7 with two ranks ahead, 8.5 with eight tasks, 10.1
+// with four and eight; one row 4.1 and 5.1.
 constexpr int kMostPasses = CR_MAX_K / 256 / 4;  // 256 columns at a time: of a CTA in a cluster of 4 (2: half the K)
 
 __device__ __forceinline__ void st_shared_cluster_f1(uint32_t cluster_addr, float v) {
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (brow) {
       b = ldcg16(brow + 8 * (p0 + p));
     }
-#pragma unroll 8
+#pragma unroll 4
     for (int j = group + (first ? groups * kAhead : 0); j < rank; j += groups) {
       float uv[8];
       widen8(ldcg16(u + static_cast<int64_t>(j) * N + 8 * p), uv);
@@ -192,19 +195,19 @@ std::atomic<bool> g_attr_done[64];
 }  // namespace
 
 // By microseconds, fitted to both forms' times for 260 calls of 1 to 1400 rows, 256 to 10240 columns, ranks 4 to
-// 128 and pools of 1 to 48 adapters: the choice costs 0.4 % over the better form on average and 27 % at worst.
-// The row form costs 4.6, a row's CTAs a fortieth, and each row's own factors come at 8.6 TB/s (L2).  The batch
-// form costs 8.3, its first adapter's factors at 0.4 TB/s, the rows' values, and for every further adapter that
-// may occur among a tile's rows 0.44 and its factors at 1.4 TB/s.
-//   693 rows, rank 8, 1672 -> 616, one adapter:     rows 31, batch 9
-//   130 rows, rank 4, 328 -> 4200, 24 adapters:     rows 6, batch 26
-//   154 rows, rank 32, 1712 -> 6464, 11 adapters:   rows 14, batch 17 (the worst choice)
+// 128 and pools of 1 to 48 adapters: the choice costs 0.4 % over the better form on average and 52 % at worst.
+// The row form costs 3.8, a row's CTAs a fiftieth, and each row's own factors come at 8.6 TB/s (L2).  The batch
+// form costs 8.3, its first adapter's factors at 0.35 TB/s, the rows' values, and for every further adapter that
+// may occur among a tile's rows 0.45 and its factors at 1.4 TB/s.
+//   960 rows, rank 16, 1488 -> 1272, 43 adapters:   rows 33, batch 13
+//   336 rows, rank 4, 584 -> 416, 7 adapters:       rows 10, batch 9
+//   34 rows, rank 64, 4112 -> 5400, one adapter:    rows 14, batch 9 (the worst choice)
 bool use_lora_rows(int M, int N, int K, int rank, int L) {
   if (M > 1024) return false;
   const double columns = static_cast<double>(K) + N, factors = 2.0 * rank * columns;
   const int most = L < M ? (L < 128 ? L : 128) : (M < 128 ? M : 128);
-  const double rows = 4.6 + M / 40.0 + M * factors / 8.6e6;
-  const double batch = 8.3 + factors / 4e5 + M * columns / 1.7e6 + (most - 1) * (0.44 + factors / 1.4e6);
+  const double rows = 3.8 + M / 50.0 + M * factors / 8.6e6;
+  const double batch = 8.3 + factors / 3.5e5 + M * columns / 1.7e6 + (most - 1) * (0.45 + factors / 1.4e6);
   return rows < batch;
 }
 
