@@ -340,10 +340,9 @@ __global__ void __launch_bounds__(kVThreads, 1)
 // all column tiles: read from shared memory it would cost as many bytes there as U does, and at rank 128
 // those bytes, not memory's, set the pace (134 us against 110 us for 8192 x 12288).
 // Column tiles are dealt out over the CTAs token tile by token tile; where that does not come out even a CTA goes on
-// to the next token tile, with that one's V.  8192 tokens, 3072 -> 12288 at rank 128 with four adapters took 117 us
-// a call that way and 123 in two equal parts of each token tile, which leave 20 SMs idle.
+// to the next token tile, with that one's V.
 // By itself the kernel takes 72 us for 8192 -> 12288 at rank 32 (402 MB of base and result: 5.6 TB/s); at rank 128
-// with four adapters memory waits for the products of the tiles that hold two adapters' rows (101 us: 4 TB/s).
+// with four adapters memory waits for the products of the tiles that hold two adapters' rows (97 us: 4.1 TB/s).
 // ---------------------------------------------------------------------------------------------------
 
 constexpr int TN = 128;
@@ -1169,7 +1168,10 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
   const int64_t tiles_m = (static_cast<int64_t>(M) + TM - 1) / TM;
   const int tiles_n = (N + TN - 1) / TN;
   // the same number of column parts of every token tile, or all tiles dealt out evenly: by rounds of (column tiles +
-  // about two tiles' worth of prologue for each token tile that a CTA meets)
+  // about two tiles' worth of prologue for each token tile that a CTA meets).  Dealing evenly also evens out tiles of
+  // several adapters; of one it has to gain more than a tenth.  us a call, evenly | in parts: 5000 x 8192, rank 32,
+  // one adapter 38.5 | 36.3, four 48.9 | 49.9; 9500 x 2504, rank 64, one 30.3 | 32.8, four 34.7 | 36.4; 8192 x 12288,
+  // rank 128, one 85 | 82, four 104 | 108
   int parts = 1;
   int64_t best_cost = INT64_MAX;
   for (int s = 1; s <= tiles_n && s <= 4 * num_sms; ++s) {
@@ -1180,7 +1182,9 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
     }
   }
   const int64_t share = (tiles_m * tiles_n + num_sms - 1) / num_sms;
-  if (share + 2 * ((share + tiles_n - 1) / tiles_n + 1) < best_cost) parts = 0;
+  int64_t even = 10 * (share + 2 * ((share + tiles_n - 1) / tiles_n + 1));
+  if (!adapter || L == 1) even += even / 10;
+  if (even < 10 * best_cost) parts = 0;
   const int64_t ctas = parts ? tiles_m * parts : num_sms;
   // a programmatic dependent of the v kernel: it starts, loads base and U while that one ends, and waits for
   // it on the device before it reads V
