@@ -698,3 +698,19 @@ def test_after_other_work_on_the_stream():
             graph.replay()
             torch.cuda.synchronize()
             assert same(got, want)
+
+
+@pytest.mark.parametrize("M,kept", [(2, "bf16"), (300, "int8"), (2600, "bf16"), (2600, "int8")])
+def test_no_indices_and_a_pool_of_several(M, kept):
+    """Without indices every row has the pool's first adapter; the others' gradients are zero."""
+    m = cr()
+    d = make(M, 512, 776, 40, 3, "all", seed=91)
+    zeros = torch.zeros(M, dtype=torch.int32, device="cuda")
+    X = m.cr_ckpt_save(d["X"]) if kept == "int8" else d["X"]
+    got = []
+    for a in (None, zeros):
+        Y, V = m.cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], adapter=a, base=d["base"], save_v=True)
+        got.append((Y, V, *m.cr_lora_backward(d["dY"], X, V, d["down"], d["up"], d["scale"], adapter=a, base=d["dbase"])))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert not got[0][3][1:].any() and not got[0][4][1:].any() and got[0][3][0].any() and got[0][4][0].any()
