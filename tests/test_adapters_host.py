@@ -127,6 +127,22 @@ def test_refusals_by_code():
     assert need >= 264 * 512 * 2 and gi(M=4000, n=need) in DEV and gi(M=4000, n=need - 1) == 5
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake device pointers are only safe where no GPU can be reached")
+@pytest.mark.parametrize("M", [0, 40, 4000])
+def test_a_given_workspace_is_aligned_whether_the_form_needs_one_or_not(M):
+    """The form for few rows needs none, but it writes the status word of one that it is given."""
+    lib, P = b._lib, ctypes.c_void_p
+    A, B, C = P(1 << 20), P(1 << 22), P(1 << 23)
+
+    def fwd(w, n):
+        return lib.cr_lora_forward(A, 512, A, A, A, A, C, 264, B, 264, None, M, 264, 512, 8, 2, w, n, None)
+
+    for off in (1, 2, 4, 8, 16, 128, 255):
+        assert fwd(P((1 << 21) + off), 1 << 26) == 5
+    assert fwd(P(1 << 21), 1 << 26) in (4, 6)
+    assert fwd(None, 0) == (5 if M == 4000 else fwd(P(1 << 21), 1 << 26))
+
+
 def test_binding_wants_cuda_bf16():
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     f = torch.zeros(1, 4, 256, dtype=torch.bfloat16)

@@ -90,7 +90,8 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if (!aligned(down, 16) || !aligned(up, 16) || !aligned(scale, 4) || !aligned(adapter, 4) || !aligned(V, 8))
     return CR_ERR_MISALIGNED;
   const size_t need = M > 0 ? cr_lora_forward_workspace_size(M, N, K, rank, num_adapters) : 0;
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return CR_ERR_WORKSPACE;
+  // (of one that is given although none is needed, the status word is written)
+  if ((need > 0 && (!workspace || workspace_bytes < need)) || !aligned(workspace, 256)) return CR_ERR_WORKSPACE;
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
   if (M == 0) return CR_OK;
