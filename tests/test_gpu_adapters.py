@@ -714,3 +714,89 @@ def test_no_indices_and_a_pool_of_several(M, kept):
     for x, y in zip(*got):
         assert torch.equal(x, y)
     assert not got[0][3][1:].any() and not got[0][4][1:].any() and got[0][3][0].any() and got[0][4][0].any()
+
+
+@pytest.mark.parametrize("M", [3, 40, 600])
+def test_indices_and_scales_written_right_before_a_call(M):
+    """Every call meets indices and scales that are not those of the call before, written by the work right in front
+    of it: by a copy, or by checkpoints saved into them (a kernel that lets the call start beside its end).  The same
+    bits as with a synchronisation after every piece."""
+    m = cr()
+    from w4a8_rotated_quantized_b200 import binding
+
+    K = N = 512
+    L, rounds = 4, 6
+    d = make(M, K, N, 16, L, "all", seed=101)
+    g = gen(102)
+    Wq, _ = m.cr_pack_weight(randn(g, N, K, std=0.04))
+    _, V = m.cr_lora_forward(d["X"], d["down"], d["up"], d["scale"], save_v=True)
+
+    # Rows whose rotated values are, four bytes to an index: an index of -0 .. L (L: none) in the lowest, zeros in the
+    # others, and 127 in the last index of each row, which makes the scale 1 and is no adapter.
+    rows = (M + 63) // 64
+    want_ids = torch.randint(0, L + 1, (rounds, rows, 64), device="cuda", generator=g, dtype=torch.int32)
+    want_ids[:, :, 63] = 127
+    y = torch.zeros(rounds, rows, 64, 4, device="cuda", dtype=torch.float64)
+    y[..., 0] = want_ids.double()
+    h = torch.from_numpy(np.asarray(oracle.regular_hadamard(256), np.float64)).cuda()
+    id_rows = (y.reshape(rounds, rows, 256) @ h).to(BF)
+    scale_rows = randn(g, rounds, L, 256)  # scales of about 0.02, all different
+    w_rows = randn(g, rounds, N, 256)
+
+    codes = torch.zeros(max(rows, N), 256, dtype=torch.int8, device="cuda")
+    adapter = codes.view(torch.int32).reshape(-1)[:M]
+    spare = torch.zeros(max(rows, N), 256, dtype=torch.int8, device="cuda")
+    one = torch.zeros(rows, device="cuda")
+    scale, w_scale = torch.zeros(L, device="cuda"), torch.zeros(N, device="cuda")
+    ptr = binding._ptr
+
+    def save(x, codes, scales):
+        binding._check("cr_ckpt_save", binding._lib.cr_ckpt_save(ptr(x), x.shape[0], 256, 256, ptr(codes), ptr(scales),
+                                                                 binding._stream(x.device)))
+
+    def run(between):
+        codes.zero_(), scale.zero_(), w_scale.zero_()
+        torch.cuda.synchronize()
+        seen = []
+        calls = (lambda: m.cr_lora_forward(d["X"], d["down"], d["up"], scale, adapter=adapter, base=d["base"], save_v=True),
+                 lambda: m.cr_lora_backward(d["dY"], d["X"], V, d["down"], d["up"], scale, adapter=adapter, base=d["dbase"]),
+                 lambda: m.cr_lora_backward(d["dY"], None, V, d["down"], d["up"], scale, adapter=adapter, need_dx=False,
+                                            need_down=False)[2:])
+        for k in range(rounds):
+            for i, call in enumerate(calls):
+                j = (k + i) % rounds
+                save(scale_rows[j], spare, scale)
+                between()
+                save(id_rows[j], codes, one)
+                between()
+                seen += [*call(), adapter.clone()]
+                between()
+                save(id_rows[(j + 1) % rounds], codes, one)
+                between()
+                save(scale_rows[(j + 1) % rounds], spare, scale)
+                between()
+                seen += call()
+                between()
+                adapter.copy_(want_ids[j].reshape(-1)[:M])
+                between()
+                scale.copy_(one[:1].expand(L) * (j + 1))
+                between()
+                seen += call()
+                between()
+            save(w_rows[k], spare, w_scale)
+            between()
+            seen.append(m.cr_w4a4_grad_input(d["dY"], Wq, w_scale))
+            between()
+            w_scale.copy_(w_scale.flip(0))
+            between()
+            seen.append(m.cr_w4a4_grad_input(d["dY"], Wq, w_scale))
+            between()
+        torch.cuda.synchronize()
+        return seen
+
+    want = run(torch.cuda.synchronize)
+    assert torch.equal(want[2], want_ids[0].reshape(-1)[:M])  # the checkpoint's codes are the indices meant
+    for _ in range(5):
+        got = run(lambda: None)
+        for x, w in zip(got, want):
+            assert torch.equal(x.view(torch.uint8), w.view(torch.uint8))

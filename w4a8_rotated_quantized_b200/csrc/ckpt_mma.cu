@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
       const int64_t m0 = t / slices * TM;
       const int slice = static_cast<int>(t % slices);
-      float s = m0 + row < M ? __ldcg(scales + (m0 + row) * slices + slice) * 0.0625f : 0.f;
+      float s = m0 + row < M ? ldcg_here_f1(scales + (m0 + row) * slices + slice) * 0.0625f : 0.f;
       if (ok) ok = mbar_sleep_warp(bars.acc_full(b), ph, abort);
       if (!ok) s = __uint_as_float(0x7FC00000u);
       tc_fence_after();

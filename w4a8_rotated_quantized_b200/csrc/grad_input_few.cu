@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(256)
   if (n >= N) return;
   float v[8] = {};
   if (m < M) {
-    widen8(ldcg16(dY + m * lddy + n), v);
+    widen8(ldcg_here_u4(dY + m * lddy + n), v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= __ldg(w_scale + n + e);
+    for (int e = 0; e < 8; ++e) v[e] *= ldcg_here_f1(w_scale + n + e);
   }
   *reinterpret_cast<uint4*>(V + static_cast<int64_t>(m) * N + n) = narrow8(v);
 }

@@ -10,9 +10,6 @@ namespace cr {
 
 __device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// Past L1: of what a kernel may have written that this one started beside.
-__device__ __forceinline__ uint4 ldcg16(const uint16_t* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
-
 // Eight bf16 values as floats: the bit patterns 16 bits up.
 __device__ __forceinline__ void widen8(uint4 q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -33,8 +30,11 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
-// Loads that stay where they are written: the compiler sinks plain read-only loads to their first use, which
-// undoes a prefetch into registers.  Past L1, as above.
+// Loads of what a kernel may have written that this one started beside, indices and scales included.  Past L1,
+// which may hold older values: a read-only load (ld.global.nc) asks that nobody writes while the kernel runs, and this
+// kernel runs before the writer has ended.  Volatile, so that they stay where they are written: behind
+// griddepcontrol.wait, and before their first use, to which the compiler would sink them and undo a prefetch into
+// registers.
 __device__ __forceinline__ float4 ldcg_here_f4(const float* p) {
   float4 v;
   asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
@@ -55,6 +55,11 @@ __device__ __forceinline__ float ldcg_here_f1(const float* p) {
   asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
+__device__ __forceinline__ int ldcg_here_s32(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 
 // Two floats as bf16 pairs: the rounded values in `hi`, what they leave, rounded, in `lo`.  A non-finite
 // value's rest is NaN, which the sum keeps.
@@ -64,9 +69,9 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
 }
 
 // Row m's adapter, -1 where it has none (an index outside the pool); without indices every row has the first.
-__device__ __forceinline__ int row_adapter(const int32_t* __restrict__ adapter, int64_t m, int L) {
+__device__ __forceinline__ int row_adapter(const int32_t* adapter, int64_t m, int L) {
   if (!adapter) return 0;
-  const int a = __ldg(adapter + m);
+  const int a = ldcg_here_s32(adapter + m);
   return static_cast<unsigned>(a) < static_cast<unsigned>(L) ? a : -1;
 }
 

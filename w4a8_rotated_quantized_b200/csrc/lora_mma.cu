@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
       bool ok = nd == 0 || !v_tma || mbar_sleep_warp(v_in, vs & 1, abort);
       if (ok && nd > 0) {
         // this warp's rows, every other 16 ranks
-        const float sc = mine >= 0 ? __ldg(scale + mine) : 0.f;
+        const float sc = mine >= 0 ? ldcg_here_f1(scale + mine) : 0.f;
         auto put = [&](int g, const float4 (&f)[4]) {
           uint32_t hi[8], lo[8];
 #pragma unroll
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine >= 0 && 16 * half + 4 * k < rank) f[k] = __ldcg(reinterpret_cast<const float4*>(src + 4 * k));
+            if (mine >= 0 && 16 * half + 4 * k < rank) f[k] = ldcg_here_f4(src + 4 * k);
           }
           put(half, f);
         }
@@ -1003,7 +1003,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
     if constexpr (kV16) griddep_wait();  // this kernel's end is to mean the ones before have ended, too
     const int q = warp & 3, half = (warp >> 2) & 1, part = warp >> 3;  // every other 16 ranks
     const int c = c0 + 128 * half + 32 * q + lane;
-    const float sc = __ldg(scale + a) * (kCodes ? 64.f : 1.f);  // codes come as 2^-6 of themselves
+    const float sc = ldcg_here_f1(scale + a) * (kCodes ? 64.f : 1.f);  // codes come as 2^-6 of themselves
     const bool whole = splits == 1;  // no other part: rounded here
     float* out = G + (static_cast<int64_t>(split) * L + a) * rank * C + c;
     uint16_t* rows16 = grad + static_cast<int64_t>(a) * rank * C + c0;

@@ -74,12 +74,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (a < 0) {
     for (int p = tid; p < pieces; p += kThreads)
       *reinterpret_cast<uint4*>(Y + m * ldy + 8 * (p0 + p)) =
-          brow ? ldcg16(brow + 8 * (p0 + p)) : make_uint4(0, 0, 0, 0);
+          brow ? ldcg_here_u4(brow + 8 * (p0 + p)) : make_uint4(0, 0, 0, 0);
     if (V32 && c == 0 && tid < rank) V32[m * rank + tid] = 0.f;
     if (Vout && c == 0 && tid < rank) Vout[m * rank + tid] = 0;
     return;
   }
   cluster_arrive();
+  const float sc = ldcg_here_f1(scale + a);
   const uint16_t* u = up + static_cast<int64_t>(a) * rank * N + 8 * p0;
   uint4 ahead[kAhead], b = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -104,9 +105,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int q = q0 + 32 * pass + lane;
       const bool in = q < q_end && t < rank * passes;
       const uint16_t* src = w + static_cast<int64_t>(j) * K + 8 * q;
-      xq[i / 4] = in ? ldcg16(x + 8 * q) : make_uint4(0, 0, 0, 0);
+      xq[i / 4] = in ? ldcg_here_u4(x + 8 * q) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) wq[i + e] = in ? ldcg16(src + static_cast<int64_t>(e) * K) : make_uint4(0, 0, 0, 0);
+      for (int e = 0; e < 4; ++e) wq[i + e] = in ? ldcg_here_u4(src + static_cast<int64_t>(e) * K) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (i < ctas) t += part[i][tid];
     if (V32 && c == 0) V32[m * rank + tid] = t;
     if (Vout && c == 0) Vout[m * rank + tid] = bf16_bits(t);
-    v[tid] = t * __ldg(scale + a);
+    v[tid] = t * sc;
   }
   __syncthreads();
   for (int p = piece, first = 1; p < pieces && group < groups; p += kThreads, first = 0) {
@@ -154,12 +155,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     } else if (brow) {
-      b = ldcg16(brow + 8 * (p0 + p));
+      b = ldcg_here_u4(brow + 8 * (p0 + p));
     }
 #pragma unroll 4
     for (int j = group + (first ? groups * kAhead : 0); j < rank; j += groups) {
       float uv[8];
-      widen8(ldcg16(u + static_cast<int64_t>(j) * N + 8 * p), uv);
+      widen8(ldcg_here_u4(u + static_cast<int64_t>(j) * N + 8 * p), uv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = fmaf(v[j], uv[e], y[e]);
     }

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool join_parts(const float* __restrict__ src, int pa
   for (int f = 0; f < kF; ++f) v[f] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p = warp; p < (in ? parts : 0); p += kJoinWarps) {
 #pragma unroll
-    for (int f = 0; f < kF; ++f) add4(v[f], __ldcg(reinterpret_cast<const float4*>(src + p * stride + at(f))));
+    for (int f = 0; f < kF; ++f) add4(v[f], ldcg_here_f4(src + p * stride + at(f)));
   }
   if (warp > 0) {
 #pragma unroll
