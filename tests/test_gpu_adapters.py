@@ -800,3 +800,30 @@ def test_indices_and_scales_written_right_before_a_call(M):
         got = run(lambda: None)
         for x, w in zip(got, want):
             assert torch.equal(x.view(torch.uint8), w.view(torch.uint8))
+
+
+def test_empty_calls_write_the_status_word():
+    """A call without rows, or without anything to make, says so in the workspace that it is given, too."""
+    m = cr()
+    d = make(0, 512, 264, 8, 2, "all", seed=111)
+    full = make(5, 512, 264, 8, 2, "rows", seed=112)
+    tail = (d["down"], d["up"], d["scale"])
+    codes = torch.zeros(0, 512, dtype=torch.int8, device="cuda"), torch.zeros(0, 2, device="cuda")
+    V = torch.zeros(0, 8, dtype=BF, device="cuda")
+    Wq, s = m.cr_pack_weight(randn(gen(113), 264, 512))
+    none = torch.zeros(5, 0, dtype=BF, device="cuda")
+    from w4a8_rotated_quantized_b200 import binding
+
+    size = max(binding._lib.cr_lora_backward_workspace_size(M, 264, 512, 8, 2) for M in (0, 5))
+    size = max(size, binding._lib.cr_w4a4_grad_input_workspace_size(0, 264, 512, 256))
+    for call in (lambda ws: m.cr_lora_forward(d["X"], *tail, base=d["base"], workspace=ws),
+                 lambda ws: m.cr_lora_backward(d["dY"], d["X"], V, *tail, workspace=ws),
+                 lambda ws: m.cr_lora_backward(d["dY"], codes, V, *tail, workspace=ws),
+                 lambda ws: m.cr_lora_backward(full["dY"], None, None, *tail, need_dx=False, need_down=False, need_up=False,
+                                               workspace=ws),
+                 lambda ws: m.cr_w4a4_grad_input(d["dY"], Wq, s, workspace=ws),
+                 lambda ws: m.cr_w4a4_grad_input(none, Wq[:0], s[:0], workspace=ws)):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        call(ws)
+        assert m.cr_read_device_status(ws=ws) == 0
+        assert not ws[:16].any() and (ws[16:] == 255).all()  # and nothing else

@@ -22,6 +22,12 @@ inline int* ws_status(void* workspace) {
   return reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + cr::kWsStatusOff);
 }
 
+// The status word of a call that launches no kernel to clear it.
+inline cr_status clear_status(void* workspace, size_t workspace_bytes, cudaStream_t s) {
+  if (!workspace || workspace_bytes < 16) return CR_OK;
+  return cuda_status(cudaMemsetAsync(ws_status(workspace), 0, 16, s));
+}
+
 // Workspace of the adapter calls: the status word's 256 bytes, then the parts below, each on 256 bytes.
 constexpr size_t kWsHead = 256;
 
@@ -94,8 +100,8 @@ cr_status cr_lora_forward(const void* X, int64_t ldx, const int32_t* adapter, co
   if ((need > 0 && (!workspace || workspace_bytes < need)) || !aligned(workspace, 256)) return CR_ERR_WORKSPACE;
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
-  if (M == 0) return CR_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) return clear_status(workspace, workspace_bytes, s);
   float* v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead);
   uint16_t* vout = static_cast<uint16_t*>(V);
   int* status = ws_status(workspace);
@@ -151,8 +157,8 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
   const int L = num_adapters;
   const int64_t nd = static_cast<int64_t>(L) * rank * K, nu = static_cast<int64_t>(L) * rank * N;
   if (M == 0) {  // no rows: the gradients are zero
-    cudaError_t e = cudaSuccess;
-    if (d_down) e = cudaMemsetAsync(d_down, 0, static_cast<size_t>(nd) * 2, s);
+    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, 16, s);
+    if (e == cudaSuccess && d_down) e = cudaMemsetAsync(d_down, 0, static_cast<size_t>(nd) * 2, s);
     if (e == cudaSuccess && d_up) e = cudaMemsetAsync(d_up, 0, static_cast<size_t>(nu) * 2, s);
     return cuda_status(e);
   }
@@ -174,8 +180,8 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
     r = cr::launch_lora_v_mma(dy, lddy, adapter, u, dv, nullptr, M, N, rank, L, status, nsm, s);
     if (r == CR_OK && dX)
       r = cr::launch_lora_y_mma(dv, adapter, dn, scale, xb, ldb, dx, lddx, M, K, rank, L, status, nsm, s);
-  } else if (cudaMemsetAsync(workspace, 0, 16, s) != cudaSuccess) {
-    return CR_ERR_CUDA;
+  } else {
+    r = clear_status(workspace, workspace_bytes, s);
   }
   if (r != CR_OK) return static_cast<cr_status>(r);
   if (d_down || d_up) {
@@ -246,11 +252,14 @@ cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const
     return CR_ERR_WORKSPACE;
   int nsm = 0;
   if ((st = static_cast<cr_status>(cr::check_current_device(&nsm))) != CR_OK) return st;
-  if (M == 0) return CR_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (N == 0)  // no outputs: the gradient is zero
+  if (M == 0 || N == 0) {
+    st = clear_status(workspace, workspace_bytes, s);
+    if (st != CR_OK || M == 0) return st;
+    // no outputs: the gradient is zero
     return cuda_status(cudaMemset2DAsync(dX, static_cast<size_t>(lddx) * 2, 0, static_cast<size_t>(K) * 2,
                                          static_cast<size_t>(M), s));
+  }
   uint16_t* w = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWsHead);
   if (cr::use_grad_input_few(M, N, K)) {
     float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHead +
