@@ -432,6 +432,9 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  *            NULL if not wanted.  (Y is computed from the float32 V.)
  * A row's values never enter another row's results: infinities and NaN stay in
  * their row, and those of an adapter in the rows that name it.
+ * An infinite V, dV or scale times a factor other than zero is an infinity of
+ * the product's sign.  A factor (up, down, or X in d_down) that is infinite
+ * itself makes the results that it enters infinite or NaN.
  *
  * cr_lora_backward -- gradients of the same map:
  *   dV[m, :]    = scale[a] * dY[m, :] U[a]^T           (float32 sums)

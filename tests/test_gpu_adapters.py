@@ -827,3 +827,54 @@ def test_empty_calls_write_the_status_word():
         call(ws)
         assert m.cr_read_device_status(ws=ws) == 0
         assert not ws[:16].any() and (ws[16:] == 255).all()  # and nothing else
+
+
+@pytest.mark.parametrize("r", [8, 64])
+@pytest.mark.parametrize("M", [3, 600])
+def test_infinities_by_the_formula(M, r):
+    """An infinite V or dV gives infinities of the formula's sign and a V past bf16's largest value finite results,
+    in the form for few rows and in the one for batches, of up to 32 ranks and of more."""
+    m = cr()
+    K, N, inf = 64, 72, float("inf")
+    X = torch.zeros(M, K, dtype=BF, device="cuda")
+    X[:, 0] = 1
+    X[0, 1] = inf  # V infinite
+    X[1, 1] = float("nan")
+    # 2^128 - 2^120 is bf16's largest value; with 1.5 * 2^119 more V is float32 still, but rounds to an infinity
+    X[2, 0], X[2, 2] = 2.0 ** 128 - 2.0 ** 120, 1.5 * 2.0 ** 119
+    down = torch.zeros(2, r, K, dtype=BF, device="cuda")
+    down[:, 0, :3] = 1
+    down[:, 1:, 0] = 2.0 ** -126
+    down[:, 1:, 1] = 1
+    up = torch.full((2, r, N), 2.0 ** -30, dtype=BF, device="cuda")
+    up[:, :, 1::2] *= -1
+    scale = torch.tensor([1.0, inf], device="cuda")
+    a = torch.zeros(M, dtype=torch.int32, device="cuda")
+    if M > 3:
+        a[3] = 1  # scale infinite
+    Y, V = m.cr_lora_forward(X, down, up, scale, adapter=a, save_v=True)
+    sign = torch.ones(N, device="cuda")
+    sign[1::2] = -1
+    assert (V[0] == inf).all() and torch.isnan(V[1]).all() and V[2, 0] == inf and torch.isfinite(V[2, 1:]).all()
+    assert torch.equal(Y[0].float(), sign * inf) and torch.isnan(Y[1]).all()
+    v, want = f64(X[2]) @ f64(down[0]).T, f64(up[0])
+    want = v @ want
+    # one rounding of the output, the pair's 2^-16, float32 sums of r products
+    within(Y[2], want, np.abs(want) * (ao.BF16 + ao.PAIR + ao.steps(2 * r)), "Y")
+    assert torch.isfinite(Y[4:]).all()
+    if M > 3:
+        assert torch.equal(Y[3].float(), sign * inf)
+    # backward: dV of row 0 infinite, X positive in one column and negative in another, one row to an adapter
+    dY = torch.zeros(M, N, dtype=BF, device="cuda")
+    dY[0, 0], dY[1:, 0] = inf, 1
+    a = torch.full((M,), 1, dtype=torch.int32, device="cuda")
+    a[0] = 0
+    Z = torch.ones(M, K, dtype=BF, device="cuda")
+    Z[:, 1::2] = -1
+    flip = torch.ones(K, device="cuda")
+    flip[1::2] = -1
+    down = torch.ones(2, r, K, dtype=BF, device="cuda")
+    down[:, :, 1::2] = -1
+    dX, dd, _ = m.cr_lora_backward(dY, Z, None, down, up, torch.ones(2, device="cuda"), adapter=a, need_up=False)
+    assert torch.equal(dX[0].float(), flip * inf) and torch.isfinite(dX[1:]).all()
+    assert torch.equal(dd[0].float(), (flip * inf).expand(r, K)) and torch.isfinite(dd[1]).all()

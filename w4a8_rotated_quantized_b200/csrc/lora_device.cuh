@@ -61,10 +61,17 @@ __device__ __forceinline__ int ldcg_here_s32(const int32_t* p) {
   return v;
 }
 
-// Two floats as bf16 pairs: the rounded values in `hi`, what they leave, rounded, in `lo`.  A non-finite
-// value's rest is NaN, which the sum keeps.
+// Two floats as bf16 pairs: the rounded values in `hi`, what they leave, rounded, in `lo`.  `hi` stays finite: what
+// would round to an infinity there, infinities themselves included, is held at the largest bf16 value and leaves the
+// rest to `lo`, or else the rest would be inf - inf.  So an infinity times a factor other than zero is an infinity of
+// the product's sign, as it is without the split.  A NaN's rest is NaN, which the sum keeps.
+__device__ __forceinline__ float hold_bf16(float a) {
+  float d;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(__uint_as_float(0x7F7F0000u)));
+  return d;
+}
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(a, b);
+  hi = pack_bf16(hold_bf16(a), hold_bf16(b));
   lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
 }
 

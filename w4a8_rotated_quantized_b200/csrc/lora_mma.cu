@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(kYMmaThreads, 1)
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            split_bf16(f[k].x * sc, f[k].y * sc, hi[2 * k], lo[2 * k]);
-            split_bf16(f[k].z * sc, f[k].w * sc, hi[2 * k + 1], lo[2 * k + 1]);
+            const float t = 16 * g + 4 * k < rank ? sc : 0.f;  // (an infinite scale makes NaN of the zeros past the rank)
+            split_bf16(f[k].x * t, f[k].y * t, hi[2 * k], lo[2 * k]);
+            split_bf16(f[k].z * t, f[k].w * t, hi[2 * k + 1], lo[2 * k + 1]);
           }
           const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(kVCol + 8 * g);
           tmem_st8(at, hi);
