@@ -2,6 +2,7 @@
 ABI's refusals (fake device pointers, never dereferenced) and the binding's argument checks."""
 
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -9,6 +10,8 @@ import torch
 
 from oracle import adapter_oracle as ao
 from w4a8_rotated_quantized_b200 import binding as b
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _case(seed=0, M=9, K=256, N=16, r=4, L=3):
@@ -159,3 +162,41 @@ def test_binding_wants_cuda_bf16():
         b.cr_ckpt_load(torch.zeros(4, 256), torch.ones(4, 1))
     with pytest.raises(TypeError):
         b.cr_w4a4_grad_input(x, torch.zeros(256, 128, dtype=torch.uint8), torch.ones(256))
+
+
+def test_the_other_calls_work_without_the_extension_module():
+    """Without _calls the package imports and every ctypes call works; a call that needs it says what is missing."""
+    import subprocess
+    import sys
+
+    code = """
+import sys
+sys.modules["w4a8_rotated_quantized_b200._calls"] = None  # what a missing or unloadable module comes to
+import torch
+import w4a8_rotated_quantized_b200 as cr
+assert cr.cr_api_version() == 1 and cr.cr_status_string(0)
+x = torch.zeros(4, 256, dtype=torch.bfloat16)
+try:
+    cr.cr_pack_weight(x.float())
+    raise SystemExit("no TypeError")
+except TypeError:
+    pass
+for call in (lambda: cr.cr_ckpt_save(x), lambda: cr.cr_lora_forward(x, x, x, x), lambda: cr.cr_w4a4_grad_input(x, x, x)):
+    try:
+        call()
+        raise SystemExit("no ImportError")
+    except ImportError as e:
+        assert "_calls" in str(e) and "build" in str(e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_the_extension_module_is_rebuilt_for_another_torch(monkeypatch):
+    from w4a8_rotated_quantized_b200 import build
+
+    assert not build._calls_stale()  # built when the tests were collected
+    made = build._calls_made_with()
+    assert torch.__version__.split("+")[0] in made
+    monkeypatch.setattr(build, "_calls_made_with", lambda: made.replace(torch.__version__.split("+")[0], "0.0"))
+    assert build._calls_stale()

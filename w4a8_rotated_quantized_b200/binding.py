@@ -676,13 +676,24 @@ def cr_selftest_wait_timeout(ws: torch.Tensor) -> None:
 # then be read with ``cr_read_device_status(ws=...)``.
 # ---------------------------------------------------------------------------
 
-try:
-    from . import _calls
-except ImportError as e:
-    raise ImportError("the extension module _calls is not built; build it with "
-                      "`python -m w4a8_rotated_quantized_b200.build`") from e
 
-_calls.set_error(ConvRotError)
+class _CallsLater:
+    """Stands for ``_calls`` until the first call that needs it: the other calls work without it (they need no
+    torch ABI), and one that needs it fails loudly."""
+
+    def __getattr__(self, name):
+        global _calls
+        try:
+            from . import _calls as calls
+        except ImportError as e:
+            raise ImportError("the extension module _calls is not built, or was built for another torch; build it with "
+                              "`python -m w4a8_rotated_quantized_b200.build`") from e
+        calls.set_error(ConvRotError)
+        _calls = calls
+        return getattr(calls, name)
+
+
+_calls = _CallsLater()
 
 
 def cr_lora_forward(X: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,

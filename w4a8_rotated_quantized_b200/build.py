@@ -10,6 +10,8 @@ library beside it.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -22,6 +24,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconvrot_b200.so")
 CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
+CALLS_MADE_WITH = os.path.join(BUILD, "_calls.made_with")
 SOURCES = ["api.cu", "act_kernels.cu", "gemm_w4a4.cu", "gemm_w4a4_pair.cu", "gemm_w4a4_small.cu", "gemm_i8.cu",
            "gemm_w4a8.cu", "gemm_a8w4.cu", "tmap.cu", "noalloc.cu",
            "selftest.cu", "api_adapters.cu", "lora_rows.cu", "lora_mma.cu", "grad_values.cu", "ckpt_mma.cu", "gemm_bf16.cu",
@@ -59,6 +62,19 @@ def _calls_cmd() -> list:
             "-L" + os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
+def _calls_made_with() -> str:
+    """What _calls.so is bound to beside its own source: this Python and the torch that it is compiled against."""
+    torch = importlib.util.find_spec("torch")
+    return "\n".join([sys.version, importlib.metadata.version("torch"), torch.origin if torch else ""])
+
+
+def _calls_stale() -> bool:
+    if _mtime(CALLS) < max(_mtime(CALLS_SRC), _mtime(HEADERS[0])) or not os.path.exists(CALLS_MADE_WITH):
+        return True
+    with open(CALLS_MADE_WITH) as f:
+        return f.read() != _calls_made_with()
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every .cu source and link the shared library; return its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -87,8 +103,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 sys.stderr.write(err)
     if jobs or force or _mtime(LIB) < max(_mtime(o) for o in objs):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs])
-    if force or _mtime(CALLS) < max(_mtime(CALLS_SRC), _mtime(HEADERS[0])):
+    if force or _calls_stale():
         run(_calls_cmd())
+        with open(CALLS_MADE_WITH, "w") as f:
+            f.write(_calls_made_with())
     return LIB
 
 
