@@ -878,3 +878,25 @@ def test_infinities_by_the_formula(M, r):
     dX, dd, _ = m.cr_lora_backward(dY, Z, None, down, up, torch.ones(2, device="cuda"), adapter=a, need_up=False)
     assert torch.equal(dX[0].float(), flip * inf) and torch.isfinite(dX[1:]).all()
     assert torch.equal(dd[0].float(), (flip * inf).expand(r, K)) and torch.isfinite(dd[1]).all()
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_copy_on_write_outputs_are_made_their_own(M):
+    """An output that shares its memory with another tensor until it is written: the other keeps its values."""
+    m = cr()
+    d = make(M, 512, 512, 8, 2, "rows", seed=121)
+    tail, a = (d["down"], d["up"], d["scale"]), d["adapter"]
+    Wq, s = m.cr_pack_weight(randn(gen(122), 512, 512))
+    kept = m.cr_ckpt_save(d["X"])
+    for shared, call in ((d["base"], lambda **k: m.cr_lora_forward(d["X"], *tail, adapter=a, **k)),
+                         (d["dbase"], lambda **k: m.cr_lora_backward(d["dY"], None, None, *tail, adapter=a, need_down=False,
+                                                                     need_up=False, **k)[0]),
+                         (d["X"], lambda **k: m.cr_ckpt_load(*kept, **k)),
+                         (d["dY"], lambda **k: m.cr_w4a4_grad_input(d["dY"], Wq, s, **k))):
+        before = shared.clone()
+        for in_place in (False, True) if shared is d["base"] or shared is d["dbase"] else (False,):
+            want = call(**({"base": shared} if in_place else {}))
+            out = torch._lazy_clone(shared)
+            got = call(out=out, **({"base": out} if in_place else {}))
+            assert got is out and torch.equal(out, want) and torch.equal(shared, before)
+            assert out.data_ptr() != shared.data_ptr()

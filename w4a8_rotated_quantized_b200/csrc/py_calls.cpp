@@ -50,6 +50,10 @@ struct Matrix {
   const void* p = nullptr;
   int64_t ld = 0;
 };
+struct Rows {  // of an output
+  void* p = nullptr;
+  int64_t ld = 0;
+};
 
 // A bf16 [M, C] matrix with dense columns.
 Matrix matrix(const at::Tensor& t, const char* name, at::Device dev, int64_t M, int64_t C) {
@@ -91,11 +95,15 @@ at::Tensor make(at::IntArrayRef size, at::ScalarType dtype, at::Device dev) {
   return at::empty(size, at::TensorOptions().dtype(dtype).device(dev));
 }
 
-// The caller's output or a new one, bf16 [M, C].
-Matrix output(at::Tensor& out, at::Device dev, int64_t M, int64_t C) {
-  if (out.defined()) return matrix(out, "out", dev, M, C);
-  out = make({M, C}, at::kBFloat16, dev);
-  return {out.const_data_ptr(), C};
+// The caller's output or a new one, bf16 [M, C].  Taken for writing, which gives a copy-on-write tensor memory of its
+// own: so before the address of any operand that may be the same tensor.
+Rows output(at::Tensor& out, at::Device dev, int64_t M, int64_t C) {
+  int64_t ld = C;
+  if (out.defined())
+    ld = matrix(out, "out", dev, M, C).ld;
+  else
+    out = make({M, C}, at::kBFloat16, dev);
+  return {out.mutable_data_ptr(), ld};
 }
 
 // Scratch: the caller's, or a buffer of this call's own from torch's allocator on the current stream (inside a
@@ -200,16 +208,16 @@ PyObject* lora_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor down = tensor(a[1], "down"), up = tensor(a[2], "up"), scale = tensor(a[3], "scale");
   const at::Tensor adapter = tensor(a[4], "adapter", true), base = tensor(a[5], "base", true);
   const Pool p = pool(down, up, scale, adapter, dev, M, K, -1);
-  const Matrix b = base.defined() ? matrix(base, "base", dev, M, p.N) : Matrix{};
   at::Tensor Y = tensor(a[6], "out", true), V;
-  const Matrix y = output(Y, dev, M, p.N);
+  const Rows y = output(Y, dev, M, p.N);
+  const Matrix b = base.defined() ? matrix(base, "base", dev, M, p.N) : Matrix{};
   if (truth(a[7])) V = make({M, p.r}, at::kBFloat16, dev);
   const Scratch ws = scratch(a[8], cr_lora_forward_workspace_size(M, p.N, K, p.r, p.L), dev);
   {
     On on(dev);
     check("cr_lora_forward",
           cr_lora_forward(x.p, x.ld, static_cast<const int32_t*>(p.adapter), p.down, p.up, static_cast<const float*>(p.scale),
-                          b.p, b.ld, const_cast<void*>(y.p), y.ld, V.defined() ? V.mutable_data_ptr() : nullptr, M, p.N, K,
+                          b.p, b.ld, y.p, y.ld, V.defined() ? V.mutable_data_ptr() : nullptr, M, p.N, K,
                           p.r, p.L, ws.p, ws.n, stream(dev)));
   }
   PyObject* out = a[6] != Py_None ? Py_NewRef(a[6]) : wrap(Y);
@@ -252,10 +260,10 @@ PyObject* lora_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const at::Tensor V = tensor(a[2], "V", true);
   if (V.defined()) v = exact(V, "V", at::kBFloat16, dev, {M, p.r});
-  const Matrix b = base.defined() ? matrix(base, "base", dev, M, p.K) : Matrix{};
   at::Tensor dX = tensor(a[8], "out", true), dd, du;
-  Matrix dx;
+  Rows dx;
   if (need_dx) dx = output(dX, dev, M, p.K);
+  const Matrix b = base.defined() ? matrix(base, "base", dev, M, p.K) : Matrix{};
   if (need_down) dd = make({p.L, p.r, p.K}, at::kBFloat16, dev);
   if (need_up) du = make({p.L, p.r, N}, at::kBFloat16, dev);
   const Scratch ws = scratch(a[12], cr_lora_backward_workspace_size(M, N, p.K, p.r, p.L), dev);
@@ -264,7 +272,7 @@ PyObject* lora_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check("cr_lora_backward",
           cr_lora_backward(dy.p, dy.ld, x.p, x.ld, codes, static_cast<const float*>(code_scales), v,
                            static_cast<const int32_t*>(p.adapter), p.down, p.up, static_cast<const float*>(p.scale), b.p,
-                           b.ld, const_cast<void*>(dx.p), dx.ld, dd.defined() ? dd.mutable_data_ptr() : nullptr,
+                           b.ld, dx.p, dx.ld, dd.defined() ? dd.mutable_data_ptr() : nullptr,
                            du.defined() ? du.mutable_data_ptr() : nullptr, M, N, p.K, p.r, p.L, ws.p, ws.n, stream(dev)));
   }
   PyObject* out[3] = {a[8] != Py_None ? Py_NewRef(a[8]) : wrap(dX), wrap(dd), wrap(du)};
@@ -309,11 +317,10 @@ PyObject* ckpt_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor scales = tensor(a[1], "scales");
   const void* s = exact(scales, "scales", at::kFloat, dev, {M, K / 256});
   at::Tensor X = tensor(a[2], "out", true);
-  const Matrix x = output(X, dev, M, K);
+  const Rows x = output(X, dev, M, K);
   {
     On on(dev);
-    check("cr_ckpt_load", cr_ckpt_load(codes.const_data_ptr(), static_cast<const float*>(s), M, K, const_cast<void*>(x.p),
-                                       x.ld, stream(dev)));
+    check("cr_ckpt_load", cr_ckpt_load(codes.const_data_ptr(), static_cast<const float*>(s), M, K, x.p, x.ld, stream(dev)));
   }
   return a[2] != Py_None ? Py_NewRef(a[2]) : wrap(X);
   END_HANDLE_TH_ERRORS
@@ -335,12 +342,12 @@ PyObject* grad_input(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const long group = PyLong_AsLong(a[3]);
   if (group == -1 && PyErr_Occurred()) throw python_error();
   at::Tensor dX = tensor(a[4], "out", true);
-  const Matrix dx = output(dX, dev, M, K);
+  const Rows dx = output(dX, dev, M, K);
   const Scratch ws = scratch(a[5], cr_w4a4_grad_input_workspace_size(M, N, K, static_cast<int>(group)), dev);
   {
     On on(dev);
     check("cr_w4a4_grad_input",
-          cr_w4a4_grad_input(dy.p, dy.ld, w, static_cast<const float*>(s), const_cast<void*>(dx.p), dx.ld, M, N, K,
+          cr_w4a4_grad_input(dy.p, dy.ld, w, static_cast<const float*>(s), dx.p, dx.ld, M, N, K,
                              static_cast<int>(group), ws.p, ws.n, stream(dev)));
   }
   return a[4] != Py_None ? Py_NewRef(a[4]) : wrap(dX);
