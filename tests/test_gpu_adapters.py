@@ -900,3 +900,11 @@ def test_copy_on_write_outputs_are_made_their_own(M):
             got = call(out=out, **({"base": out} if in_place else {}))
             assert got is out and torch.equal(out, want) and torch.equal(shared, before)
             assert out.data_ptr() != shared.data_ptr()
+
+
+@pytest.mark.parametrize("group", [(1 << 32) + 256, -(1 << 32) + 64, 1 << 31, 1 << 80])
+def test_a_group_past_32_bits_is_refused(group):
+    m = cr()
+    Wq, s = m.cr_pack_weight(randn(gen(131), 8, 256))
+    with pytest.raises((ValueError, OverflowError)):
+        m.cr_w4a4_grad_input(randn(gen(132), 4, 8), Wq, s, group=group)

@@ -341,6 +341,7 @@ PyObject* grad_input(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* s = exact(w_scale, "w_scale", at::kFloat, dev, {N});
   const long group = PyLong_AsLong(a[3]);
   if (group == -1 && PyErr_Occurred()) throw python_error();
+  if (group != static_cast<int>(group)) refuse(PyExc_ValueError, "group must be 16, 64, 256 or 1024");
   at::Tensor dX = tensor(a[4], "out", true);
   const Rows dx = output(dX, dev, M, K);
   const Scratch ws = scratch(a[5], cr_w4a4_grad_input_workspace_size(M, N, K, static_cast<int>(group)), dev);
