@@ -445,6 +445,9 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  *   X        bf16 [M, K], row stride ldx, or NULL and
  *   codes, code_scales  X's 8-bit checkpoint from cr_ckpt_save (K % 256 == 0);
  *            the product reads the codes themselves, nothing is restored first
+ *            (its sums are rotated before the division by 16: they hold as long
+ *            as the magnitudes |dV s c| of a rank and slice add up to less than
+ *            2^128)
  *   V        bf16 [M, rank] from cr_lora_forward
  *   dX_base  bf16 [M, K], row stride ldb (the projection's own input gradient,
  *            e.g. from cr_w4a4_grad_input), NULL for zero; may be dX itself
@@ -492,8 +495,10 @@ cr_status cr_lora_backward(const void* dY, int64_t lddy, const void* X, int64_t 
  * and back: x^ = bf16_rn( (c s) H256 ).
  *   X       bf16 [M, K], row stride ldx >= K
  *   codes   int8 [M, K], dense;  scales  float32 [M, K/256], dense
- * A slice whose rotation holds an infinity or NaN gets the scale NaN: all its
- * values come back as NaN.  Half a step of the code is s / 2 in the rotated
+ * The sums are taken before the division by sqrt(256): a slice holds as long as
+ * its magnitudes |x| add up to less than 2^128 (values of about 2^120 and more,
+ * all of one slice, may not).  A slice whose sums hold an infinity or NaN gets the
+ * scale NaN: all its values come back as NaN.  Half a step of the code is s / 2 in the rotated
  * values.  cr_lora_backward takes codes and scales in place of X.
  * Shape rules: M >= 0, K >= 256, K % 256 == 0, K <= CR_MAX_K.  Alignment: X,
  * codes 16-byte aligned, ldx % 8 == 0.  No workspace.
@@ -507,7 +512,10 @@ cr_status cr_ckpt_load(const void* codes, const float* scales, int M, int K, voi
  *   dX = dY W^,   W^[n, :] = w_scale[n] * (q[n, :] H_group)
  * with float32 sums, rounded once to bf16.  One operand of the product is
  * rounded to bf16 before it: W^, or, where there are few tokens for that many
- * weights, w_scale[n] dY[:, n] (the codes are exact then; W^ is never made).
+ * weights, w_scale[n] dY[:, n] (the codes are exact then; W^ is never made, and
+ * sums are rotated before the division by sqrt(group): they hold as long as, for
+ * a token and a group of columns, the magnitudes |w_scale dY q| add up to less
+ * than 2^128).
  * The same Wq and w_scale as the forward calls (either scale mode).
  *   dY  bf16 [M, N], row stride lddy >= N;  dX  out: bf16 [M, K], row stride lddx >= K
  * Shape and alignment rules as cr_w4a4_linear, lddy and lddx % 8 == 0,

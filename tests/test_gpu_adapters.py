@@ -908,3 +908,21 @@ def test_a_group_past_32_bits_is_refused(group):
     Wq, s = m.cr_pack_weight(randn(gen(131), 8, 256))
     with pytest.raises((ValueError, OverflowError)):
         m.cr_w4a4_grad_input(randn(gen(132), 4, 8), Wq, s, group=group)
+
+
+@pytest.mark.parametrize("power", [-90, 40, 100, 112])
+def test_checkpoint_over_its_range(power):
+    """A power of two on the values is one on the scales and leaves the codes, up to magnitudes that add up to
+    almost 2^128 in a slice and down to scales of 2^-100."""
+    m = cr()
+    x = torch.randn(140, 768, device="cuda", generator=gen(141)).clamp(-4, 4)
+    x *= 2.0 ** 15 / x.abs().reshape(140, 3, 256).sum(-1).max()  # at most 2^15 in all, before one rounding
+    x = (x * 0.99).to(BF)
+    assert x.abs().double().reshape(140, 3, 256).sum(-1).max() < 2.0 ** 15
+    c, s = m.cr_ckpt_save(x)
+    y = (x.double() * 2.0 ** power).to(BF)
+    assert torch.equal(y.double(), x.double() * 2.0 ** power)  # exact
+    c2, s2 = m.cr_ckpt_save(y)
+    assert torch.equal(c, c2) and torch.equal(s2.double(), s.double() * 2.0 ** power)
+    r, r2 = m.cr_ckpt_load(c, s), m.cr_ckpt_load(c2, s2)
+    assert torch.isfinite(r2).all() and torch.equal(r2.double(), r.double() * 2.0 ** power)
