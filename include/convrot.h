@@ -540,6 +540,12 @@ cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const
 cr_status cr_selftest_wait_timeout(void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * cr_selftest_lost_wait -- diagnostic: the same without a workspace; the wait
+ * that ran out is found by cr_read_timeouts.
+ */
+cr_status cr_selftest_lost_wait(void* stream);
+
+/*
  * cr_selftest_act_fallback -- diagnostic: cr_rotate_quant_act_ex on the
  * fallback kernels, the two streaming passes (per-block maxima, then codes)
  * that run when the device refuses the one-launch activation pass's
@@ -558,6 +564,16 @@ cr_status cr_selftest_act_fallback(const void* X, int M, int K, int64_t ldx, int
  * Synchronises `stream`.  Clearing the word is the caller's job (write zero).
  */
 cr_status cr_read_device_status(const void* workspace, int* status, void* stream);
+
+/*
+ * cr_read_timeouts -- for callers that do not keep the workspaces of
+ * cr_lora_forward, cr_lora_backward and cr_w4a4_grad_input, and for cr_ckpt_save
+ * and cr_ckpt_load, which have none: *status is CR_ERR_TIMEOUT if a device-side
+ * wait of these calls' kernels ran out on the current device since this was last
+ * asked, up to here on `stream`, else CR_OK.  Results of calls in between may
+ * then be incomplete.  Synchronises `stream`; asking clears it.
+ */
+cr_status cr_read_timeouts(int* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -200,3 +200,11 @@ def test_the_extension_module_is_rebuilt_for_another_torch(monkeypatch):
     assert torch.__version__.split("+")[0] in made
     monkeypatch.setattr(build, "_calls_made_with", lambda: made.replace(torch.__version__.split("+")[0], "0.0"))
     assert build._calls_stale()
+
+
+def test_timeouts_need_a_place_for_the_answer():
+    assert b._lib.cr_read_timeouts(None, None) == 1
+    if not torch.cuda.is_available():
+        st = ctypes.c_int(-1)
+        assert b._lib.cr_read_timeouts(ctypes.byref(st), None) in (4, 6) and st.value == -1
+        assert b._lib.cr_selftest_lost_wait(None) in (4, 6)

@@ -67,6 +67,8 @@ _SIGS = {
     "cr_a8w4_gemm_s32": (_i, [_vp, _vp, _vp, _i64, _i, _i, _i, _vp, _sz, _vp]),
     "cr_a8w4_linear": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _sz, _vp]),
     "cr_selftest_wait_timeout": (_i, [_vp, _sz, _vp]),
+    "cr_selftest_lost_wait": (_i, [_vp]),
+    "cr_read_timeouts": (_i, [ctypes.POINTER(_i), _vp]),
     "cr_selftest_act_fallback": (_i, [_vp, _i, _i, _i64, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "cr_w4a4_gemm_multi": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "cr_w4a4_gemm_multi_s32": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -305,13 +307,19 @@ def cr_w4a4_linear(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, bia
 
 def cr_read_device_status(device: Optional[torch.device] = None, ws: Optional[torch.Tensor] = None) -> int:
     """Device status word of this device's shared workspace, or of the workspace ``ws`` that a call was
-    given (synchronises the current stream)."""
+    given (synchronises the current stream).  Without ``ws`` a device-side wait that ran out in an adapter,
+    checkpoint or input-gradient call on this device since the last time counts, too: those calls' own scratch,
+    and its status word with it, is gone by then."""
+    st = ctypes.c_int(0)
     if ws is not None:
         device = ws.device
     else:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        with torch.cuda.device(device):
+            _check("cr_read_timeouts", _lib.cr_read_timeouts(ctypes.byref(st), _stream(device)))
+        if st.value != CR_OK:
+            return st.value
         ws = workspace(device, 256)
-    st = ctypes.c_int(0)
     _check("cr_read_device_status", _lib.cr_read_device_status(_ptr(ws), ctypes.byref(st), _stream(device)))
     return st.value
 
@@ -673,7 +681,8 @@ def cr_selftest_wait_timeout(ws: torch.Tensor) -> None:
 # in the extension module (csrc/py_calls.cpp).  Scratch is a buffer of its own for each call, taken from
 # torch's allocator on the current stream (inside a graph capture: from the graph's pool), so calls on several
 # streams and captured graphs share nothing.  A caller's ``workspace`` takes its place; its status word can
-# then be read with ``cr_read_device_status(ws=...)``.
+# then be read with ``cr_read_device_status(ws=...)``.  A wait that ran out in a call with scratch of its own is found
+# by ``cr_read_device_status()``.
 # ---------------------------------------------------------------------------
 
 

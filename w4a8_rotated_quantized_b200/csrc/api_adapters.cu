@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/convrot.h"
 #include "cr_internal.h"
@@ -273,6 +274,20 @@ cr_status cr_w4a4_grad_input(const void* dY, int64_t lddy, const void* Wq, const
                                            ws_status(workspace), s);
   if (e != cudaSuccess) return CR_ERR_CUDA;
   return static_cast<cr_status>(cr::launch_gemm_bf16(dY, lddy, w, dX, lddx, M, N, K, ws_status(workspace), nsm, s));
+}
+
+cr_status cr_read_timeouts(int* status, void* stream) {
+  if (!status) return CR_ERR_INVALID_ARG;
+  int nsm = 0;
+  const cr_status st = static_cast<cr_status>(cr::check_current_device(&nsm));
+  if (st != CR_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool found = false;
+  for (auto ask : {cr::lora_lost_wait, cr::ckpt_lost_wait, cr::gemm_bf16_lost_wait, cr::grad_input_few_lost_wait,
+                   cr::selftest_lost_wait})
+    if (ask(s, &found) != cudaSuccess) return CR_ERR_CUDA;
+  *status = found ? CR_ERR_TIMEOUT : CR_OK;
+  return CR_OK;
 }
 
 }  // extern "C"

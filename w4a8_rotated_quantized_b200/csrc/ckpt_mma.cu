@@ -32,6 +32,7 @@
 #include "cr_internal.h"
 #include "grid_sync.cuh"
 #include "lora_device.cuh"
+#include "lost_wait.cuh"
 
 namespace cr {
 namespace {
@@ -122,6 +123,7 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
 // A wait that ran out: no status word here, so the values say it (NaN scales, NaN rows); copies on their way
 // land before the block ends.
 __device__ __forceinline__ void gave_up(volatile int* abort) {
+  record_timeout(nullptr);
   *abort = 1;
   const uint64_t t0 = globaltimer_ns();
   while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
@@ -478,5 +480,7 @@ int launch_ckpt_load(const int8_t* codes, const float* scales, int M, int K, uin
   Launch l(blocks(M, K, num_sms), kLoadSmem, stream);
   return cudaLaunchKernelEx(&l.cfg, ckpt_load_kernel, tc, tx, scales, M, K / TC) == cudaSuccess ? CR_OK : CR_ERR_CUDA;
 }
+
+cudaError_t ckpt_lost_wait(cudaStream_t stream, bool* found) { return take_lost_wait(stream, found); }
 
 }  // namespace cr

@@ -208,6 +208,14 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
                           float* P, uint16_t* dX, int64_t lddx, int M, int N, int K, int group, int splits, int* status,
                           cudaStream_t stream);
 
+// Whether a wait of a file's kernels ran out on the current device since this was last asked (lost_wait.cuh): sets
+// *found, never clears it.  Synchronises the stream.
+cudaError_t lora_lost_wait(cudaStream_t stream, bool* found);
+cudaError_t ckpt_lost_wait(cudaStream_t stream, bool* found);
+cudaError_t gemm_bf16_lost_wait(cudaStream_t stream, bool* found);
+cudaError_t grad_input_few_lost_wait(cudaStream_t stream, bool* found);
+cudaError_t selftest_lost_wait(cudaStream_t stream, bool* found);
+
 // Supported device = compute capability 10.0 (api.cu): CR_OK and its SM count, or the status to return.
 int check_current_device(int* num_sms);
 

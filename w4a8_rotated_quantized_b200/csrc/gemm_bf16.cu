@@ -29,6 +29,7 @@
 #include "cr_device.cuh"
 #include "cr_internal.h"
 #include "lora_device.cuh"
+#include "lost_wait.cuh"
 
 namespace cr {
 namespace {
@@ -75,7 +76,7 @@ struct Smem {
 };
 
 __device__ __forceinline__ void fail(const Smem& sm, int* status) {
-  record_status(status, CR_ERR_TIMEOUT);
+  record_timeout(status);
   *sm.abort_flag() = 1;
 }
 
@@ -304,5 +305,7 @@ int launch_gemm_bf16(const void* A, int64_t lda, const void* W, void* Y, int64_t
   return cudaLaunchKernelEx(&cfg, gemm_bf16_pair_kernel, ta, tw, ty, M, N, K, status) == cudaSuccess ? CR_OK
                                                                                                      : CR_ERR_CUDA;
 }
+
+cudaError_t gemm_bf16_lost_wait(cudaStream_t stream, bool* found) { return take_lost_wait(stream, found); }
 
 }  // namespace cr

@@ -29,6 +29,7 @@
 #include "cr_internal.h"
 #include "grid_sync.cuh"
 #include "lora_device.cuh"
+#include "lost_wait.cuh"
 
 namespace cr {
 namespace {
@@ -83,7 +84,7 @@ __device__ __forceinline__ uint4 nibbles_to_bf16(uint32_t w) {
 
 // A producer whose wait ran out: copies on their way land before the block ends.
 __device__ __forceinline__ void give_up(volatile int* abort, int* status) {
-  record_status(status, CR_ERR_TIMEOUT);
+  record_timeout(status);
   *abort = 1;
   const uint64_t t = globaltimer_ns();
   while (globaltimer_ns() - t < 1000000ull) __nanosleep(1000);
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) umma_commit(acc_full);
       if (!ok) {
-        record_status(status, CR_ERR_TIMEOUT);
+        record_timeout(status);
         *abort = 1;
         volatile int never = 0;
         if (i > 0) mbar_sleep(last_bar, last_ph, &never);
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (m0 + j + e < M) out[static_cast<int64_t>(j + e) * K] = __uint_as_float(r[e]);
       }
     } else {
-      record_status(status, CR_ERR_TIMEOUT);
+      record_timeout(status);
       *abort = 1;
     }
   }
@@ -389,5 +390,7 @@ int launch_grad_input_few(const uint16_t* dY, int64_t lddy, const uint8_t* Wq, c
   return cudaLaunchKernelEx(&cfg, fin, sums, splits, stride, dX, lddx, units, K / 256) == cudaSuccess ? CR_OK
                                                                                                       : CR_ERR_CUDA;
 }
+
+cudaError_t grad_input_few_lost_wait(cudaStream_t stream, bool* found) { return take_lost_wait(stream, found); }
 
 }  // namespace cr

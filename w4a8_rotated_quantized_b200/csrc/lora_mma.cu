@@ -32,6 +32,7 @@
 #include "cr_internal.h"
 #include "grid_sync.cuh"
 #include "lora_device.cuh"
+#include "lost_wait.cuh"
 
 namespace cr {
 namespace {
@@ -53,7 +54,7 @@ __device__ __forceinline__ uint8_t* align_smem(uint8_t* p) {
 }
 
 __device__ __forceinline__ void fail(volatile int* abort, int* status) {
-  record_status(status, CR_ERR_TIMEOUT);
+  record_timeout(status);
   *abort = 1;
 }
 
@@ -1275,5 +1276,7 @@ int launch_lora_grad_mma(const void* X, int64_t ldx, const float* code_scale, co
              ? CR_OK
              : CR_ERR_CUDA;
 }
+
+cudaError_t lora_lost_wait(cudaStream_t stream, bool* found) { return take_lost_wait(stream, found); }
 
 }  // namespace cr
