@@ -208,3 +208,13 @@ def test_timeouts_need_a_place_for_the_answer():
         st = ctypes.c_int(-1)
         assert b._lib.cr_read_timeouts(ctypes.byref(st), None) in (4, 6) and st.value == -1
         assert b._lib.cr_selftest_lost_wait(None) in (4, 6)
+
+
+def test_backward_splits_up_to_the_most_rows():
+    """The number of token tiles does not leave 32 bits for the last values of M."""
+    size = b._lib.cr_lora_backward_workspace_size
+    for N, K, r, L in ((8, 8, 4, 1), (264, 512, 8, 2)):
+        most = size(2 ** 31 - 1, N, K, r, L)
+        assert most >= size(2 ** 31 - 64, N, K, r, L) > 2 ** 31 * r * 4
+        # the partial sums of 2^25 tiles, 512 to a part
+        assert most >= 2 ** 31 * r * 4 - 4 * r + 2 ** 16 * L * r * (K + N) * 4

@@ -765,7 +765,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tmap_z, const float
   const int c0 = (block % colblocks) * GC;
   const int a = block / colblocks % L;
   const int split = block / colblocks / L;
-  const int tiles = (M + GM - 1) / GM;
+  const int tiles = static_cast<int>((static_cast<int64_t>(M) + GM - 1) / GM);
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
   const int nt = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits) - t0;
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(base + p.off_mask);
@@ -1212,7 +1212,7 @@ int launch_lora_y_mma(const float* V, const int32_t* adapter, const uint16_t* up
 // memory and back (about 0.8 MB a unit).  Up's splits follow from down's so that both kinds of CTA take as long.
 void lora_grad_splits(int M, int K, int N, int rank, int L, bool codes, int num_sms, int* down, int* up) {
   const int64_t cd = static_cast<int64_t>((K + GC - 1) / GC) * L, cu = static_cast<int64_t>((N + GC - 1) / GC) * L;
-  const int tiles = (M + GM - 1) / GM;
+  const int tiles = static_cast<int>((static_cast<int64_t>(M) + GM - 1) / GM);
   const int least = tiles > kMaxGradTiles ? (tiles + kMaxGradTiles - 1) / kMaxGradTiles : 1;
   int64_t best = INT64_MAX;
   *down = *up = least;
