@@ -1105,15 +1105,33 @@ def run_ours(args):
         "gpu_launches_source": "kernel nodes of the captured per-step graph x timed steps"
         if launches_per_step is not None else "unavailable (graph introspection failed)",
         "clocks": clk,
-        "rows": rows,
+        "rows": short_rows(rows) if rows else rows,
     }
     if rank == 0:
+        if rows:  # every figure of them
+            print(json.dumps({"rows": rows}), file=sys.stderr, flush=True)
         print(json.dumps(line), flush=True)
     if world > 1:
         import torch.distributed as dist
 
         dist.destroy_process_group()
     return 0
+
+
+def short_rows(rows):
+    """What the line keeps of each row; a reader that takes only the end of a long output gets it whole."""
+    def figure(v):
+        return float(f"{v:.6g}") if isinstance(v, float) else v
+
+    short = {}
+    for name, r in rows.items():
+        short[name] = {k: figure(r[k]) for k in ("dtype", "value", "unit", "ms_per_step") if k in r}
+        roof = r.get("roofline")
+        if isinstance(roof, dict):
+            short[name].update({k: figure(roof[k]) for k in ("bound", "frac") if k in roof})
+        if isinstance(r.get("kernels_us"), dict):
+            short[name]["kernels_us"] = {k: figure(v) for k, v in r["kernels_us"].items()}
+    return short
 
 
 def main(argv=None):

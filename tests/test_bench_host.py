@@ -108,3 +108,15 @@ def test_reference_arm_prints_one_json_line(capsys, monkeypatch):
     assert line["impl"] == "reference" and line["value"] > 0 and line["cpu_baseline"]["kind"] == "oracle"
     cpu = line["cpu_baseline"]
     assert cpu["cores"] >= 1 and cpu["nproc"] >= 1 and cpu["cpu_model"]
+
+
+def test_rows_of_the_line_are_short():
+    """The line stays short enough to be read whole from the end of an output; all figures go to stderr."""
+    row = {"workload": "w" * 200, "M": 1, "dtype": "s4", "value": 1234.56789012345, "unit": "TOP/s", "ms_per_step": 0.0123456789,
+           "kernels_us": {"act": 1.23456789, "gemm": 2.0}, "gpu_launches_per_step": 2, "cpu_baseline": {"sample": "s" * 500},
+           "roofline": {"bound": "tensor", "frac": 0.7123456789, "kernel": "k" * 200, "traffic": None}}
+    short = bench.short_rows({f"row{i}": row for i in range(12)})
+    assert len(json.dumps(short)) < 3000
+    assert short["row0"] == {"dtype": "s4", "value": 1234.57, "unit": "TOP/s", "ms_per_step": 0.0123457, "bound": "tensor",
+                             "frac": 0.712346, "kernels_us": {"act": 1.23457, "gemm": 2.0}}
+    assert bench.short_rows({"odd": {"value": 1}}) == {"odd": {"value": 1}}
