@@ -104,8 +104,17 @@ __global__ void __launch_bounds__(256)
   float v[8] = {};
   if (m < M) {
     widen8(ldcg_here_u4(dY + m * lddy + n), v);
+    float s[8];
+    if ((reinterpret_cast<uintptr_t>(w_scale) & 15) == 0) {  // (one sector for each thread instead of eight loads)
+      const float4 s0 = ldcg_here_f4(w_scale + n), s1 = ldcg_here_f4(w_scale + n + 4);
+      s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
+      s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= ldcg_here_f1(w_scale + n + e);
+      for (int e = 0; e < 8; ++e) s[e] = ldcg_here_f1(w_scale + n + e);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= s[e];
   }
   *reinterpret_cast<uint4*>(V + static_cast<int64_t>(m) * N + n) = narrow8(v);
 }

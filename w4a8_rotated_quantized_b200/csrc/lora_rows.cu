@@ -62,7 +62,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int c = static_cast<int>(cluster_ctarank());
   const int64_t m = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int a = row_adapter(adapter, m, L);  // the same in the whole cluster
+  // The adapter, the same in the whole cluster.  One thread asks for it: past L1 each warp's load is a request of its
+  // own, and those of all CTAs meet in the same few bytes of L2 (calls in a chain, each warp | one thread: 64 rows 8.2 |
+  // 7.8 us; one row, where the barrier is all that counts, 4.0 | 4.2).
+  __shared__ int own;
+  if (tid == 0) own = row_adapter(adapter, m, L);
+  __syncthreads();
+  const int a = own;
   // this CTA's columns of Y in pieces of eight, and their ranks in groups where there are threads to spare
   const int per_n = (N / 8 + ctas - 1) / ctas;
   const int p0 = c * per_n;
@@ -80,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   cluster_arrive();
-  const float sc = ldcg_here_f1(scale + a);
+  const float sc = tid < rank ? ldcg_here_f1(scale + a) : 0.f;
   const uint16_t* u = up + static_cast<int64_t>(a) * rank * N + 8 * p0;
   uint4 ahead[kAhead], b = make_uint4(0, 0, 0, 0);
 #pragma unroll
