@@ -926,3 +926,16 @@ def test_checkpoint_over_its_range(power):
     assert torch.equal(c, c2) and torch.equal(s2.double(), s.double() * 2.0 ** power)
     r, r2 = m.cr_ckpt_load(c, s), m.cr_ckpt_load(c2, s2)
     assert torch.isfinite(r2).all() and torch.equal(r2.double(), r.double() * 2.0 ** power)
+
+
+@pytest.mark.parametrize("M,N", [(3, 2640), (600, 264)])
+def test_weight_scales_at_odd_places(M, N):
+    """Weight scales that start at any float: straight from the packed weights and by way of the unpacked ones."""
+    m = cr()
+    Wq, s = m.cr_pack_weight(randn(gen(151), N, 512, std=0.02), scale_mode="row")
+    dY = randn(gen(152), M, N, std=1e-3)
+    want = m.cr_w4a4_grad_input(dY, Wq, s)
+    for off in (1, 2, 3):
+        odd = torch.full((N + off + 1,), float("nan"), device="cuda")
+        odd[off:off + N] = s
+        assert torch.equal(m.cr_w4a4_grad_input(dY, Wq, odd[off:off + N]), want)
