@@ -425,8 +425,9 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  *   X        bf16 [M, K], row stride ldx >= K
  *   base     bf16 [M, N], row stride ldb >= N (the projection's output), or
  *            NULL for zero.  base may be Y itself (same pointer and stride);
- *            any other overlap is an error of the caller (refused where the
- *            pointers are equal).
+ *            any other overlap of an output with another operand is an error of
+ *            the caller (refused where Y starts at X or V; so below, where dX
+ *            starts at dY or X).
  *   Y        out: bf16 [M, N], row stride ldy >= N.  Rows without adapter: base.
  *   V        out: bf16 [M, rank], dense: V rounded once, for the backward pass;
  *            NULL if not wanted.  (Y is computed from the float32 V.)
@@ -469,9 +470,10 @@ cr_status cr_w4a4_linear_noalloc(const void* X, int64_t ldx, const void* Wq, con
  * time: calls on different streams, and graphs that may run at the same time,
  * need one each.
  *
- * These calls and the three below start on the device beside the end of the
- * stream's work before them, and wait there for its results: the order of the
- * stream holds as for any other call.
+ * These calls and the three below (cr_w4a4_grad_input where it works straight
+ * from the packed weights) start on the device beside the end of the stream's work
+ * before them, and wait there for its results: the order of the stream holds as
+ * for any other call, for indices and scales, too.
  */
 #define CR_MAX_RANK 128
 #define CR_MAX_ADAPTERS 4096

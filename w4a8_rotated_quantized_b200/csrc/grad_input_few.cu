@@ -15,8 +15,10 @@
 //   rotates and rounds once.  (Joined by a cluster through distributed shared memory instead, without the third
 //   kernel, 130 tokens of 9728 x 2560 took 31 us instead of 24: few clusters fit, and the sums' way is no shorter.)
 //
-// What bounds it: the codes' way through the ALUs (13 instructions for 8), with few tiles a CTA setting up, and the
-// parts' way to the third kernel: of 24 us for 130 tokens of 9728 x 2560 the packed weights' 12.5 MB are two.
+// What bounds it: not the packed weights' bytes (of 24 us for 130 tokens of 9728 x 2560 their 12.5 MB are two) and not
+// the codes' way through the ALUs (13 instructions for 8: 1.3 million of a warp's, 1.4 us over 114 SMs), but waiting.
+// Token blocks of more than 128 rows leave room for two tiles of codes, 16 KB, on their way to an SM, one for each set
+// of warps; with few tiles a CTA, setting up and the parts' way to the third kernel come on top.
 
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -108,10 +108,11 @@ __device__ __forceinline__ int tile_adapters(const int32_t* __restrict__ adapter
 // ---------------------------------------------------------------------------------------------------
 // v: 128 tokens x (up to 256 / rank adapters side by side); the sum over k split over a cluster's CTAs,
 // whose partial sums go to the CTA that adds up their row, in rank order, through distributed shared memory.
-// By itself it takes 13.5 us for 4096 x 3072 at rank 64 and 16 us for 8192 x 3072 at rank 32 (1.9 and 3.2 TB/s):
-// X comes in about 5 and 9 of them, the rest is starting and the exchange, which is why the kernels before and
-// after it run into it.  (As one kernel with y, V passed round a cluster, the two took 28.4 us instead of 26.6 for
-// 4096 tokens and 20.5 instead of 15.5 for 130.)
+// By itself it takes 12 to 13 us for 4096 x 3072 at rank 64 and 15 to 16 us for 8192 x 3072 at rank 32 (2.0 and 3.3
+// TB/s): X comes in about 5 and 9 of them, the rest is starting and the exchange.  Of the kernels after it little runs
+// beside it: with rings that fill an SM's shared memory, here and in y, a CTA of y starts where one of v has ended or
+// none ran.  (As one kernel with y, V passed round a cluster, the two took 28.4 us where the two kernels of that time
+// took 26.6 for 4096 tokens, and 20.5 against 15.5 for 130.)
 // ---------------------------------------------------------------------------------------------------
 
 struct VPlan {

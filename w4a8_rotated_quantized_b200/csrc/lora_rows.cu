@@ -12,8 +12,8 @@
 // four loads on their way whatever the rank (its tasks are pairs of a rank and 256 columns, not ranks), the
 // ranks of a column are shared out between the threads that columns leave idle, their first U and the base are
 // on their way before the first product, and the only other wait is one barrier of the cluster.  One token of
-// rank 16, 2560 -> 9728, takes 4.1 us, 64 tokens of 48 adapters 7.1 (21.7 MB: 3.1 TB/s; two dependent rounds of
-// loads and the cluster's exchange, not bandwidth).  Asking L2 for the rest of U before the first product took
+// rank 16, 2560 -> 9728, takes 4.2 us, 64 tokens of 48 adapters, of which they name 33, 7.1 a call (16 MB: 2.3 TB/s;
+// the index, two dependent rounds of loads and the cluster's exchange, not bandwidth).  Asking L2 for the rest of U before the first product took
 // longer.
 
 #include <cuda_bf16.h>
@@ -36,8 +36,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 1;     // ranks of U that a thread has on their way from the start
 constexpr int kTasks = 4;     // loads of A that a warp has on their way
 // More of either, or of U in the second product, does not fit 64 registers a thread, two CTAs an SM, and costs more
-// in spills than it hides: 64 rows of 48 adapters take 7.1 us so, 8.7 with two ranks ahead, 8.5 with eight tasks, 10.1
-// with four and eight; one row 4.1 and 5.1.
+// in spills than it hides: 64 rows of 48 adapters take 7.5 us a call so, 8.5 with two ranks ahead, 8.4 with eight
+// tasks, 10.9 with four and eight; one row 4.0 on the device, with eight tasks 4.7 (all before the index was asked for
+// once a CTA).
 constexpr int kMostPasses = CR_MAX_K / 256 / 4;  // 256 columns at a time: of a CTA in a cluster of 4 (2: half the K)
 
 __device__ __forceinline__ void st_shared_cluster_f1(uint32_t cluster_addr, float v) {
@@ -209,6 +210,8 @@ std::atomic<bool> g_attr_done[64];
 //   960 rows, rank 16, 1488 -> 1272, 43 adapters:   rows 33, batch 13
 //   336 rows, rank 4, 584 -> 416, 7 adapters:       rows 10, batch 9
 //   34 rows, rank 64, 4112 -> 5400, one adapter:    rows 14, batch 9 (the worst choice)
+// The workspace's size goes by the same rule and its call knows of no indices, so a pool of several counts as that also
+// for calls without indices, whose rows all use the first adapter.
 bool use_lora_rows(int M, int N, int K, int rank, int L) {
   if (M > 1024) return false;
   const double columns = static_cast<double>(K) + N, factors = 2.0 * rank * columns;
