@@ -110,6 +110,16 @@ def test_reference_arm_prints_one_json_line(capsys, monkeypatch):
     assert cpu["cores"] >= 1 and cpu["nproc"] >= 1 and cpu["cpu_model"]
 
 
+def test_traffic_figures_are_of_the_present_kernels():
+    """The figures that the bench reports beside these kernels' times were captured on the sources as they are."""
+    for prof, sources in [(bench.GEMM_PROFILE, bench.GEMM_SOURCES)] + [bench.ROW_PROFILES[n] for n in (
+            "int8_convrot", "w4a8_asym_g16", "int8_branch_w4")]:
+        assert bench.profile_traffic(prof, sources) > 0, f"{prof}: capture it anew, the kernel has changed"
+    for kern, name in (("small", "text_enc_up_21"), ("pair", "text_enc_up_130")):
+        prof, sources = bench.FEW_TOKEN_PROFILES[kern]
+        assert bench.profile_traffic(prof, sources, workload=name) > 0, f"{prof}: capture it anew, the kernel has changed"
+
+
 def test_rows_of_the_line_are_short():
     """The line stays short enough to be read whole from the end of an output; all figures go to stderr."""
     row = {"workload": "w" * 200, "M": 1, "dtype": "s4", "value": 1234.56789012345, "unit": "TOP/s", "ms_per_step": 0.0123456789,

@@ -31,7 +31,7 @@ SOURCES = ["api.cu", "act_kernels.cu", "gemm_w4a4.cu", "gemm_w4a4_pair.cu", "gem
            "grad_input_few.cu"]
 HEADERS = [os.path.join(ROOT, "include", "convrot.h")] + [
     os.path.join(CSRC, f) for f in ("cr_device.cuh", "cr_internal.h", "act_device.cuh", "grid_sync.cuh", "lora_device.cuh",
-                                    "unit_device.cuh", "lost_wait.cuh")
+                                    "unit_device.cuh", "lost_wait.cuh", "f16_device.cuh")
 ]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=default",

@@ -28,6 +28,7 @@
 
 #include "cr_device.cuh"
 #include "cr_internal.h"
+#include "f16_device.cuh"
 #include "lora_device.cuh"
 #include "lost_wait.cuh"
 

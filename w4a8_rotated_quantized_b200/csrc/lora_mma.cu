@@ -30,6 +30,7 @@
 
 #include "cr_device.cuh"
 #include "cr_internal.h"
+#include "f16_device.cuh"
 #include "grid_sync.cuh"
 #include "lora_device.cuh"
 #include "lost_wait.cuh"
